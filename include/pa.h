@@ -188,6 +188,84 @@ int pa_reshape_and_cache(const void* k, const void* v, void* k_cache, void* v_ca
                          pa_dtype dtype, void* stream);
 
 /*
+ * Rotary positions.  Pair i < rotary_dim / 2 of a head row x of a token at position n
+ * turns by the angle n * inv_freq[i]:
+ *   y_a = magnitude * (x_a cos - x_b sin),  y_b = magnitude * (x_b cos + x_a sin),
+ * with (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved != 0; dims from
+ * rotary_dim on pass unchanged.  Every head uses the same frequencies.  The angle is
+ * exact for every int32 position (it is reduced to a fraction of a turn in integer
+ * arithmetic), so far positions lose nothing to fp32.
+ *
+ * pa_rotary_frequencies: host helper, no CUDA call.  Writes the rotary_dim / 2 angles per
+ * position (radians) to inv_freq (HOST):
+ *   PA_ROPE_NONE      f_i = base^(-2 i / rotary_dim)
+ *   PA_ROPE_LINEAR    f_i / factor (positions squeezed by factor)
+ *   PA_ROPE_NTK       base replaced by base * factor^(rotary_dim / (rotary_dim - 2))
+ *   PA_ROPE_BY_PARTS  g f_i + (1 - g) f_i / factor, where g = clamp((r_i - low_turns) /
+ *                     (high_turns - low_turns), 0, 1) and r_i = original_len * f_i / 2 pi is
+ *                     how often pair i turns over the original context: fast pairs keep
+ *                     their angle, slow ones are squeezed.  A magnitude of
+ *                     0.1 ln(factor) + 1 is the usual companion of this form.
+ * factor >= 1 (ignored by NONE); rotary_dim even, 2 .. 256 (NTK: from 4); base > 1;
+ * BY_PARTS: original_len > 0, 0 <= low_turns < high_turns.  PA_ERR_INVALID otherwise.
+ */
+typedef enum {
+    PA_ROPE_NONE = 0,
+    PA_ROPE_LINEAR = 1,
+    PA_ROPE_NTK = 2,
+    PA_ROPE_BY_PARTS = 3
+} pa_rope_scaling;
+int pa_rotary_frequencies(double* inv_freq, int32_t rotary_dim, double base,
+                          pa_rope_scaling scaling, double factor, double low_turns,
+                          double high_turns, int32_t original_len);
+
+/*
+ * pa_rotary_and_cache: turns q and k by their positions and writes the cache, in one
+ * launch: q_out[i] = rot(q[i]); with slot = slot_mapping[i] >= 0 and each kv head h,
+ * k_cache[slot / B][h][slot % B][:] = rot(k[i][h]) and v_cache[..] = v[i][h] (bit for bit).
+ * A token with a negative slot (padding) gets its q_out row and writes no cache.  Each
+ * result is computed in fp32 and rounded once.
+ *   q, q_out       device, num_tokens rows of [Hq][D]; k, v: rows of [Hkv][D]; `dtype`.
+ *                  *_stride: elements from one token's row to the next, so the three may be
+ *                  views of one projection's output.  Pointers 16-byte aligned, strides a
+ *                  multiple of 16 bytes and at least one row.
+ *   q_out          may be q itself (same pointer and stride: turned in place); otherwise
+ *                  its rows overlap none of q, k, v
+ *   k_cache, v_cache, slot_mapping, num_blocks: as in pa_reshape_and_cache; the caches
+ *                  overlap neither each other nor any row
+ *   positions      device int32 [num_tokens]; every value is valid
+ *   inv_freq       HOST double [rotary_dim / 2], radians per position, |inv_freq| < 2^20;
+ *                  read before the call returns
+ *   rotary_dim     even, 2 .. min(head_dim, 256)
+ *   magnitude      factor on the turned dims of q and k (1 in the usual case)
+ * head_dim * element size must be a multiple of 16 bytes (PA_ERR_UNSUPPORTED).  A slot
+ * >= num_blocks * B is skipped and flags PA_DEVERR_SLOT.
+ */
+int pa_rotary_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                        const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                        pa_dtype dtype, void* k_cache, void* v_cache,
+                        const int64_t* slot_mapping, const int32_t* positions,
+                        int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                        int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                        const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                        float magnitude, void* stream);
+
+/*
+ * pa_rotary_and_cache_fp8: the same into an E4M3 cache: the codes are
+ * e4m3(rot(k)[d] / k_scale[h]) and e4m3(fp32(v) / v_scale[h]), rounded from the fp32
+ * values as in pa_reshape_and_cache_fp8 (rot(k) is not rounded to `dtype` first).
+ * k_scale, v_scale: DEVICE float [Hkv].  head_dim must be a multiple of 16.
+ */
+int pa_rotary_and_cache_fp8(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                            const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            pa_dtype dtype, void* k_cache, void* v_cache, const float* k_scale,
+                            const float* v_scale, const int64_t* slot_mapping,
+                            const int32_t* positions, int64_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                            int64_t num_blocks, const double* inv_freq, int32_t rotary_dim,
+                            int32_t interleaved, float magnitude, void* stream);
+
+/*
  * Block copy for copy-on-write: for every layer l < num_layers and every pair p,
  * the whole block src = pairs[2p] of k_caches[l] and of v_caches[l] is copied to
  * block dst = pairs[2p+1] (block_bytes bytes each; every block of every pool).

@@ -15,11 +15,13 @@ PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3 = 0, 1, 2, 3
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = 0, -1, -2, -3, -4
 PA_DEVERR_BLOCK_ID, PA_DEVERR_CONTEXT_LEN, PA_DEVERR_SLOT, PA_DEVERR_TIMEOUT = 1, 2, 4, 8
 PA_DEVERR_RANGE = 0x10
+PA_ROPE_NONE, PA_ROPE_LINEAR, PA_ROPE_NTK, PA_ROPE_BY_PARTS = 0, 1, 2, 3
 PA_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 # Every symbol include/pa.h and include/pa_block_manager.h declare, with (restype, argtypes).
 _i32, _i64, _sz, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, \
     ctypes.c_float
+_f64 = ctypes.c_double
 SIGNATURES = {
     "pa_decode_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
     "pa_decode": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _vp, ctypes.c_int, _i64, _vp, _i64,
@@ -49,6 +51,15 @@ SIGNATURES = {
                                                 _i64, _i32, _i32, _i32, _i64, _vp]),
     "pa_reshape_and_cache": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64,
                                             ctypes.c_int, _vp]),
+    "pa_rotary_frequencies": (ctypes.c_int, [_vp, _i32, _f64, ctypes.c_int, _f64, _f64, _f64,
+                                             _i32]),
+    "pa_rotary_and_cache": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                           ctypes.c_int, _vp, _vp, _vp, _vp, _i64, _i32, _i32,
+                                           _i32, _i32, _i64, _vp, _i32, _i32, _f32, _vp]),
+    "pa_rotary_and_cache_fp8": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                               ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                               _i32, _i32, _i32, _i32, _i64, _vp, _i32, _i32,
+                                               _f32, _vp]),
     "pa_copy_blocks": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.POINTER(_vp), _i32,
                                       ctypes.POINTER(_i64), _i64, _i64, _i64, _vp]),
     "pa_swap_blocks": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.POINTER(_vp), _i32,

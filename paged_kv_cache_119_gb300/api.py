@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 
+import numpy as np
 import torch
 
 from . import _native as N
@@ -149,6 +150,118 @@ def pa_reshape_and_cache(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor
                                            v_cache.data_ptr(), slot_mapping.data_ptr(), T, Hkv,
                                            D, B, Nb, _dtype(k), _stream(stream))
     N.check("pa_reshape_and_cache", status)
+
+
+_ROPE = {"none": N.PA_ROPE_NONE, "linear": N.PA_ROPE_LINEAR, "ntk": N.PA_ROPE_NTK,
+         "by_parts": N.PA_ROPE_BY_PARTS}
+
+
+def pa_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                          factor: float = 1.0, low_turns: float = 1.0, high_turns: float = 32.0,
+                          original_len: int = 0) -> np.ndarray:
+    """Angles per position (radians, float64 [rotary_dim / 2]) for pa_rotary_and_cache.
+
+    scaling: "none"; "linear" (frequencies / factor); "ntk" (a larger base); "by_parts"
+    (pairs that turn at least high_turns times over original_len keep their frequency, those
+    below low_turns are divided by factor, a ramp between)."""
+    if scaling not in _ROPE:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE)}, got {scaling!r}")
+    out = np.empty(max(int(rotary_dim), 0) // 2, dtype=np.float64)
+    N.check("pa_rotary_frequencies",
+            N.load().pa_rotary_frequencies(out.ctypes.data, int(rotary_dim), float(base),
+                                           _ROPE[scaling], float(factor), float(low_turns),
+                                           float(high_turns), int(original_len)))
+    return out
+
+
+def _rows(name: str, t: torch.Tensor) -> None:
+    """A CUDA tensor [T, H, D] whose token rows [H, D] are dense (the token stride is free)."""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (t.shape[0] and (t.stride(2) != 1 or
+                                        (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
+        raise ValueError(f"{name} must be [T, H, D] with dense rows [H, D]")
+
+
+def _one_device(q: torch.Tensor, *others: torch.Tensor) -> None:
+    """Every tensor on q's device, and that device current: the launch goes there."""
+    if any(t is not None and t.device != q.device for t in others):
+        raise ValueError("all tensors must be on one device")
+    if q.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {q.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _rotary(fn, q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_freq, scales,
+            interleaved, magnitude, stream):
+    for name, t in (("q_out", q_out), ("q", q), ("k", k), ("v", v)):
+        _rows(name, t)
+    for name, t in (("slot_mapping", slot_mapping), ("positions", positions)):
+        _cuda(name, t)
+    if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int32:
+        raise TypeError("slot_mapping must be int64 and positions int32")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if q_out.shape != q.shape or k.shape != (T, Hkv, D) or v.shape != k.shape:
+        raise ValueError("q, q_out must be [T, Hq, D] and k, v [T, Hkv, D]")
+    if slot_mapping.shape != (T,) or positions.shape != (T,):
+        raise ValueError("slot_mapping and positions must be [T]")
+    if not (q.dtype == q_out.dtype == k.dtype == v.dtype):
+        raise TypeError("q, q_out, k and v must share a dtype")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or \
+            (k_cache.shape[1], k_cache.shape[3]) != (Hkv, D):
+        raise ValueError(f"caches must be [N, {Hkv}, B, {D}]")
+    _one_device(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, *scales)
+    freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if freq.ndim != 1:
+        raise ValueError("inv_freq must be a host sequence of rotary_dim / 2 numbers")
+    status = getattr(N.load(), fn)(
+        q_out.data_ptr(), _row_stride(q_out), q.data_ptr(), _row_stride(q), k.data_ptr(),
+        _row_stride(k), v.data_ptr(), _row_stride(v), _dtype(q), k_cache.data_ptr(),
+        v_cache.data_ptr(), *[t.data_ptr() for t in scales], slot_mapping.data_ptr(),
+        positions.data_ptr(), T, Hq, Hkv, D, k_cache.shape[2], k_cache.shape[0],
+        freq.ctypes.data, 2 * freq.size, int(bool(interleaved)), float(magnitude),
+        _stream(stream))
+    N.check(fn, status)
+    return q_out
+
+
+def pa_rotary_and_cache(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                        positions: torch.Tensor, inv_freq, interleaved: bool = False,
+                        magnitude: float = 1.0, stream=None) -> torch.Tensor:
+    """Turn q and k by their positions and write the cache: q_out = rot(q), and rot(k[i]),
+    v[i] into slot slot_mapping[i] (negative: q only).
+
+    q, q_out [T, Hq, D], k, v [T, Hkv, D]: rows [H, D] dense, any token stride (views of one
+    projection); q_out may be q.  positions int32 [T]; inv_freq: rotary_dim / 2 host numbers
+    (pa_rotary_frequencies), radians per position; pairs are (i, i + rotary_dim / 2), or
+    (2i, 2i + 1) when interleaved; magnitude multiplies the turned dims."""
+    _cuda("k_cache", k_cache)
+    _cuda("v_cache", v_cache)
+    if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
+        raise TypeError("k, v and the caches must share a dtype")
+    return _rotary("pa_rotary_and_cache", q_out, q, k, v, k_cache, v_cache, slot_mapping,
+                   positions, inv_freq, (), interleaved, magnitude, stream)
+
+
+def pa_rotary_and_cache_fp8(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                            v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                            slot_mapping: torch.Tensor, positions: torch.Tensor, inv_freq,
+                            k_scale: torch.Tensor, v_scale: torch.Tensor,
+                            interleaved: bool = False, magnitude: float = 1.0,
+                            stream=None) -> torch.Tensor:
+    """pa_rotary_and_cache into E4M3 caches: codes e4m3(rot(k) / k_scale[h]) and
+    e4m3(v / v_scale[h]), rounded from fp32; scales float32 [Hkv]."""
+    _fp8_cache("k_cache", k_cache)
+    _fp8_cache("v_cache", v_cache)
+    _scales(k_scale, v_scale, k.shape[1])
+    return _rotary("pa_rotary_and_cache_fp8", q_out, q, k, v, k_cache, v_cache, slot_mapping,
+                   positions, inv_freq, (k_scale, v_scale), interleaved, magnitude, stream)
 
 
 def pa_copy_blocks(k_caches, v_caches, src_dst_pairs, stream=None) -> None:

@@ -921,6 +921,189 @@ int pa_reshape_and_cache(const void* k, const void* v, void* k_cache, void* v_ca
                : PA_ERR_CUDA;
 }
 
+int pa_rotary_frequencies(double* inv_freq, int32_t rotary_dim, double base,
+                          pa_rope_scaling scaling, double factor, double low_turns,
+                          double high_turns, int32_t original_len)
+{
+    if (!inv_freq || rotary_dim < 2 || rotary_dim > 2 * kRotMaxPairs || rotary_dim % 2 != 0 ||
+        !(base > 1.0) || !std::isfinite(base))
+        return PA_ERR_INVALID;
+    if (scaling != PA_ROPE_NONE && scaling != PA_ROPE_LINEAR && scaling != PA_ROPE_NTK &&
+        scaling != PA_ROPE_BY_PARTS)
+        return PA_ERR_INVALID;
+    if (scaling != PA_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
+        return PA_ERR_INVALID;
+    if (scaling == PA_ROPE_NTK && rotary_dim < 4)
+        return PA_ERR_INVALID;
+    if (scaling == PA_ROPE_BY_PARTS &&
+        (original_len <= 0 || !(low_turns >= 0.0) || !(high_turns > low_turns) ||
+         !std::isfinite(high_turns)))
+        return PA_ERR_INVALID;
+    if (scaling == PA_ROPE_NTK)
+        base *= std::pow(factor, (double)rotary_dim / (rotary_dim - 2));
+    const double turn = 6.283185307179586;       // 2 pi
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rotary_dim);
+        if (scaling == PA_ROPE_LINEAR) {
+            f /= factor;
+        } else if (scaling == PA_ROPE_BY_PARTS) {
+            const double r = original_len * f / turn;
+            const double g = std::min(1.0, std::max(0.0, (r - low_turns) / (high_turns - low_turns)));
+            f = g * f + (1.0 - g) * f / factor;
+        }
+        inv_freq[i] = f;
+    }
+    return PA_OK;
+}
+
+// Radians per position -> turns per position as a 0.64 fixed-point fraction.  1 / 2 pi is
+// taken as hi + lo and the product as t + e (fma), so the fraction is good to about 2^-63.
+static uint64_t turn_fraction(double f)
+{
+    const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+    const double t = f * hi;
+    const double e = std::fma(f, hi, -t) + f * lo;
+    const double part = std::ldexp(t - std::floor(t), 64);      // exact, in [0, 2^64]
+    const double whole = std::floor(part);
+    const uint64_t w = whole >= 0x1p64 ? 0u : (uint64_t)whole;
+    return w + (uint64_t)std::llrint((part - whole) + std::ldexp(e, 64));
+}
+
+// Whether two sets of `rows` rows (wa / wb bytes each, sa / sb bytes apart) share a byte:
+// exact where the row strides are equal (views of one projection), by their whole ranges
+// otherwise.
+static bool rows_overlap(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb,
+                         int64_t wb, int64_t rows)
+{
+    if (!overlaps(a, (size_t)((rows - 1) * sa + wa), b, (size_t)((rows - 1) * sb + wb)))
+        return false;
+    if (sa != sb || rows == 1)
+        return true;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    // row i of a and row j of b meet when y - x + (j - i) sa lies in (-wb, wa); the
+    // residue m of y - x modulo sa is the only offset in [0, sa), m - sa the one below
+    const int64_t m = (int64_t)(y >= x ? (y - x) % (uintptr_t)sa
+                                       : ((uintptr_t)sa - (x - y) % (uintptr_t)sa) % (uintptr_t)sa);
+    return m < wa || m + wb > sa;
+}
+
+static int rotary_impl(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                       const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                       pa_dtype dtype, void* k_cache, void* v_cache, bool fp8,
+                       const float* k_scale, const float* v_scale, const int64_t* slot_mapping,
+                       const int32_t* positions, int64_t num_tokens, int32_t num_q_heads,
+                       int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                       int64_t num_blocks, const double* inv_freq, int32_t rotary_dim,
+                       int32_t interleaved, float magnitude, void* stream)
+{
+    if (!valid_dtype(dtype) || num_tokens < 0 || num_tokens > INT32_MAX || num_q_heads <= 0 ||
+        num_kv_heads <= 0 || head_dim <= 0 || head_dim > 65536 || block_size <= 0 ||
+        num_blocks <= 0 || num_blocks > INT32_MAX || !std::isfinite(magnitude))
+        return PA_ERR_INVALID;
+    if (rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > head_dim ||
+        rotary_dim > 2 * kRotMaxPairs || !inv_freq)
+        return PA_ERR_INVALID;
+    const int64_t esz = (int64_t)elem_size(dtype);
+    if (head_dim * esz % 16 != 0 || (fp8 && head_dim % 16 != 0))
+        return PA_ERR_UNSUPPORTED;
+    for (int i = 0; i < rotary_dim / 2; ++i)
+        if (!(std::fabs(inv_freq[i]) < 1048576.0))
+            return PA_ERR_INVALID;
+    // the items of a token are counted in 32 bits
+    if (((int64_t)num_q_heads + 2 * (int64_t)num_kv_heads) * head_dim > INT32_MAX / 2)
+        return PA_ERR_INVALID;
+    if (num_tokens == 0)
+        return PA_OK;
+    if (!q_out || !q || !k || !v || !k_cache || !v_cache || !slot_mapping || !positions ||
+        (fp8 && (!k_scale || !v_scale)))
+        return PA_ERR_INVALID;
+    const int64_t q_row = (int64_t)num_q_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+    const int64_t strides[4] = {q_out_stride, q_stride, k_stride, v_stride};
+    const int64_t widths[4] = {q_row, q_row, kv_row, kv_row};
+    const void* rows[4] = {q_out, q, k, v};
+    for (int i = 0; i < 4; ++i)
+        if (strides[i] < widths[i] || strides[i] > (int64_t(1) << 40) ||
+            strides[i] * esz % 16 != 0 || !aligned16(rows[i]))
+            return PA_ERR_INVALID;
+    if (!aligned16(k_cache) || !aligned16(v_cache))
+        return PA_ERR_INVALID;
+    const size_t pool_bytes = (size_t)num_blocks * num_kv_heads * block_size * head_dim *
+                              (fp8 ? 1 : (size_t)esz);
+    if (overlaps(k_cache, pool_bytes, v_cache, pool_bytes))
+        return PA_ERR_INVALID;
+    for (int i = 0; i < 4; ++i) {
+        const size_t span = (size_t)((num_tokens - 1) * strides[i] + widths[i]) * esz;
+        if (overlaps(rows[i], span, k_cache, pool_bytes) || overlaps(rows[i], span, v_cache, pool_bytes))
+            return PA_ERR_INVALID;
+        if (i > 0 && !(i == 1 && q_out == q && q_out_stride == q_stride) &&
+            rows_overlap(q_out, q_out_stride * esz, q_row * esz, rows[i], strides[i] * esz,
+                         widths[i] * esz, num_tokens))
+            return PA_ERR_INVALID;
+    }
+    RotaryParams p{};
+    p.q_out = q_out;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = fp8 ? k_scale : nullptr;
+    p.v_scale = fp8 ? v_scale : nullptr;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.err = device_error_word();
+    if (!p.err)
+        return PA_ERR_CUDA;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out_stride = q_out_stride;
+    p.num_tokens = num_tokens;
+    p.num_blocks = num_blocks;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.half = rotary_dim / 2;
+    p.block_size = block_size;
+    p.magnitude = magnitude;
+    for (int i = 0; i < rotary_dim / 2; ++i)
+        p.phase[i] = turn_fraction(inv_freq[i]);
+    return launch_rotary(p, dtype, fp8, interleaved != 0, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+int pa_rotary_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                        const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                        pa_dtype dtype, void* k_cache, void* v_cache,
+                        const int64_t* slot_mapping, const int32_t* positions,
+                        int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                        int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                        const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                        float magnitude, void* stream)
+{
+    return rotary_impl(q_out, q_out_stride, q, q_stride, k, k_stride, v, v_stride, dtype, k_cache,
+                       v_cache, false, nullptr, nullptr, slot_mapping, positions, num_tokens,
+                       num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, inv_freq,
+                       rotary_dim, interleaved, magnitude, stream);
+}
+
+int pa_rotary_and_cache_fp8(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                            const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            pa_dtype dtype, void* k_cache, void* v_cache, const float* k_scale,
+                            const float* v_scale, const int64_t* slot_mapping,
+                            const int32_t* positions, int64_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                            int64_t num_blocks, const double* inv_freq, int32_t rotary_dim,
+                            int32_t interleaved, float magnitude, void* stream)
+{
+    return rotary_impl(q_out, q_out_stride, q, q_stride, k, k_stride, v, v_stride, dtype, k_cache,
+                       v_cache, true, k_scale, v_scale, slot_mapping, positions, num_tokens,
+                       num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, inv_freq,
+                       rotary_dim, interleaved, magnitude, stream);
+}
+
 int pa_copy_blocks(void* const* k_caches, void* const* v_caches, int32_t num_layers,
                    const int64_t* src_dst_pairs_host, int64_t num_pairs, int64_t block_bytes,
                    int64_t num_blocks, void* stream)

@@ -159,6 +159,35 @@ struct ReshapeFp8Params {
 cudaError_t launch_reshape_and_cache_fp8(const ReshapeFp8Params& p, pa_dtype src_dtype,
                                          cudaStream_t stream);
 
+// Rotary positions fused with the cache write (rotary.cu).  Strides are elements between
+// tokens; heads of a row are contiguous.
+constexpr int kRotMaxPairs = 128;   // rotary_dim <= 256
+struct RotaryParams {
+    void* q_out;
+    const void* q;
+    const void* k;
+    const void* v;
+    void* k_cache;
+    void* v_cache;
+    const float* k_scale;            // [Hkv] scales of an E4M3 cache, else null
+    const float* v_scale;
+    const int64_t* slot_mapping;
+    const int32_t* positions;
+    unsigned* err;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    int64_t num_tokens;
+    int64_t num_blocks;
+    int num_q_heads;
+    int num_kv_heads;
+    int head_dim;
+    int half;                        // rotary_dim / 2
+    int block_size;
+    float magnitude;
+    uint64_t phase[kRotMaxPairs];    // turns per position as 0.64 fixed-point fractions
+};
+cudaError_t launch_rotary(const RotaryParams& p, pa_dtype dtype, bool fp8, bool interleaved,
+                          cudaStream_t stream);
+
 // One copy_blocks launch covers up to kCopyMaxLayers layers and kCopyMaxPairs
 // pairs; the parameter block stays under the classic 4 KB kernel-parameter limit.
 constexpr int kCopyMaxLayers = 8;
