@@ -428,6 +428,131 @@ int pa_chunk_attention_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtyp
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Attention with modified scores: pa_decode and pa_chunk_attention (and their E4M3 forms)
+ * with any of a tanh cap, a bias that grows with distance, a sliding window and tokens that
+ * every row sees.  For the row at position pos (pa_decode: L_s - 1; chunk token j:
+ * L_s - n_s + j) and cached token t < L_s, with x = scale q.k_t:
+ *   score   = softcap > 0 ? softcap * tanh(x / softcap) : x
+ *             - alibi_slopes[h] * |pos - t|                 (when alibi_slopes is given)
+ *   visible = t < g_s, or t <= pos and (window == 0 or pos - t < window)
+ *             with g_s = clamp(global_lens[s], 0, min(L_s, max_global_len)), 0 without
+ *             global_lens
+ * and out = the softmax of the visible scores times V, as in the plain calls.
+ * Uses: global_lens with a window keeps the first tokens of a stream in sight; global_lens
+ * up to a prompt's length in a chunk call lets the prompt's tokens see one another (prefix
+ * mask: tokens after pos are visible below g_s).
+ *
+ *   softcap        0 (none) or 1e-30 .. 1e30
+ *   alibi_slopes   DEVICE float [num_q_heads], or NULL
+ *   window         0 (none), or the number of tokens a row sees up to and with its own
+ *   global_lens    DEVICE int32 [num_seqs], or NULL
+ *   max_global_len host bound on global_lens (larger entries count as this); sizes the
+ *                  grid.  Ignored without global_lens.
+ *   partition_size 0 = automatic; < 0 = one pass; > 0 = partitions of this many tokens to
+ *                  read (a multiple of 128)
+ * Only cache blocks that hold a token some row of the sequence sees are read: a windowed
+ * call costs about window + g_s tokens whatever the context.  The table entries of the
+ * other blocks are not looked at, and K and V of tokens that no row sees may hold anything
+ * (NaN included).  Tokens that some row of the call sees must be finite.
+ * All other arguments, kinds of cache, output types, checks and errors are those of
+ * pa_decode, pa_decode_fp8, pa_chunk_attention and pa_chunk_attention_fp8;
+ * max_context_len is at most 2^30.  Workspace: pa_decode_workspace_bytes /
+ * pa_chunk_workspace_bytes of the same sizes.  out overlaps no input.
+ */
+int pa_decode_mod(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
+                  const void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                  const int32_t* block_tables, int64_t block_table_stride,
+                  const int32_t* context_lens, int32_t max_context_len, int32_t num_seqs,
+                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                  float scale, float softcap, const float* alibi_slopes, int32_t window,
+                  const int32_t* global_lens, int32_t max_global_len, int32_t partition_size,
+                  void* workspace, size_t workspace_bytes, void* stream);
+int pa_decode_mod_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
+                      const void* k_cache, const void* v_cache, const float* k_scale,
+                      const float* v_scale, int64_t num_blocks, const int32_t* block_tables,
+                      int64_t block_table_stride, const int32_t* context_lens,
+                      int32_t max_context_len, int32_t num_seqs, int32_t num_q_heads,
+                      int32_t num_kv_heads, int32_t head_dim, int32_t block_size, float scale,
+                      float softcap, const float* alibi_slopes, int32_t window,
+                      const int32_t* global_lens, int32_t max_global_len, int32_t partition_size,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int pa_chunk_attention_mod(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
+                           const void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                           const int32_t* block_tables, int64_t block_table_stride,
+                           const int32_t* context_lens, const int32_t* query_start,
+                           int64_t num_query_tokens, int32_t max_query_len, int32_t max_context_len,
+                           int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                           int32_t head_dim, int32_t block_size, float scale, float softcap,
+                           const float* alibi_slopes, int32_t window, const int32_t* global_lens,
+                           int32_t max_global_len, int32_t partition_size, void* workspace,
+                           size_t workspace_bytes, void* stream);
+int pa_chunk_attention_mod_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
+                               const void* k_cache, const void* v_cache, const float* k_scale,
+                               const float* v_scale, int64_t num_blocks,
+                               const int32_t* block_tables, int64_t block_table_stride,
+                               const int32_t* context_lens, const int32_t* query_start,
+                               int64_t num_query_tokens, int32_t max_query_len,
+                               int32_t max_context_len, int32_t num_seqs, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                               float scale, float softcap, const float* alibi_slopes,
+                               int32_t window, const int32_t* global_lens, int32_t max_global_len,
+                               int32_t partition_size, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
+ * Shared-prefix decode: pa_decode for a batch whose sequences share long prefixes (samples
+ * forked from one prompt, questions about one document), with the keys and values of each
+ * shared prefix read once for its whole group instead of once per sequence.
+ *
+ * The sequences of group g are group_start[g] .. group_start[g+1]-1 (consecutive;
+ * group_start[0] = 0, group_start[num_groups] = num_seqs; a group of one sequence, or of
+ * prefix length 0, is fine).  The first prefix_lens[s] tokens of a sequence are the ones its
+ * group shares: whole blocks (a multiple of block_size, equal within a group), whose table
+ * entries are read from the group's first sequence; the others of the group name the same
+ * blocks.  out is what pa_decode returns for the same tables and lengths (up to rounding:
+ * the prefix of a group with more than 16 (sequence, head) rows per kv head runs on the
+ * tcgen05 chunk kernel, whose probabilities are one f16 term; see pa_chunk_attention, also
+ * for V elements without an f16 value over a bf16 cache, PA_DEVERR_RANGE).
+ *
+ *   prefix_lens      DEVICE int32 [num_seqs], 0 <= prefix_lens[s] <= context_lens[s]
+ *   group_start      DEVICE int32 [num_groups + 1], non-decreasing
+ *   max_group_size   host bound on the sequences of a group
+ *   max_prefix_len   host bound on prefix_lens (a multiple of block_size)
+ *   max_suffix_len   host bound on context_lens[s] - prefix_lens[s]
+ *   partition_size   0 = automatic split of both passes; < 0 = never; > 0 = that many tokens
+ *                    (a multiple of 128)
+ *   workspace        DEVICE scratch of pa_decode_prefix_workspace_bytes(...), 16-byte
+ *                    aligned, always required; overlaps neither out nor any input
+ * Other arguments as in pa_decode / pa_decode_fp8, kv_dtype PA_F16 or PA_BF16 (PA_F32 is
+ * PA_ERR_UNSUPPORTED), num_q_heads / num_kv_heads <= 128.  A sequence in no group, a group
+ * larger than max_group_size, lengths beyond their bounds, a prefix that is no whole number
+ * of blocks or differs within its group, and a context longer than the table row or shorter
+ * than its prefix set PA_DEVERR_CONTEXT_LEN; the sequence's rows become NaN.
+ */
+size_t pa_decode_prefix_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t head_dim,
+                                        int32_t max_prefix_len, int32_t max_suffix_len,
+                                        int32_t partition_size);
+int pa_decode_prefix(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
+                     const void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                     const int32_t* block_tables, int64_t block_table_stride,
+                     const int32_t* context_lens, const int32_t* prefix_lens,
+                     const int32_t* group_start, int32_t num_groups, int32_t max_group_size,
+                     int32_t max_prefix_len, int32_t max_suffix_len, int32_t num_seqs,
+                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                     int32_t block_size, float scale, int32_t partition_size, void* workspace,
+                     size_t workspace_bytes, void* stream);
+int pa_decode_prefix_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
+                         const void* k_cache, const void* v_cache, const float* k_scale,
+                         const float* v_scale, int64_t num_blocks, const int32_t* block_tables,
+                         int64_t block_table_stride, const int32_t* context_lens,
+                         const int32_t* prefix_lens, const int32_t* group_start,
+                         int32_t num_groups, int32_t max_group_size, int32_t max_prefix_len,
+                         int32_t max_suffix_len, int32_t num_seqs, int32_t num_q_heads,
+                         int32_t num_kv_heads, int32_t head_dim, int32_t block_size, float scale,
+                         int32_t partition_size, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
  * The partition length (tokens) a pa_decode / pa_decode_fp8 call, or a
  * pa_chunk_attention call, with these arguments splits contexts into; 0 when it
  * runs one pass per sequence (no merge launch).  partition_size as in those calls;

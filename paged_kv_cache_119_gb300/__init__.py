@@ -19,7 +19,9 @@ __version__ = "0.1.0"
 
 _API = ("pa_decode", "pa_decode_noalloc", "pa_decode_fp8", "pa_reshape_and_cache",
         "pa_reshape_and_cache_fp8", "pa_rotary_frequencies", "pa_rotary_and_cache",
-        "pa_rotary_and_cache_fp8", "pa_copy_blocks", "pa_decode_workspace_bytes",
+        "pa_rotary_and_cache_fp8", "pa_decode_mod", "pa_decode_mod_fp8", "pa_chunk_attention_mod",
+        "pa_chunk_attention_mod_fp8", "pa_decode_prefix", "pa_decode_prefix_fp8",
+        "pa_decode_prefix_workspace_bytes", "pa_copy_blocks", "pa_decode_workspace_bytes",
         "pa_chunk_attention", "pa_chunk_workspace_bytes", "pa_decode_partition_tokens",
         "pa_decode_orders_sequences",
         "pa_chunk_partition_tokens", "pa_swap_blocks", "pa_chunk_attention_fp8",

@@ -60,6 +60,28 @@ SIGNATURES = {
                                                ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
                                                _i32, _i32, _i32, _i32, _i64, _vp, _i32, _i32,
                                                _f32, _vp]),
+    "pa_decode_mod": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _vp, ctypes.c_int, _i64, _vp,
+                                     _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _f32,
+                                     _vp, _i32, _vp, _i32, _i32, _vp, _sz, _vp]),
+    "pa_decode_mod_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, _vp, _vp,
+                                         _i64, _vp, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                         _f32, _f32, _vp, _i32, _vp, _i32, _i32, _vp, _sz, _vp]),
+    "pa_chunk_attention_mod": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _vp, ctypes.c_int, _i64,
+                                              _vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _i32,
+                                              _i32, _i32, _i32, _f32, _f32, _vp, _i32, _vp, _i32,
+                                              _i32, _vp, _sz, _vp]),
+    "pa_chunk_attention_mod_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp,
+                                                  _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32,
+                                                  _i32, _i32, _i32, _i32, _i32, _i32, _f32, _f32,
+                                                  _vp, _i32, _vp, _i32, _i32, _vp, _sz, _vp]),
+    "pa_decode_prefix_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
+    "pa_decode_prefix": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _vp, ctypes.c_int, _i64, _vp,
+                                        _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                        _i32, _i32, _i32, _f32, _i32, _vp, _sz, _vp]),
+    "pa_decode_prefix_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, _vp,
+                                            _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32,
+                                            _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp,
+                                            _sz, _vp]),
     "pa_copy_blocks": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.POINTER(_vp), _i32,
                                       ctypes.POINTER(_i64), _i64, _i64, _i64, _vp]),
     "pa_swap_blocks": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.POINTER(_vp), _i32,

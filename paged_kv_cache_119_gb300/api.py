@@ -522,6 +522,245 @@ def pa_chunk_attention_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
     return out
 
 
+def _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_size):
+    """Checks shared by the calls below; returns (kv dtype arguments, scale pointers)."""
+    _cuda("out", out)
+    _cuda("q", q)
+    for name, t in ints:
+        _cuda(name, t)
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError(f"q and out must be [rows, Hq, D] of one shape, got {tuple(q.shape)}, "
+                         f"{tuple(out.shape)}")
+    D = q.shape[2]
+    if scales:
+        _fp8_cache("k_cache", k_cache)
+        _fp8_cache("v_cache", v_cache)
+        _scales(*scales, num_kv_heads)
+        if q.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError("q must be float16 or bfloat16 for an E4M3 cache")
+    else:
+        _cuda("k_cache", k_cache)
+        _cuda("v_cache", v_cache)
+        if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
+            raise TypeError("q, k_cache and v_cache must share a dtype")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or \
+            tuple(k_cache.shape[1:]) != (num_kv_heads, block_size, D):
+        raise ValueError(f"k_cache/v_cache must be [N, {num_kv_heads}, {block_size}, {D}], "
+                         f"got {tuple(k_cache.shape)}, {tuple(v_cache.shape)}")
+    _one_device(q, out, k_cache, v_cache, *scales, *[t for _, t in ints])
+
+
+def _scratch(need, workspace, q, stream):
+    """(workspace to keep alive, pointer, bytes): the caller's, or `need` fresh bytes that a
+    call on another stream than the current one may go on using."""
+    if workspace is None:
+        if not need:
+            return None, 0, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(_stream(stream), device=q.device)
+            workspace.record_stream(stream)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _mod(fn, out, q, k_cache, v_cache, scales, block_tables, context_lens, query_start, scale,
+         num_kv_heads, block_size, max_query_len, softcap, alibi_slopes, window, global_lens,
+         max_global_len, max_context_len, partition_size, workspace, stream):
+    ints = [("block_tables", block_tables), ("context_lens", context_lens)]
+    if query_start is not None:
+        ints.append(("query_start", query_start))
+    if global_lens is not None:
+        ints.append(("global_lens", global_lens))
+    _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_size)
+    R, Hq, D = q.shape
+    S = context_lens.shape[0]
+    if context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [S, W] and context_lens [S]")
+    if query_start is None and S != R:
+        raise ValueError("q must hold one row per sequence")
+    if query_start is not None and query_start.shape != (S + 1,):
+        raise ValueError("query_start must be [S + 1]")
+    if alibi_slopes is not None:
+        _cuda("alibi_slopes", alibi_slopes)
+        if alibi_slopes.dtype != torch.float32 or alibi_slopes.shape != (Hq,):
+            raise ValueError("alibi_slopes must be float32 [Hq]")
+        _one_device(q, alibi_slopes)
+    W = block_tables.shape[1]
+    if global_lens is not None:
+        if global_lens.shape != (S,):
+            raise ValueError("global_lens must be [S]")
+        if max_global_len is None:
+            max_global_len = W * block_size
+    if max_context_len is None:
+        max_context_len = W * block_size
+    if query_start is None:
+        need = pa_decode_workspace_bytes(S, Hq, D, max_context_len, block_size, partition_size) \
+            if partition_size >= 0 else 0
+    else:
+        need = pa_chunk_workspace_bytes(R, Hq, D, max_context_len, partition_size) \
+            if partition_size >= 0 else 0
+    workspace, ws_ptr, ws_bytes = _scratch(need, workspace, q, stream)
+    args = [out.data_ptr(), _dtype(out), q.data_ptr()]
+    if scales:
+        args.append(_dtype(q))
+    args += [k_cache.data_ptr(), v_cache.data_ptr()]
+    args += [t.data_ptr() for t in scales] if scales else [_dtype(q)]
+    args += [k_cache.shape[0], block_tables.data_ptr(), W, context_lens.data_ptr()]
+    if query_start is not None:
+        args += [query_start.data_ptr(), R, int(max_query_len)]
+    args += [int(max_context_len), S, Hq, num_kv_heads, D, block_size, float(scale), float(softcap),
+             0 if alibi_slopes is None else alibi_slopes.data_ptr(), int(window),
+             0 if global_lens is None else global_lens.data_ptr(), int(max_global_len or 0),
+             int(partition_size), ws_ptr, ws_bytes, _stream(stream)]
+    N.check(fn, getattr(N.load(), fn)(*args))
+    return out
+
+
+def pa_decode_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                  num_kv_heads: int, block_size: int, softcap: float = 0.0,
+                  alibi_slopes: torch.Tensor | None = None, window: int = 0,
+                  global_lens: torch.Tensor | None = None, max_global_len: int | None = None,
+                  max_context_len: int | None = None, partition_size: int = 0,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_decode with modified scores: softcap > 0 turns x = scale q.k into
+    softcap * tanh(x / softcap); alibi_slopes (float32 [Hq]) subtract slope * distance;
+    window > 0 shows a row its last `window` tokens only; the first global_lens[s] tokens
+    (int32 [S], bounded by max_global_len) stay visible beside the window.  Only blocks that
+    hold a visible token are read."""
+    return _mod("pa_decode_mod", out, q, k_cache, v_cache, (), block_tables, context_lens, None,
+                scale, num_kv_heads, block_size, None, softcap, alibi_slopes, window, global_lens,
+                max_global_len, max_context_len, partition_size, workspace, stream)
+
+
+def pa_decode_mod_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                      block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                      num_kv_heads: int, block_size: int, softcap: float = 0.0,
+                      alibi_slopes: torch.Tensor | None = None, window: int = 0,
+                      global_lens: torch.Tensor | None = None, max_global_len: int | None = None,
+                      max_context_len: int | None = None, partition_size: int = 0,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_decode_mod over E4M3 caches with per-kv-head scales; q float16 or bfloat16."""
+    return _mod("pa_decode_mod_fp8", out, q, k_cache, v_cache, (k_scale, v_scale), block_tables,
+                context_lens, None, scale, num_kv_heads, block_size, None, softcap, alibi_slopes,
+                window, global_lens, max_global_len, max_context_len, partition_size, workspace,
+                stream)
+
+
+def pa_chunk_attention_mod(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, block_tables: torch.Tensor,
+                           context_lens: torch.Tensor, query_start: torch.Tensor, scale: float,
+                           num_kv_heads: int, block_size: int, max_query_len: int,
+                           softcap: float = 0.0, alibi_slopes: torch.Tensor | None = None,
+                           window: int = 0, global_lens: torch.Tensor | None = None,
+                           max_global_len: int | None = None, max_context_len: int | None = None,
+                           partition_size: int = 0, workspace: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
+    """pa_chunk_attention with the modified scores of pa_decode_mod; tokens below
+    global_lens[s] are visible to every row of the sequence, also to rows before them (a
+    prompt whose first tokens see one another)."""
+    return _mod("pa_chunk_attention_mod", out, q, k_cache, v_cache, (), block_tables, context_lens,
+                query_start, scale, num_kv_heads, block_size, max_query_len, softcap, alibi_slopes,
+                window, global_lens, max_global_len, max_context_len, partition_size, workspace,
+                stream)
+
+
+def pa_chunk_attention_mod_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                               v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                               block_tables: torch.Tensor, context_lens: torch.Tensor,
+                               query_start: torch.Tensor, scale: float, num_kv_heads: int,
+                               block_size: int, max_query_len: int, softcap: float = 0.0,
+                               alibi_slopes: torch.Tensor | None = None, window: int = 0,
+                               global_lens: torch.Tensor | None = None,
+                               max_global_len: int | None = None,
+                               max_context_len: int | None = None, partition_size: int = 0,
+                               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_chunk_attention_mod over E4M3 caches with per-kv-head scales."""
+    return _mod("pa_chunk_attention_mod_fp8", out, q, k_cache, v_cache, (k_scale, v_scale),
+                block_tables, context_lens, query_start, scale, num_kv_heads, block_size,
+                max_query_len, softcap, alibi_slopes, window, global_lens, max_global_len,
+                max_context_len, partition_size, workspace, stream)
+
+
+def pa_decode_prefix_workspace_bytes(num_seqs: int, num_q_heads: int, head_dim: int,
+                                     max_prefix_len: int, max_suffix_len: int,
+                                     partition_size: int = 0) -> int:
+    """Workspace bytes of a pa_decode_prefix call with these sizes."""
+    return int(N.load().pa_decode_prefix_workspace_bytes(num_seqs, num_q_heads, head_dim,
+                                                         max_prefix_len, max_suffix_len,
+                                                         partition_size))
+
+
+def _prefix(fn, out, q, k_cache, v_cache, scales, block_tables, context_lens, prefix_lens,
+            group_start, scale, num_kv_heads, block_size, max_group_size, max_prefix_len,
+            max_suffix_len, partition_size, workspace, stream):
+    _attention_args(out, q, k_cache, v_cache, scales,
+                    [("block_tables", block_tables), ("context_lens", context_lens),
+                     ("prefix_lens", prefix_lens), ("group_start", group_start)],
+                    num_kv_heads, block_size)
+    S, Hq, D = q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or \
+            prefix_lens.shape != (S,) or group_start.dim() != 1 or group_start.shape[0] < 1:
+        raise ValueError("block_tables must be [S, W], context_lens and prefix_lens [S], "
+                         "group_start [G + 1]")
+    W = block_tables.shape[1]
+    if max_suffix_len is None:
+        max_suffix_len = W * block_size
+    need = pa_decode_prefix_workspace_bytes(S, Hq, D, max_prefix_len, max_suffix_len,
+                                            partition_size)
+    workspace, ws_ptr, ws_bytes = _scratch(need, workspace, q, stream)
+    args = [out.data_ptr(), _dtype(out), q.data_ptr()]
+    if scales:
+        args.append(_dtype(q))
+    args += [k_cache.data_ptr(), v_cache.data_ptr()]
+    args += [t.data_ptr() for t in scales] if scales else [_dtype(q)]
+    args += [k_cache.shape[0], block_tables.data_ptr(), W, context_lens.data_ptr(),
+             prefix_lens.data_ptr(), group_start.data_ptr(), group_start.shape[0] - 1,
+             int(max_group_size), int(max_prefix_len), int(max_suffix_len), S, Hq, num_kv_heads, D,
+             block_size, float(scale), int(partition_size), ws_ptr, ws_bytes, _stream(stream)]
+    N.check(fn, getattr(N.load(), fn)(*args))
+    return out
+
+
+def pa_decode_prefix(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                     prefix_lens: torch.Tensor, group_start: torch.Tensor, scale: float,
+                     num_kv_heads: int, block_size: int, max_group_size: int, max_prefix_len: int,
+                     max_suffix_len: int | None = None, partition_size: int = 0,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_decode for sequences that share prefixes, reading each shared prefix once.
+
+    Group g is sequences group_start[g] .. group_start[g+1]-1 (int32 [G + 1]); they share
+    their first prefix_lens[s] tokens (int32 [S], whole blocks, equal within a group), found
+    through the first member's table row.  max_group_size, max_prefix_len and max_suffix_len
+    (default W * block_size) are host bounds.  A workspace of
+    pa_decode_prefix_workspace_bytes(...) is allocated with torch when none is given."""
+    return _prefix("pa_decode_prefix", out, q, k_cache, v_cache, (), block_tables, context_lens,
+                   prefix_lens, group_start, scale, num_kv_heads, block_size, max_group_size,
+                   max_prefix_len, max_suffix_len, partition_size, workspace, stream)
+
+
+def pa_decode_prefix_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                         v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                         block_tables: torch.Tensor, context_lens: torch.Tensor,
+                         prefix_lens: torch.Tensor, group_start: torch.Tensor, scale: float,
+                         num_kv_heads: int, block_size: int, max_group_size: int,
+                         max_prefix_len: int, max_suffix_len: int | None = None,
+                         partition_size: int = 0, workspace: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """pa_decode_prefix over E4M3 caches with per-kv-head scales; q float16 or bfloat16."""
+    return _prefix("pa_decode_prefix_fp8", out, q, k_cache, v_cache, (k_scale, v_scale),
+                   block_tables, context_lens, prefix_lens, group_start, scale, num_kv_heads,
+                   block_size, max_group_size, max_prefix_len, max_suffix_len, partition_size,
+                   workspace, stream)
+
+
 def pa_decode_partition_tokens(q_dtype: torch.dtype, kv_dtype: torch.dtype, num_seqs: int,
                                num_q_heads: int, num_kv_heads: int, head_dim: int,
                                block_size: int, max_context_len: int,

@@ -69,6 +69,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "score_mods.cuh"
 #include "tc_device.cuh"
 
 namespace pa {
@@ -85,6 +86,7 @@ constexpr int kChunkConvWarps = 4;
 constexpr int kChunkThreadsConv = kChunkThreads + 32 * kChunkConvWarps;
 // P.V takes P as 2^kChunkPExp p: p <= 2^8 (the lazy rescale), so 2^15 at most in f16
 constexpr float kChunkPExp = 7.f;
+static_assert(kChunkPExp == 7.f, "the partial rows of a shared prefix take 2^-7 off again");
 
 // NRAW > 0 (E4M3 caches): a ring of NRAW raw one-byte K + V tiles that the converter
 // warps turn into the 16-bit tiles of the NST-stage ring.
@@ -173,16 +175,27 @@ __device__ __forceinline__ float max3f(float a, float b, float c)
 // tensor-core operands are f16: the codes convert exactly, a bf16 query row is scaled
 // into f16 range by a power of two (exact), and the scales fold into the scores and
 // the output.
-template <typename T, int D, int BS, int NST, int NRAW = 0>
-__global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>) ? kChunkThreadsConv
-                                                                                 : kChunkThreads,
-                                  1)
+// MODE: kPlain; kMod, modified scores: only the tiles that hold a token some row of the CTA
+// sees are read, and the converter warps (over every cache type) zero the V rows of tokens no
+// row sees; kPrefix, the rows of a group of sequences (query_start = the group's first one)
+// over the tokens they share, partial rows only.
+template <typename T, int NRAW, int MODE>
+constexpr int chunk_threads()
+{
+    return (NRAW > 0 || std::is_same_v<T, __nv_bfloat16> || MODE == kMod) ? kChunkThreadsConv
+                                                                          : kChunkThreads;
+}
+
+template <typename T, int D, int BS, int NST, int NRAW = 0, int MODE = kPlain>
+__global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     chunk_attn_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv)
 {
     using Sm = ChunkSmem<D, NST, NRAW>;
     constexpr bool kF8 = NRAW > 0;
     constexpr bool kVConv = !kF8 && std::is_same_v<T, __nv_bfloat16>;   // bf16 V -> f16 in place
+    constexpr bool kVHand = kVConv || (!kF8 && MODE == kMod);           // V handed over (vconv)
+    constexpr bool kVZero = !kVConv && MODE != kMod;    // softmax warps zero the last tile's V rows
     using TM = std::conditional_t<kF8, __half, T>;   // operand type of the score product
     constexpr int NT = kChunkTileTok;
     constexpr int BPT = NT / BS;                 // cache blocks per K/V tile
@@ -214,16 +227,19 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
     const int kvh = blockIdx.y / p.m_tiles;
     const int mt = blockIdx.y - kvh * p.m_tiles;
     const int part = blockIdx.x;
-    const bool split = p.partition_tokens > 0;
+    const bool split = MODE == kPrefix || p.partition_tokens > 0;
     const int G = p.group;
     const int TT = p.rows_tokens;
 
     const int qs0 = p.query_start[seq];
     const int qs1 = p.query_start[seq + 1];
     const int n = qs1 - qs0;
-    const int L = p.context_lens[seq];
     const bool rows_sane = qs0 >= 0 && n >= 0 && (int64_t)qs1 <= p.num_rows;
-    if (!rows_sane || L < 0 || L > p.max_context_len || n > L || n > p.max_query_len) {
+    // the sequence whose table row and lengths count: a group's first one (kPrefix)
+    const int tseq = MODE == kPrefix ? (rows_sane && n > 0 ? qs0 : 0) : seq;
+    const int L = MODE == kPrefix ? p.prefix_lens[tseq] : p.context_lens[seq];
+    if (!rows_sane || L < 0 || L > p.max_context_len || n > p.max_query_len ||
+        (MODE == kPrefix ? L % BS != 0 : n > L)) {
         if (part == 0 && blockIdx.y == 0 && threadIdx.x == 0)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
         if (!split && rows_sane && part == 0 && mt == 0) {
@@ -249,15 +265,37 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
         return;                                  // no chunk token in this row tile
     const int ntok = min(TT, n - j0);
     const int pos_first = L - n + j0;            // position of the tile's first token
-    const int t_end = pos_first + ntok;          // tokens [0, t_end) are seen by some row
-    int t0 = 0, t1 = t_end;
-    if (split) {
-        t0 = part * p.partition_tokens;
-        if (t0 >= t_end)
+    int t_end = MODE == kPrefix ? L : pos_first + ntok;   // tokens [0, t_end) are seen by some row
+    int t0 = 0, ntiles = 0;
+    Seen seen{0, 0, 0};
+    TileOrder order{0, 0, 0};
+    int c0 = 0;                                  // kMod: first tile of the list to read
+    if constexpr (MODE == kMod) {
+        seen = seen_by(p.mods, seq, L, pos_first, pos_first + ntok - 1);
+        order = seen_tiles(seen, NT);
+        t_end = seen.end;
+        c0 = split ? part * (p.partition_tokens / NT) : 0;
+        if (c0 >= order.count)
             return;
-        t1 = min(t_end, t0 + p.partition_tokens);
+        ntiles = split ? min(order.count - c0, p.partition_tokens / NT) : order.count;
     }
-    const int ntiles = (t1 - t0 + NT - 1) / NT;  // >= 1
+    int t1 = t_end;
+    if constexpr (MODE != kMod) {
+        if (p.partition_tokens > 0) {
+            t0 = part * p.partition_tokens;
+            t1 = min(t_end, t0 + p.partition_tokens);
+        }
+        if (t0 >= t_end)
+            return;                              // (unsplit: an empty shared prefix)
+        ntiles = (t1 - t0 + NT - 1) / NT;        // >= 1
+    }
+    // first token of tile it
+    auto tile_token = [&](int it) -> int {
+        if constexpr (MODE == kMod)
+            return order(c0 + it) * NT;
+        else
+            return t0 + it * NT;
+    };
 
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -302,7 +340,7 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
 
     if (warp == 0) {
         // ------------------------------------------------------------------ producer
-        const int32_t* bt_row = p.block_tables + (int64_t)seq * p.bt_stride;
+        const int32_t* bt_row = p.block_tables + (int64_t)tseq * p.bt_stride;
         const uint64_t policy = l2_evict_first_policy();
         const int blk_end = (t1 + BS - 1) / BS;
         // 16-bit caches fill the MMA ring directly; E4M3 caches fill the raw ring
@@ -313,11 +351,14 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
         int issued = 0;
         for (int it = 0; it < ntiles; ++it) {
             const int st = it % NP;
-            const int b0 = (t0 + it * NT) / BS;
-            const int nb = min(BPT, blk_end - b0);
+            const int b0 = tile_token(it) / BS;
+            bool want = lane < min(BPT, blk_end - b0);
+            if constexpr (MODE == kMod)          // only blocks that hold a seen token
+                want = want && any_seen(seen, (b0 + lane) * BS, min((b0 + lane) * BS + BS, t1));
+            const int nb = __popc(__ballot_sync(kFullMask, want));
             int pbn = -1;
             bool valid = false;
-            if (lane < nb) {
+            if (want) {
                 pbn = __ldg(bt_row + b0 + lane);
                 valid = pbn >= 0 && (int64_t)pbn < p.num_blocks;
             }
@@ -361,7 +402,7 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
             for (int it = max(0, issued - NP); it < issued; ++it)
                 mbar_wait(&pfull[it % NP], (it / NP) & 1);
         __syncwarp();
-    } else if ((kF8 || kVConv) && warp > 2 + kChunkSoftmaxWarps) {
+    } else if ((kF8 || kVHand) && warp > 2 + kChunkSoftmaxWarps) {
         // ------------------------------------------------ E4M3 -> f16 tile conversion
         // A raw tile row is 128 codes in 128-byte-swizzled order (16-byte chunk c of row
         // t at c ^ (t & 7)); the f16 tile is two 64-dim halves of 128-byte rows in the
@@ -382,14 +423,17 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
                 }
                 const unsigned char* raw = smem + Sm::kRawOff + r * Sm::kRawStage;
                 unsigned char* dst = smem + Sm::kStageOff + st * Sm::kStageBytes;
+                const int tb = tile_token(it);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll 4
                     for (int item = ct; item < kItems; item += 32 * kChunkConvWarps) {
                         const int t = item >> 3;
                         const int c = item & 7;
-                        const uint4 w = *reinterpret_cast<const uint4*>(
+                        uint4 w = *reinterpret_cast<const uint4*>(
                             raw + kv * Sm::kRawTile + t * 128 + ((c ^ (t & 7)) << 4));
+                        if (MODE == kMod && kv == 1 && !is_seen(seen, tb + t))
+                            w = make_uint4(0u, 0u, 0u, 0u);
                         unsigned char* row =
                             dst + kv * Sm::kKBytes + (c >> 2) * Sm::kKVHalf + t * 128;
                         const int c0 = 2 * (c & 3);
@@ -428,7 +472,8 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
                         atomicOr(p.err, PA_DEVERR_TIMEOUT);
                     break;
                 }
-                const int nv = min(NT, t1 - (t0 + it * NT));  // rows inside the range
+                const int tb = tile_token(it);
+                const int nv = min(NT, t1 - tb);              // rows inside the range
                 unsigned char* vt = smem + Sm::kStageOff + st * Sm::kStageBytes + Sm::kKBytes;
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
@@ -437,7 +482,7 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
                     uint4* chunk = reinterpret_cast<uint4*>(vt + (item / (NT * 8)) * Sm::kKVHalf +
                                                             w * 16);
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if ((w >> 3) < nv) {
+                    if ((w >> 3) < nv && (MODE != kMod || is_seen(seen, tb + (w >> 3)))) {
                         const uint4 b = *chunk;
                         const uint32_t in[4] = {b.x, b.y, b.z, b.w};
                         uint32_t o[4];
@@ -452,6 +497,31 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
                     *chunk = v;
                 }
                 fence_proxy_async_smem();                    // f16 V -> tensor core
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&vconv[st]);
+            }
+        } else if constexpr (kVHand) {
+            // f16 V needs no conversion: only the rows of tokens no row sees become 0
+            const int ct = threadIdx.x - kChunkThreads;
+            for (int it = 0; it < ntiles; ++it) {
+                const int st = it % NST;
+                if (!mbar_wait(&full[st], (it / NST) & 1)) {
+                    if (lane == 0)
+                        atomicOr(p.err, PA_DEVERR_TIMEOUT);
+                    break;
+                }
+                const int tb = tile_token(it);
+                if (tb + NT > t1 || (tb < seen.lo && tb + NT > seen.glob)) {
+                    unsigned char* vt = smem + Sm::kStageOff + st * Sm::kStageBytes + Sm::kKBytes;
+                    for (int item = ct; item < NT * 8 * Sm::kHalves; item += 32 * kChunkConvWarps) {
+                        const int w = item % (NT * 8);
+                        if (!is_seen(seen, tb + (w >> 3)))
+                            *reinterpret_cast<uint4*>(vt + (item / (NT * 8)) * Sm::kKVHalf + w * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&vconv[st]);
@@ -496,10 +566,10 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
                     issue_scores(it + 1);
                 }
                 ok = mbar_wait(&p_full[q * 2 + (it & 1)], (it >> 1) & 1);
-                if constexpr (kVConv) {
+                if constexpr (kVHand) {
                     if (ok)                           // V in f16, rows past the range zeroed
                         ok = mbar_wait(&vconv[it % NST], (it / NST) & 1);
-                } else {
+                } else if constexpr (kVZero) {
                     if (ok && t0 + (it + 1) * NT > t1)
                         ok = mbar_wait(v_zero, 0);   // last tile: V rows past the range zeroed
                 }
@@ -533,7 +603,12 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
         const int tok = r / G;
         const int g = r - tok * G;
         const bool row_valid = tok < ntok;               // (r >= TT * G gives tok >= TT)
-        const int pos = pos_first + tok;
+        const int pos = MODE == kPrefix ? L - 1 : pos_first + tok;
+        // kMod: first visible position past the global tokens, base-2 distance slope
+        const int low = MODE == kMod && p.mods.window > 0 ? max(0, pos - p.mods.window + 1) : 0;
+        const float slope = MODE == kMod && p.mods.slopes
+                                ? p.mods.slopes[kvh * G + g] * 1.4426950408889634f
+                                : 0.f;
         const int64_t qrow = (int64_t)(qs0 + j0 + tok) * p.num_q_heads + (int64_t)kvh * G + g;
         // scores are used as s * sl2 with sl2 > 0: a negative scale flips the sign of q
         // (exact), a zero scale makes q zero (every score 0); over E4M3 caches the K scale
@@ -608,7 +683,7 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
         for (int it = 0; it < ntiles; ++it) {
             const int b = it & 1;
             const int st = it % NST;
-            const int tb = t0 + it * NT;
+            const int tb = tile_token(it);
             bool ok = mbar_wait(&s_full[q * 2 + b], (it >> 1) & 1);
             ok = ok && mbar_wait(&full[st], (it / NST) & 1);   // stage_ok and the tile's bytes
             if (!ok) {
@@ -626,7 +701,29 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
                 tmem_ld64(sp_col, s);
             if (warp_live) {
                 const int lim = row_valid ? pos - tb : -1;   // columns c <= lim are visible
-                if (lim < NT - 1) {
+                if constexpr (MODE == kMod) {
+                    // from here on s holds the modified scores in base-2 units
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+                        s[c] *= sl2;
+                    if (p.mods.cap > 0.f) {
+#pragma unroll
+                        for (int c = 0; c < NT; ++c)
+                            s[c] = cap_score(s[c], p.mods);
+                    }
+                    if (p.mods.slopes) {
+#pragma unroll
+                        for (int c = 0; c < NT; ++c)
+                            s[c] = fmaf(-slope, (float)abs(pos - tb - c), s[c]);
+                    }
+                    // column c is visible when c < gl, or lo <= c <= lim
+                    const int gl = row_valid ? seen.glob - tb : 0, lo = low - tb;
+                    if (gl < NT && (lim < NT - 1 || lo > 0)) {
+#pragma unroll
+                        for (int c = 0; c < NT; ++c)
+                            s[c] = (c < gl || (c >= lo && c <= lim)) ? s[c] : -INFINITY;
+                    }
+                } else if (lim < NT - 1) {
 #pragma unroll
                     for (int c = 0; c < NT; ++c)
                         s[c] = c <= lim ? s[c] : -INFINITY;
@@ -645,7 +742,8 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
                     mx[c & 7] = fmaxf(mx[c & 7], s[c]);
                 const float smax = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]),
                                          fmaxf(mx[6], mx[7]));
-                const float tmax = smax == -INFINITY ? -INFINITY : smax * sl2;
+                const float mul = MODE == kMod ? 1.f : sl2;
+                const float tmax = smax == -INFINITY ? -INFINITY : smax * mul;
                 const bool need = tmax > m_ref + 8.f;
                 if (it > 0 && __any_sync(kFullMask, need)) {
                     // O holds P.V of tiles 0 .. it-1: wait for the last, then rescale the
@@ -681,7 +779,7 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
                                  make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < NT; c += 2) {
-                    const float2 x = ffma2(make_float2(s[c], s[c + 1]), make_float2(sl2, sl2),
+                    const float2 x = ffma2(make_float2(s[c], s[c + 1]), make_float2(mul, mul),
                                            make_float2(nm, nm));
                     s[c] = ex2_approx(x.x);
                     s[c + 1] = ex2_approx(x.y);
@@ -701,7 +799,7 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
                 }
                 tmem_st32_raw(sp_col, ph);
             }
-            if (!kVConv && tb + NT > t1) {
+            if (kVZero && tb + NT > t1) {
                 // V rows past the range may hold anything (unused slots, stale tiles):
                 // zero them so that 0 * V stays 0; both issuers wait for v_zero before
                 // their last P.V
@@ -760,7 +858,8 @@ __global__ void __launch_bounds__((NRAW > 0 || std::is_same_v<T, __nv_bfloat16>)
                     store_row32(p.part_o, prw * D + 32 * c4, o, inv, poisoned, 0);
                     if (c4 == 0) {
                         p.part_ml[prw * 2 + 0] = poisoned ? __int_as_float(0x7fc00000) : m_ref;
-                        p.part_ml[prw * 2 + 1] = lsum;
+                        // the sum carries 2^7; the suffix rows it is merged with do not
+                        p.part_ml[prw * 2 + 1] = MODE == kPrefix ? lsum * 0x1p-7f : lsum;
                     }
                 } else {
                     store_row32(p.out, qrow * D + 32 * c4, o, inv, poisoned, which);

@@ -45,6 +45,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "score_mods.cuh"
 
 namespace pa {
 
@@ -125,7 +126,9 @@ __device__ __forceinline__ int2 decode_seq(const DecodeParams& p)
 
 // T: query / native output type.  TK: cache element type (T itself, or
 // __nv_fp8_e4m3 for a quantised cache whose value is code * per-kv-head scale).
-template <typename T, typename TK, int D, int BS, int GC, int NSTAGE>
+// MODE: kPlain; kMod reads only the tiles that hold a visible token; kSuffix reads the
+// tokens after the shared prefix and writes partial rows (split or not).
+template <typename T, typename TK, int D, int BS, int GC, int NSTAGE, int MODE = kPlain>
 __global__ void __launch_bounds__(kDecodeThreads)
     decode_kernel(const DecodeParams p)
 {
@@ -159,10 +162,18 @@ __global__ void __launch_bounds__(kDecodeThreads)
     const int kvh = blockIdx.y / p.chunks;
     const int h0 = kvh * p.group + (blockIdx.y % p.chunks) * GC;
     const int part = blockIdx.x;
-    const bool split = p.partition_tokens > 0;
+    const bool split = MODE == kSuffix || p.partition_tokens > 0;
 
     const int L = seq_len.y;
-    if (L < 0 || L > p.max_context_len) {
+    int start = 0;                                // first token of this pass
+    bool bad_len = L < 0 || L > p.max_context_len;
+    if constexpr (MODE == kSuffix) {
+        start = p.prefix_lens[seq];
+        bad_len = start < 0 || start > p.max_prefix_len || start % BS != 0 || start > L ||
+                  L > p.max_context_len ||
+                  L - start > p.max_suffix_len;
+    }
+    if (bad_len) {
         if (part == 0 && blockIdx.y == 0 && threadIdx.x == 0)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
         if (!split) {                             // the reduce pass handles split calls
@@ -172,15 +183,35 @@ __global__ void __launch_bounds__(kDecodeThreads)
         }
         return;
     }
-    int t0 = 0, t1 = L;
-    if (split) {
-        t0 = part * p.partition_tokens;
-        if (t0 >= L)
-            return;                               // this partition lies past the context
-        t1 = min(L, t0 + p.partition_tokens);
+    int t0 = start, t1 = L;
+    int jb = 0, ntiles = 0;
+    Seen seen{0, 0, 0};
+    TileOrder order{0, 0, 0};
+    if constexpr (MODE == kMod) {
+        // partitions cut the list of tiles to read
+        seen = seen_by(p.mods, seq, L, L - 1, L - 1);
+        order = seen_tiles(seen, BS);
+        jb = split ? part * (p.partition_tokens / BS) : 0;
+        if (split && jb >= order.count)
+            return;
+        ntiles = split ? min(order.count - jb, p.partition_tokens / BS) : order.count;
+    } else {
+        if (p.partition_tokens > 0) {
+            t0 += part * p.partition_tokens;
+            if (t0 >= L)
+                return;                           // this partition lies past the context
+            t1 = min(L, t0 + p.partition_tokens);
+        }
+        jb = t0 / BS;                             // partitions start on block boundaries
+        ntiles = (t1 > t0) ? (t1 + BS - 1) / BS - jb : 0;
     }
-    const int jb = t0 / BS;                       // partitions start on block boundaries
-    const int ntiles = (t1 > t0) ? (t1 + BS - 1) / BS - jb : 0;
+    // the cache block of tile it
+    auto block_of = [&](int it) -> int {
+        if constexpr (MODE == kMod)
+            return order(jb + it);
+        else
+            return jb + it;
+    };
 
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -206,17 +237,17 @@ __global__ void __launch_bounds__(kDecodeThreads)
         // ------------------------------------------------------------------ producer
         if (fault)
             return;
-        const int32_t* bt_row = p.block_tables + (int64_t)seq * p.bt_stride + jb;
+        const int32_t* bt_row = p.block_tables + (int64_t)seq * p.bt_stride;
         const TK* kpool = reinterpret_cast<const TK*>(p.k_cache) + (int64_t)kvh * kTile;
         const TK* vpool = reinterpret_cast<const TK*>(p.v_cache) + (int64_t)kvh * kTile;
         const int64_t blk_stride = (int64_t)p.num_kv_heads * kTile;
         const uint64_t policy = l2_evict_first_policy();
-        int next = (lane < ntiles) ? __ldg(bt_row + lane) : 0;
+        int next = (lane < ntiles) ? __ldg(bt_row + block_of(lane)) : 0;
         bool aborted = false;
         for (int base = 0; base < ntiles && !aborted; base += 32) {
             const int cur = next;
             if (base + 32 + lane < ntiles)
-                next = __ldg(bt_row + base + 32 + lane);   // next round, in flight meanwhile
+                next = __ldg(bt_row + block_of(base + 32 + lane));   // next round, in flight meanwhile
             const int cnt = min(32, ntiles - base);
             for (int i = 0; i < cnt; ++i) {
                 const int pbn = __shfl_sync(kFullMask, cur, i);
@@ -274,6 +305,12 @@ __global__ void __launch_bounds__(kDecodeThreads)
         for (int e = 0; e < E; ++e)
             acc[g][e] = 0.f;
     }
+    float slope[GC];                              // kMod: base-2 distance slopes
+    if constexpr (MODE == kMod) {
+#pragma unroll
+        for (int g = 0; g < GC; ++g)
+            slope[g] = p.mods.slopes ? p.mods.slopes[h0 + g] * 1.4426950408889634f : 0.f;
+    }
     bool poisoned = false;
     float* my_p = pbuf + warp * GC * BS;
     const int mytok = lane >> TOK_SHIFT;
@@ -295,7 +332,13 @@ __global__ void __launch_bounds__(kDecodeThreads)
         }
         const TK* Ks = ring + stage * 2 * kTile;
         const TK* Vs = Ks + kTile;
-        const int nvalid = min(BS, t1 - (jb + it) * BS);
+        const int tb = block_of(it) * BS;          // first token of the tile
+        const int nvalid = min(BS, t1 - tb);
+        // kMod: bit t is set when token tb + t is visible (the others' rows may hold
+        // anything, and 0 * NaN is NaN: P.V skips them)
+        uint32_t vis = 0xffffffffu;
+        if constexpr (MODE == kMod)
+            vis = __ballot_sync(kFullMask, lane < nvalid && is_seen(seen, tb + lane));
 
         // Small tiles are copied to registers and the stage is released at once, so
         // the producer refills it while this warp computes (the stage would
@@ -350,12 +393,24 @@ __global__ void __launch_bounds__(kDecodeThreads)
             }
         }
 #pragma unroll
-        for (int c = 0; c < NCH; ++c)
-            if (c * TC + mytok >= nvalid) {
+        for (int c = 0; c < NCH; ++c) {
+            bool hidden = c * TC + mytok >= nvalid;
+            if constexpr (MODE == kMod) {
+                hidden = !((vis >> (c * TC + mytok)) & 1u);
+                const float dist = (float)(L - 1 - (tb + c * TC + mytok));
+#pragma unroll
+                for (int g = 0; g < GC; ++g) {
+                    if (p.mods.cap > 0.f)
+                        s[g][c] = p.mods.cap * tanhf(s[g][c] * p.mods.inv_cap);
+                    s[g][c] = fmaf(-slope[g], dist, s[g][c]);
+                }
+            }
+            if (hidden) {
 #pragma unroll
                 for (int g = 0; g < GC; ++g)
                     s[g][c] = -INFINITY;
             }
+        }
 
         // online softmax update per head
 #pragma unroll
@@ -367,7 +422,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
 #pragma unroll
             for (int msk = 16; msk >= (1 << TOK_SHIFT); msk >>= 1)
                 tmax = fmaxf(tmax, __shfl_xor_sync(kFullMask, tmax, msk));
-            const float mnew = fmaxf(m[g], tmax);        // finite: nvalid >= 1
+            const float mnew = fmaxf(m[g], tmax);        // finite: a tile has a visible token
             const float alpha = exp2f(m[g] - mnew);       // 0 on the first tile
             m[g] = mnew;
             float psum = 0.f;
@@ -395,14 +450,14 @@ __global__ void __launch_bounds__(kDecodeThreads)
         // acc += P . V over the valid tokens of the tile
 #pragma unroll
         for (int t4 = 0; t4 < BS; t4 += 4) {
-            if (t4 < nvalid) {
+            if (MODE == kMod ? ((vis >> t4) & 15u) != 0u : t4 < nvalid) {
                 float4 pv[GC];
 #pragma unroll
                 for (int g = 0; g < GC; ++g)
                     pv[g] = *reinterpret_cast<const float4*>(my_p + g * BS + t4);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    if (t4 + u < nvalid) {
+                    if (MODE == kMod ? ((vis >> (t4 + u)) & 1u) != 0u : t4 + u < nvalid) {
                         float vf[E];
                         v_row(t4 + u, vf);
 #pragma unroll
@@ -472,7 +527,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
             o = __int_as_float(0x7fc00000);
         const int64_t row = (int64_t)seq * p.num_q_heads + h0 + g;
         if (split) {
-            const int64_t prow = row * p.max_parts + part;
+            const int64_t prow = row * p.max_parts + (MODE == kSuffix ? p.part_base : 0) + part;
             p.part_o[prow * D + d] = o;
             if (d == 0) {
                 p.part_ml[prow * 2 + 0] = M;
@@ -541,11 +596,11 @@ inline int kernel_occupancy(const void* kernel, int smem_bytes)
     return n;
 }
 
-template <typename T, typename TK, int D, int BS, int GC>
+template <typename T, typename TK, int D, int BS, int GC, int MODE = kPlain>
 struct CoreVariant {
     static constexpr int kStages = DecodeStages<TK, D, BS>::value;
     using Smem = DecodeSmem<TK, D, BS, GC, kStages>;
-    static constexpr auto kernel() { return decode_kernel<T, TK, D, BS, GC, kStages>; }
+    static constexpr auto kernel() { return decode_kernel<T, TK, D, BS, GC, kStages, MODE>; }
     static cudaError_t configure()
     {
         return configure_once(reinterpret_cast<const void*>(kernel()), Smem::kBytes);
@@ -556,10 +611,10 @@ struct CoreVariant {
         if (err != cudaSuccess)
             return err;
         const bool split = p.partition_tokens > 0;
-        dim3 grid(split ? p.max_parts : 1, p.num_kv_heads * p.chunks, p.num_seqs);
+        dim3 grid(split ? p.max_parts - p.part_base : 1, p.num_kv_heads * p.chunks, p.num_seqs);
         kernel()<<<grid, kDecodeThreads, Smem::kBytes, stream>>>(p);
         err = cudaGetLastError();
-        if (err != cudaSuccess || !split)
+        if (err != cudaSuccess || !split || MODE != kPlain)   // the others merge on their own
             return err;
         reduce_kernel<T, D><<<dim3(p.num_q_heads, p.num_seqs), D, 0, stream>>>(p);
         return cudaGetLastError();

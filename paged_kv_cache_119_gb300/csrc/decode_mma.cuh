@@ -201,7 +201,12 @@ constexpr int mma_min_blocks() { return (sizeof(TK) == 1 && BS == 32) ? 3 : 4; }
 // sequence attended causally, each row masked at its own position (speculative
 // verification, short chunks) -- instead of NH query heads of one token.
 // BPT: cache blocks per tile (a ring stage); the tile is TB = BS * BPT tokens.
-template <typename T, typename TK, int D, int BS, int NH, int NSTAGE, bool CH = false, int BPT = 1>
+// MODE (with CH): kMod, chunk rows with modified scores (query_start null: one row per query
+// head of each sequence's last token); kPrefix, the rows of a group of sequences over the
+// tokens they share (blockIdx.z = group); kSuffix, each sequence's query heads over its
+// tokens after the shared prefix.  kPrefix and kSuffix write partial rows only.
+template <typename T, typename TK, int D, int BS, int NH, int NSTAGE, bool CH = false, int BPT = 1,
+          int MODE = kPlain>
 __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>())
     decode_mma_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv)
@@ -235,19 +240,41 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     const int kvh = blockIdx.y / p.chunks;
     const int h0 = kvh * p.group + (blockIdx.y % p.chunks) * NH;
     const int part = blockIdx.x;
-    const bool split = p.partition_tokens > 0;
+    static_assert(MODE == kPlain || CH, "the other modes address rows as chunk rows");
+    const bool split = MODE == kPrefix || MODE == kSuffix || p.partition_tokens > 0;
 
-    const int L = p.context_lens[seq];
     // chunk rows: the sequence's rows of q / out are query_start[seq] .. + n - 1
     int qs0 = 0, n = 1, R0 = 0;
     if constexpr (CH) {
-        qs0 = p.query_start[seq];
-        n = p.query_start[seq + 1] - qs0;
         R0 = (blockIdx.y % p.chunks) * NH;
+        if (MODE == kSuffix || (MODE == kMod && !p.query_start)) {
+            qs0 = seq;
+        } else {
+            qs0 = p.query_start[seq];
+            n = p.query_start[seq + 1] - qs0;
+        }
     }
     const bool rows_sane = !CH || (qs0 >= 0 && n >= 0 && (int64_t)qs0 + n <= p.num_rows);
-    if (L < 0 || L > p.max_context_len || !rows_sane ||
-        (CH && (n > L || n > p.max_query_len))) {
+    // the sequence whose table row and lengths count: a group's first one (kPrefix)
+    const int tseq = MODE == kPrefix ? (rows_sane && n > 0 ? qs0 : 0) : seq;
+    int L, start = 0;                             // the tokens of this pass are start .. L - 1
+    bool bad_len;
+    if constexpr (MODE == kPrefix) {
+        L = p.prefix_lens[tseq];
+        bad_len = L < 0 || L > p.max_prefix_len || L % BS != 0 || n > p.max_query_len;
+    } else {
+        L = p.context_lens[seq];
+        bad_len = L < 0 || L > p.max_context_len || (CH && MODE != kSuffix && (n > L || n > p.max_query_len));
+        if constexpr (MODE == kSuffix) {
+            start = p.prefix_lens[seq];
+            bad_len = start < 0 || start > p.max_prefix_len || start % BS != 0 || start > L ||
+                      L > p.max_context_len ||
+                      L - start > p.max_suffix_len;
+        }
+        if (MODE == kMod && !p.query_start)
+            bad_len = L < 0 || L > p.max_context_len;      // an empty context is a zero row
+    }
+    if (bad_len || !rows_sane) {
         if (part == 0 && blockIdx.y == 0 && threadIdx.x == 0)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
         if (!split && rows_sane) {
@@ -268,24 +295,61 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
         return;
     }
     int t_end = L;
+    Seen seen{0, 0, 0};
+    TileOrder order{0, 0, 0};
     if constexpr (CH) {
-        if (seq == p.num_seqs - 1 && part == 0 && blockIdx.y == 0 && threadIdx.x == 0 &&
-            (int64_t)qs0 + n != p.num_rows)
+        if (MODE != kSuffix && seq == (int)gridDim.z - 1 && part == 0 && blockIdx.y == 0 &&
+            threadIdx.x == 0 && (int64_t)qs0 + n != p.num_rows)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);   // rows after the last chunk belong to no one
         if (R0 / p.group >= n)
             return;                                // no chunk token in this row chunk
-        t_end = L - n + min(n - 1, (R0 + NH - 1) / p.group) + 1;   // last row's position + 1
+        const int last = L - n + min(n - 1, (R0 + NH - 1) / p.group);   // last row's position
+        if constexpr (MODE == kPlain)
+            t_end = last + 1;
+        if constexpr (MODE == kMod) {
+            seen = seen_by(p.mods, seq, L, L - n + R0 / p.group, last);
+            order = seen_tiles(seen, TB);
+            t_end = seen.end;
+        }
     }
-    int t0 = 0, t1 = t_end;
-    if (split) {
-        t0 = part * p.partition_tokens;
-        if (t0 >= t_end)
+    int t0 = start, t1 = t_end;
+    int jb = 0, nblk = 0, ntiles = 0;
+    if constexpr (MODE == kMod) {
+        // partitions cut the list of tiles to read; jb counts tiles of that list
+        jb = split ? part * (p.partition_tokens / TB) : 0;
+        if (split && jb >= order.count)
             return;
-        t1 = min(t_end, t0 + p.partition_tokens);
+        ntiles = split ? min(order.count - jb, p.partition_tokens / TB) : order.count;
+        nblk = ntiles * BPT;
+    } else {
+        if (p.partition_tokens > 0) {
+            t0 += part * p.partition_tokens;
+            if (t0 >= t_end)
+                return;
+            t1 = min(t_end, t0 + p.partition_tokens);
+        }
+        jb = t0 / BS;                             // first cache block (partitions start on one)
+        nblk = (t1 > t0) ? (t1 + BS - 1) / BS - jb : 0;
+        ntiles = (nblk + BPT - 1) / BPT;          // tile it: blocks jb + BPT it .. + BPT - 1
     }
-    const int jb = t0 / BS;                       // first cache block (partitions start on one)
-    const int nblk = (t1 > t0) ? (t1 + BS - 1) / BS - jb : 0;
-    const int ntiles = (nblk + BPT - 1) / BPT;    // tile it: blocks jb + BPT it .. + BPT - 1
+    // first token of tile it, and the cache block of the CTA's i-th block
+    auto tile_token = [&](int it) -> int {
+        if constexpr (MODE == kMod)
+            return order(jb + it) * TB;
+        else
+            return jb * BS + it * TB;
+    };
+    auto block_of = [&](int i) -> int {
+        if constexpr (MODE == kMod)
+            return order(jb + i / BPT) * BPT + i % BPT;
+        else
+            return jb + i;
+    };
+    // kMod: whether block b of the context holds a seen token (the others are neither read
+    // nor checked: an engine may have freed them)
+    auto block_seen = [&](int b) -> bool {
+        return MODE != kMod || any_seen(seen, b * BS, min(b * BS + BS, t1));
+    };
 
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -304,16 +368,22 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
 
     if (warp == NCW) {
         // ------------------------------------------------------------------ producer
-        const int32_t* bt_row = p.block_tables + (int64_t)seq * p.bt_stride + jb;
+        const int32_t* bt_row = p.block_tables + (int64_t)tseq * p.bt_stride;
         const uint64_t policy = l2_evict_first_policy();
-        int next = (lane < nblk) ? __ldg(bt_row + lane) : 0;
+        auto entry = [&](int i) -> int {           // the i-th block's table entry
+            if (i >= nblk)
+                return 0;
+            const int b = block_of(i);
+            return block_seen(b) ? __ldg(bt_row + b) : 0;
+        };
+        int next = entry(lane);
         bool aborted = false;
         // block-table entries 32 at a time (BPT divides 32, so no tile straddles two
         // batches), the next 32 in flight while the current ones are used
         for (int base = 0; base < nblk && !aborted; base += 32) {
             const int cur = next;
             if (base + 32 + lane < nblk)
-                next = __ldg(bt_row + base + 32 + lane);
+                next = entry(base + 32 + lane);
             const int cnt = min(32, nblk - base);
             for (int i = 0; i < cnt; i += BPT) {
                 int pbn[BPT];
@@ -321,6 +391,10 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                 for (int b = 0; b < BPT; ++b)
                     pbn[b] = __shfl_sync(kFullMask, cur, i + b);   // i + b <= 31
                 const int nb = min(BPT, cnt - i);                  // blocks of the tile in range
+                bool want[BPT];                                    // of those, the ones to read
+#pragma unroll
+                for (int b = 0; b < BPT; ++b)
+                    want[b] = b < nb && block_seen(block_of(base + i + b));
                 const int it = (base + i) / BPT;
                 const int stage = it % NSTAGE;
                 int ok = 1;
@@ -334,8 +408,8 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                         uint32_t tx = 0;
 #pragma unroll
                         for (int b = 0; b < BPT; ++b) {
-                            const bool valid = b < nb && pbn[b] >= 0 && (int64_t)pbn[b] < p.num_blocks;
-                            all_valid = all_valid && (b >= nb || valid);
+                            const bool valid = want[b] && pbn[b] >= 0 && (int64_t)pbn[b] < p.num_blocks;
+                            all_valid = all_valid && (!want[b] || valid);
                             tx += valid ? 2u * (kFp8 ? BS * D : BS * D * 2) : 0u;
                         }
                         stage_ok[stage] = all_valid ? 1 : 0;
@@ -348,7 +422,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                             mbar_arrive_expect_tx(&full[stage], tx);
 #pragma unroll
                             for (int b = 0; b < BPT; ++b) {
-                                if (b >= nb || pbn[b] < 0 || (int64_t)pbn[b] >= p.num_blocks)
+                                if (!want[b] || pbn[b] < 0 || (int64_t)pbn[b] >= p.num_blocks)
                                     continue;
                                 unsigned char* bdst = dst + b * (BS * 128);   // rows of block b
                                 if constexpr (kDirect) {
@@ -456,12 +530,24 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[kvh] * q_unscale : p.scale_log2;
     // chunk rows: the last visible position of rows 2c and 2c+1 (-1: padding row)
     int lim[2] = {0, 0};
+    // kMod: first visible position past the global tokens, the global tokens, base-2 slope
+    int low[2] = {0, 0}, glob[2] = {0, 0};
+    float slope[2] = {0.f, 0.f};
     if constexpr (CH) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int R = R0 + 2 * c + j;
             const int tk = R / p.group;
-            lim[j] = (2 * c + j < NH && tk < n) ? L - n + tk : -1;
+            const bool live = 2 * c + j < NH && tk < n;
+            lim[j] = !live ? -1 : (MODE == kPrefix || MODE == kSuffix) ? L - 1 : L - n + tk;
+            if constexpr (MODE == kMod) {
+                if (live) {
+                    low[j] = p.mods.window > 0 ? max(0, lim[j] - p.mods.window + 1) : 0;
+                    glob[j] = seen.glob;
+                    if (p.mods.slopes)
+                        slope[j] = p.mods.slopes[kvh * p.group + (R - tk * p.group)] * 1.4426950408889634f;
+                }
+            }
         }
     }
 
@@ -501,12 +587,15 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             kbase = smem_addr(smem + stage * Sm::kStageBytes);
             vbase = kbase + Sm::kTileBytes;
         }
-        const int nvalid = min(TB, t1 - (jb * BS + it * TB));
+        const int tb = tile_token(it);
+        const int nvalid = min(TB, t1 - tb);
 
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
             if (16 * mb >= nvalid)
                 break;                         // the rest of the tile lies past the context
+            if (MODE == kMod && !any_seen(seen, tb + 16 * mb, tb + 16 * mb + 16))
+                continue;                      // no row sees any of these 16 tokens
             // ---- S^T = K . Q^T for tokens 16mb .. 16mb+15
             float s[4] = {0.f, 0.f, 0.f, 0.f};
             if constexpr (kDirect) {
@@ -536,13 +625,26 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             // ---- online softmax: s[0], s[1] = token 16mb+g; s[2], s[3] = token 16mb+g+8
             const int tok_a = 16 * mb + g, tok_b = tok_a + 8;
             float x[4];
-            x[0] = tok_a < nvalid ? s[0] * sl2 : -INFINITY;
-            x[1] = tok_a < nvalid ? s[1] * sl2 : -INFINITY;
-            x[2] = tok_b < nvalid ? s[2] * sl2 : -INFINITY;
-            x[3] = tok_b < nvalid ? s[3] * sl2 : -INFINITY;
-            if constexpr (CH) {
+            if constexpr (MODE == kMod) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = j & 1, t = tb + (j < 2 ? tok_a : tok_b);
+                    x[j] = s[j] * sl2;
+                    if (p.mods.cap > 0.f)
+                        x[j] = cap_score(x[j], p.mods);
+                    x[j] = fmaf(-slope[r], (float)abs(lim[r] - t), x[j]);
+                    const bool sees = t < glob[r] || (t >= low[r] && t <= lim[r]);
+                    x[j] = sees ? x[j] : -INFINITY;
+                }
+            } else {
+                x[0] = tok_a < nvalid ? s[0] * sl2 : -INFINITY;
+                x[1] = tok_a < nvalid ? s[1] * sl2 : -INFINITY;
+                x[2] = tok_b < nvalid ? s[2] * sl2 : -INFINITY;
+                x[3] = tok_b < nvalid ? s[3] * sl2 : -INFINITY;
+            }
+            if constexpr (CH && MODE == kPlain) {
                 // causal within the chunk: token t is visible to a row at position >= t
-                const int abs_a = jb * BS + it * TB + tok_a, abs_b = abs_a + 8;
+                const int abs_a = tb + tok_a, abs_b = abs_a + 8;
                 x[0] = abs_a <= lim[0] ? x[0] : -INFINITY;
                 x[1] = abs_a <= lim[1] ? x[1] : -INFINITY;
                 x[2] = abs_b <= lim[0] ? x[2] : -INFINITY;
@@ -585,7 +687,13 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             const uint32_t bl0 = movmatrix_trans(lo_a), bl1 = movmatrix_trans(lo_b);
             // ---- O^T += V^T . P^T over tokens 16mb .. 16mb+15
             const int vr = 16 * mb + (lane & 7) + 8 * (lane >> 4);            // token row
-            const bool ragged = nvalid < 16 * (mb + 1);
+            bool ragged = nvalid < 16 * (mb + 1);
+            if constexpr (MODE == kMod)              // some of the 16 tokens are seen by no row
+                ragged = ragged || (tb + 16 * mb < seen.lo && tb + 16 * mb + 16 > seen.glob);
+            // token t of the tile is in range and seen
+            auto live_tok = [&](int t) -> bool {
+                return t < nvalid && (MODE != kMod || is_seen(seen, tb + t));
+            };
             uint32_t vpair[8];   // direct E4M3: the two m-blocks 2j, 2j+1 read together
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
@@ -633,9 +741,10 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                 if (ragged) {
                     // a0, a1 hold tokens 16mb + 2c, +1; a2, a3 tokens 16mb + 2c + 8, +9
                     const int t = 16 * mb + 2 * c;
-                    const uint32_t m01 = (t < nvalid ? 0x0000ffffu : 0u) | (t + 1 < nvalid ? 0xffff0000u : 0u);
-                    const uint32_t m23 = (t + 8 < nvalid ? 0x0000ffffu : 0u) |
-                                         (t + 9 < nvalid ? 0xffff0000u : 0u);
+                    const uint32_t m01 = (live_tok(t) ? 0x0000ffffu : 0u) |
+                                         (live_tok(t + 1) ? 0xffff0000u : 0u);
+                    const uint32_t m23 = (live_tok(t + 8) ? 0x0000ffffu : 0u) |
+                                         (live_tok(t + 9) ? 0xffff0000u : 0u);
                     a[0] &= m01;
                     a[1] &= m01;
                     a[2] &= m23;
@@ -712,7 +821,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             row = (int64_t)(qs0 + j) * p.num_q_heads + kvh * p.group + (R - j * p.group);
         }
         if (split) {
-            const int64_t prow = row * p.max_parts + part;
+            const int64_t prow = row * p.max_parts + (MODE == kSuffix ? p.part_base : 0) + part;
             p.part_o[prow * D + d] = out;
             if (d == 0) {
                 p.part_ml[prow * 2 + 0] = M;

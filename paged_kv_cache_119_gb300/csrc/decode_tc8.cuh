@@ -48,6 +48,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "score_mods.cuh"
 #include "tc_device.cuh"
 
 namespace pa {
@@ -180,7 +181,8 @@ __device__ __forceinline__ int sw128_byte(int row, int col)
 // (decode: R query heads of one kv head; CH: R (chunk token, head) rows of one kv head,
 // row R0 + r = token (R0 + r) / group, head (R0 + r) % group).
 // grid = (partitions, num_kv_heads * chunks, num_seqs); kTc8Threads threads.
-template <typename T, int BS, int R, int NST, bool CH>
+// MODE (with CH): as in decode_mma_kernel.
+template <typename T, int BS, int R, int NST, bool CH, int MODE = kPlain>
 __global__ void __launch_bounds__(kTc8Threads, 3)
     decode_tc8_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv)
@@ -214,13 +216,17 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
     const int kvh = blockIdx.y / p.chunks;
     const int R0 = (blockIdx.y - kvh * p.chunks) * R;
     const int part = blockIdx.x;
-    const bool split = p.partition_tokens > 0;
+    static_assert(MODE == kPlain || CH, "the other modes address rows as chunk rows");
+    const bool split = MODE == kPrefix || MODE == kSuffix || p.partition_tokens > 0;
 
-    const int L = p.context_lens[seq];
     int qs0 = 0, n = 1;
     if constexpr (CH) {
-        qs0 = p.query_start[seq];
-        n = p.query_start[seq + 1] - qs0;
+        if (MODE == kSuffix || (MODE == kMod && !p.query_start)) {
+            qs0 = seq;
+        } else {
+            qs0 = p.query_start[seq];
+            n = p.query_start[seq + 1] - qs0;
+        }
     }
     // the q / out row of CTA row r, or -1 for a padding row
     auto out_row = [&](int r) -> int64_t {
@@ -234,7 +240,26 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         }
     };
     const bool rows_sane = !CH || (qs0 >= 0 && n >= 0 && (int64_t)qs0 + n <= p.num_rows);
-    if (L < 0 || L > p.max_context_len || !rows_sane || (CH && (n > L || n > p.max_query_len))) {
+    // the sequence whose table row and lengths count: a group's first one (kPrefix)
+    const int tseq = MODE == kPrefix ? (rows_sane && n > 0 ? qs0 : 0) : seq;
+    int L, start = 0;                             // the tokens of this pass are start .. L - 1
+    bool bad_len;
+    if constexpr (MODE == kPrefix) {
+        L = p.prefix_lens[tseq];
+        bad_len = L < 0 || L > p.max_prefix_len || L % BS != 0 || n > p.max_query_len;
+    } else {
+        L = p.context_lens[seq];
+        bad_len = L < 0 || L > p.max_context_len || (CH && MODE != kSuffix && (n > L || n > p.max_query_len));
+        if constexpr (MODE == kSuffix) {
+            start = p.prefix_lens[seq];
+            bad_len = start < 0 || start > p.max_prefix_len || start % BS != 0 || start > L ||
+                      L > p.max_context_len ||
+                      L - start > p.max_suffix_len;
+        }
+        if (MODE == kMod && !p.query_start)
+            bad_len = L < 0 || L > p.max_context_len;      // an empty context is a zero row
+    }
+    if (bad_len || !rows_sane) {
         if (part == 0 && blockIdx.y == 0 && threadIdx.x == 0)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
         if (!split && rows_sane) {
@@ -247,22 +272,46 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         return;
     }
     int t_end = L;
+    Seen seen{0, 0, 0};
+    TileOrder order{0, 0, 0};
     if constexpr (CH) {
-        if (seq == p.num_seqs - 1 && part == 0 && blockIdx.y == 0 && threadIdx.x == 0 &&
-            (int64_t)qs0 + n != p.num_rows)
+        if (MODE != kSuffix && seq == (int)gridDim.z - 1 && part == 0 && blockIdx.y == 0 &&
+            threadIdx.x == 0 && (int64_t)qs0 + n != p.num_rows)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);   // rows after the last chunk belong to no one
         if (R0 / p.group >= n)
             return;                                // no chunk token in this row chunk
-        t_end = L - n + min(n - 1, (R0 + R - 1) / p.group) + 1;   // last row's position + 1
+        const int last = L - n + min(n - 1, (R0 + R - 1) / p.group);   // last row's position
+        if constexpr (MODE == kPlain)
+            t_end = last + 1;
+        if constexpr (MODE == kMod) {
+            seen = seen_by(p.mods, seq, L, L - n + R0 / p.group, last);
+            order = seen_tiles(seen, kTc8Tok);
+            t_end = seen.end;
+        }
     }
-    int t0 = 0, t1 = t_end;
-    if (split) {
-        t0 = part * p.partition_tokens;
-        if (t0 >= t_end)
+    int t0 = start, t1 = t_end;
+    int c0 = 0, ntiles = 0;                       // kMod: first tile of the list to read
+    if constexpr (MODE == kMod) {
+        c0 = split ? part * (p.partition_tokens / kTc8Tok) : 0;
+        if (split && c0 >= order.count)
             return;
-        t1 = min(t_end, t0 + p.partition_tokens);
+        ntiles = split ? min(order.count - c0, p.partition_tokens / kTc8Tok) : order.count;
+    } else {
+        if (p.partition_tokens > 0) {
+            t0 += part * p.partition_tokens;
+            if (t0 >= t_end)
+                return;
+            t1 = min(t_end, t0 + p.partition_tokens);
+        }
+        ntiles = (t1 - t0 + kTc8Tok - 1) / kTc8Tok;   // 0 only for an empty context
     }
-    const int ntiles = (t1 - t0 + kTc8Tok - 1) / kTc8Tok;   // 0 only for an empty context
+    // first token of tile it
+    auto tile_token = [&](int it) -> int {
+        if constexpr (MODE == kMod)
+            return order(c0 + it) * kTc8Tok;
+        else
+            return t0 + it * kTc8Tok;
+    };
 
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -303,27 +352,46 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         uint64_t* fullb = is_k ? kfull : vfull;
         uint64_t* emptyb = is_k ? kempty : vempty;
         const int half = is_k ? 0 : Sm::kTile;
-        const int32_t* bt_row = p.block_tables + (int64_t)seq * p.bt_stride;
+        const int32_t* bt_row = p.block_tables + (int64_t)tseq * p.bt_stride;
         const uint64_t policy = l2_evict_first_policy();
         const int blk_first = t0 / BS;             // partitions start on block boundaries
-        const int nblk = (t1 + BS - 1) / BS - blk_first;
+        const int nblk = MODE == kMod ? ntiles * BPT : (t1 + BS - 1) / BS - blk_first;
+        // whether the CTA's i-th block is to be read, and which block of the context it is:
+        // kMod reads (and checks) only blocks that hold a seen token
+        auto block_of = [&](int i) -> int {
+            if constexpr (MODE == kMod)
+                return order(c0 + i / BPT) * BPT + i % BPT;
+            else
+                return blk_first + i;
+        };
+        auto wanted = [&](int i) -> bool {
+            if (i >= nblk)
+                return false;
+            if constexpr (MODE == kMod) {
+                const int b = block_of(i);
+                return any_seen(seen, b * BS, min(b * BS + BS, t1));
+            }
+            return true;
+        };
+        auto entry = [&](int i) -> int { return wanted(i) ? __ldg(bt_row + block_of(i)) : -1; };
         // block-table entries 32 at a time (4 or 8 tiles), the next 32 in flight while the
         // current ones are used
-        int cur = lane < nblk ? __ldg(bt_row + blk_first + lane) : -1;
-        int nxt = 32 + lane < nblk ? __ldg(bt_row + blk_first + 32 + lane) : -1;
+        int cur = entry(lane);
+        int nxt = entry(32 + lane);
         int issued = 0;
         for (int it = 0; it < ntiles; ++it) {
             const int st = it % NST;
             const int lb = it * BPT;               // first block of the tile, CTA-relative
             if (it > 0 && (lb & 31) == 0) {
                 cur = nxt;
-                nxt = lb + 32 + lane < nblk ? __ldg(bt_row + blk_first + lb + 32 + lane) : -1;
+                nxt = entry(lb + 32 + lane);
             }
-            const int nb = min(BPT, nblk - lb);
             const int e = __shfl_sync(kFullMask, cur, ((lb & 31) + lane) & 31);
+            const bool want = lane < BPT && wanted(lb + lane);
+            const int nb = __popc(__ballot_sync(kFullMask, want));
             int pbn = -1;
             bool valid = false;
-            if (lane < nb) {
+            if (want) {
                 pbn = e;
                 valid = pbn >= 0 && (int64_t)pbn < p.num_blocks;
             }
@@ -438,13 +506,23 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         const int tl = 32 * wq + lane;               // TMEM lane: token of a tile / head dim
         int64_t orow[R];
         int lim[R];                                  // last visible position of row r (-1: none)
+        // kMod: first visible position past the global tokens, base-2 distance slope
+        int low[R];
+        float slope[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             orow[r] = out_row(r);
-            if constexpr (CH)
+            low[r] = 0;
+            slope[r] = 0.f;
+            if constexpr (CH && MODE != kPrefix && MODE != kSuffix)
                 lim[r] = orow[r] >= 0 ? L - n + (R0 + r) / p.group : -1;
             else
                 lim[r] = L - 1;
+            if constexpr (MODE == kMod) {
+                low[r] = p.mods.window > 0 ? max(0, lim[r] - p.mods.window + 1) : 0;
+                if (p.mods.slopes && orow[r] >= 0)
+                    slope[r] = p.mods.slopes[orow[r] % p.num_q_heads] * 1.4426950408889634f;
+            }
         }
         // ---- query terms into Qt: this thread is head dim tl of every row
         float mult[R];                               // score multiplier (base 2) per row
@@ -529,7 +607,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         for (int it = 0; it < ntiles; ++it) {
             const int b = it & 1;
             const int st = it % NST;
-            const int tb = t0 + it * kTc8Tok;
+            const int tb = tile_token(it);
             // the scores imply the tile's K (the K slot may already hold a later tile:
             // neither kfull nor any per-stage word is read here)
             if (!mbar_wait(&s_full[b], (it >> 1) & 1)) {
@@ -546,7 +624,16 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const float s = combine_terms(sv[4 * r], sv[4 * r + 1], sv[4 * r + 2], sv[4 * r + 3]);
-                x[r] = (pos < t1 && pos <= lim[r]) ? s * mult[r] : -INFINITY;
+                if constexpr (MODE == kMod) {
+                    x[r] = s * mult[r];
+                    if (p.mods.cap > 0.f)
+                        x[r] = cap_score(x[r], p.mods);
+                    x[r] = fmaf(-slope[r], (float)abs(lim[r] - pos), x[r]);
+                    const bool sees = orow[r] >= 0 && (pos < seen.glob || (pos >= low[r] && pos <= lim[r]));
+                    x[r] = sees ? x[r] : -INFINITY;
+                } else {
+                    x[r] = (pos < t1 && pos <= lim[r]) ? s * mult[r] : -INFINITY;
+                }
                 float wmx = x[r];
 #pragma unroll
                 for (int msk = 16; msk >= 1; msk >>= 1)
@@ -595,7 +682,8 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                     const int n = kTc8Terms * r + k;
                     pbuf[n * 128 + (tl ^ ((n & 7) << 4))] = (unsigned char)pt[r][k];
                 }
-            if (tb + kTc8Tok > t1) {
+            if (MODE == kMod ? (tb + kTc8Tok > t1 || (tb < seen.lo && tb + kTc8Tok > seen.glob))
+                             : tb + kTc8Tok > t1) {
                 // last tile: V rows of tokens past the range (unused slot, missing block,
                 // stale tile) become 0, once the tile's V is in (its slot is not reused
                 // before this tile's P.V)
@@ -607,7 +695,13 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                 }
                 // rows nv .. 127 are one contiguous span: the 128 threads zero it together,
                 // consecutive 16-byte stores (no bank conflicts)
-                const int nv = t1 - tb;                  // 1 .. 127 rows of the range
+                if constexpr (MODE == kMod) {            // rows of unseen tokens, anywhere
+                    uint4* vt = reinterpret_cast<uint4*>(smem + st * Sm::kStage + Sm::kTile);
+                    for (int j = tl; j < kTc8Tok * 8; j += kTc8Tok)
+                        if (!is_seen(seen, tb + j / 8))
+                            vt[j] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                const int nv = min(kTc8Tok, t1 - tb);    // rows of the range
                 uint4* vz = reinterpret_cast<uint4*>(smem + st * Sm::kStage + Sm::kTile + nv * 128);
                 for (int j = tl; j < (kTc8Tok - nv) * 8; j += kTc8Tok)
                     vz[j] = make_uint4(0u, 0u, 0u, 0u);
@@ -668,7 +762,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                 continue;                            // padding row
             const float out = bad ? __int_as_float(0x7fc00000) : acc_e[r];
             if (split) {
-                const int64_t prow = orow_e[r] * p.max_parts + part;
+                const int64_t prow = orow_e[r] * p.max_parts + (MODE == kSuffix ? p.part_base : 0) + part;
                 p.part_o[prow * D + tl] = out;
                 if (tl == 0) {
                     p.part_ml[prow * 2 + 0] = m_e[r];

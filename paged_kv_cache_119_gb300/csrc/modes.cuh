@@ -1,0 +1,34 @@
+// modes.cuh -- host launchers of the attention kernels in their other modes (modified
+// scores, shared prefix, suffix; AttnMode in pa_internal.h).  Each modes_*.cu instantiates
+// one kernel family.
+#pragma once
+
+#include "pa_internal.h"
+
+namespace pa {
+
+// Launches one kernel variant V (kernel(), configure(), smem_bytes, threads) over
+// (partitions, kv heads * chunks, sequences or groups).
+template <typename V, typename... Args>
+cudaError_t launch_mode_variant(dim3 grid, cudaStream_t stream, const Args&... args)
+{
+    cudaError_t err = V::configure();
+    if (err != cudaSuccess)
+        return err;
+    V::kernel()<<<grid, V::kThreads, V::kSmem, stream>>>(args...);
+    return cudaGetLastError();
+}
+
+// Resident CTAs per SM of variant V (0 if unknown).
+template <typename V>
+int occupancy_mode_variant()
+{
+    int n = 0;
+    if (V::configure() != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, V::kernel(), V::kThreads, V::kSmem) !=
+            cudaSuccess)
+        return 0;
+    return n;
+}
+
+}  // namespace pa

@@ -26,6 +26,25 @@ constexpr int kMmaMinHeadsFp8 = 4;
 // Partition length the automatic split uses (a multiple of every block size).
 constexpr int kAutoPartitionTokens = 512;
 
+// What an attention kernel computes, a template parameter of each:
+//   kPlain   the causal softmax attention of pa_decode / pa_chunk_attention
+//   kMod     the same with modified scores (ScoreMods)
+//   kPrefix  shared-prefix pass: the rows of a group of sequences (query_start = the
+//            group's first sequence) attend over the tokens they share, no causal limit;
+//            writes partial rows only
+//   kSuffix  each sequence's own tokens after its shared prefix; writes partial rows only
+enum AttnMode : int { kPlain = 0, kMod = 1, kPrefix = 2, kSuffix = 3 };
+
+// Modified scores (score_mods.cuh), in base-2 units.
+struct ScoreMods {
+    const float* slopes;         // DEVICE [Hq] distance slopes, or null
+    const int32_t* global_lens;  // DEVICE [S] tokens every row sees, or null
+    float cap;                   // softcap * log2 e; 0: no cap
+    float inv_cap;               // 1 / cap
+    int window;                  // 0: none
+    int max_global;              // host bound: longer global_lens count as this
+};
+
 struct DecodeParams {
     void* out;
     const void* q;
@@ -62,6 +81,15 @@ struct DecodeParams {
     // issues no copy and waits fault_wait_ns at most, so its bounded waits give up
     int fault_cta;
     uint32_t fault_wait_ns;
+    ScoreMods mods;              // kMod
+    // kPrefix / kSuffix: shared tokens of each sequence, and the first partial-row index
+    // of this pass among the row's max_parts (gridDim.x of them)
+    const int32_t* prefix_lens;
+    int max_prefix_len;
+    int max_suffix_len;
+    int part_base;
+    int tile_align;              // merge of the shared prefix: block_size
+    int rows_per_cta;            // kMod: (token, head) rows of a kv head one CTA serves
 };
 
 // Longest-first dispatch of a one-pass CUDA-core decode with more CTAs than one wave:
@@ -257,6 +285,8 @@ struct ChunkParams {
     int max_parts;
     int out_f32;
     float scale_log2;
+    ScoreMods mods;              // kMod
+    const int32_t* prefix_lens;  // kPrefix: shared tokens of each sequence
 };
 cudaError_t launch_chunk_attention(const ChunkParams& p, pa_dtype dtype, int head_dim,
                                    int block_size, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -291,6 +321,58 @@ cudaError_t launch_chunk_rows_tc8(const DecodeParams& p, const ChunkParams& cp, 
                                   int block_size, int rows, const CUtensorMap& tk,
                                   const CUtensorMap& tv, cudaStream_t stream);
 int occupancy_chunk_rows_tc8(pa_dtype q_dtype, int block_size, int rows);
+
+// The other modes of the attention kernels (modes_*.cu); grid = (partitions, kv heads *
+// chunks, sequences or groups).  decode_kernel, kMod and kSuffix:
+cudaError_t launch_core_mode(const DecodeParams& p, AttnMode mode, pa_dtype q_dtype, pa_dtype kv_dtype,
+                             int head_dim, int block_size, int gc, dim3 grid, cudaStream_t stream);
+int occupancy_core_mode(AttnMode mode, pa_dtype q_dtype, pa_dtype kv_dtype, int head_dim, int block_size,
+                        int gc);
+// decode_mma_kernel, nh (4 or 8) rows per CTA:
+cudaError_t launch_rows_f16(const DecodeParams& p, AttnMode mode, int head_dim, int block_size,
+                       int nh, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+                       cudaStream_t stream);
+int occupancy_rows_f16(AttnMode mode, int head_dim, int block_size, int nh);
+cudaError_t launch_rows_bf16(const DecodeParams& p, AttnMode mode, int head_dim, int block_size,
+                       int nh, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+                       cudaStream_t stream);
+int occupancy_rows_bf16(AttnMode mode, int head_dim, int block_size, int nh);
+cudaError_t launch_rows_f16_fp8(const DecodeParams& p, AttnMode mode, int head_dim, int block_size,
+                       int nh, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+                       cudaStream_t stream);
+int occupancy_rows_f16_fp8(AttnMode mode, int head_dim, int block_size, int nh);
+cudaError_t launch_rows_bf16_fp8(const DecodeParams& p, AttnMode mode, int head_dim, int block_size,
+                       int nh, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+                       cudaStream_t stream);
+int occupancy_rows_bf16_fp8(AttnMode mode, int head_dim, int block_size, int nh);
+// decode_tc8_kernel (E4M3, head_dim 128), 1, 2 or 4 rows per CTA:
+cudaError_t launch_tc8_mode(const DecodeParams& p, AttnMode mode, pa_dtype q_dtype, int block_size,
+                            int rows, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+                            cudaStream_t stream);
+int occupancy_tc8_mode(AttnMode mode, pa_dtype q_dtype, int block_size, int rows);
+// chunk_attn_kernel, kMod and kPrefix:
+cudaError_t launch_chunk_f16(const ChunkParams& p, AttnMode mode, int head_dim, int block_size,
+                       const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+                       cudaStream_t stream);
+int occupancy_chunk_f16(AttnMode mode, int head_dim, int block_size);
+cudaError_t launch_chunk_bf16(const ChunkParams& p, AttnMode mode, int head_dim, int block_size,
+                       const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+                       cudaStream_t stream);
+int occupancy_chunk_bf16(AttnMode mode, int head_dim, int block_size);
+cudaError_t launch_chunk_f16_fp8(const ChunkParams& p, AttnMode mode, int head_dim, int block_size,
+                       const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+                       cudaStream_t stream);
+int occupancy_chunk_f16_fp8(AttnMode mode, int head_dim, int block_size);
+cudaError_t launch_chunk_bf16_fp8(const ChunkParams& p, AttnMode mode, int head_dim, int block_size,
+                       const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+                       cudaStream_t stream);
+int occupancy_chunk_bf16_fp8(AttnMode mode, int head_dim, int block_size);
+// Merges of their partial rows (attn_merge.cuh).
+cudaError_t launch_mod_merge(const DecodeParams& p, pa_dtype q_dtype, int head_dim, int64_t rows,
+                             int tile_tokens, cudaStream_t stream);
+cudaError_t launch_prefix_merge(const DecodeParams& p, pa_dtype q_dtype, int head_dim,
+                                const int32_t* group_start, int num_groups, int max_group,
+                                int prefix_part, cudaStream_t stream);
 
 // Sets the dynamic shared-memory limit of a kernel once per device and process.
 inline cudaError_t configure_once(const void* kernel, int smem_bytes)
