@@ -169,6 +169,53 @@ __device__ __forceinline__ float max3f(float a, float b, float c)
     return r;
 }
 
+// Largest of a row's 64 scores.
+__device__ __forceinline__ float row_max(const float (&s)[kChunkTileTok])
+{
+    float mx[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        mx[i] = s[i];
+#pragma unroll
+    for (int c = 8; c + 16 <= kChunkTileTok; c += 16)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            mx[i] = max3f(mx[i], s[c + i], s[c + 8 + i]);
+#pragma unroll
+    for (int c = 8 + (kChunkTileTok - 8) / 16 * 16; c < kChunkTileTok; ++c)
+        mx[c & 7] = fmaxf(mx[c & 7], s[c]);
+    return max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+}
+
+__device__ __forceinline__ float min3f(float a, float b, float c)
+{
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Smallest (x) and largest (y) of a row's 64 scores.
+__device__ __forceinline__ float2 row_range(const float (&s)[kChunkTileTok])
+{
+    float lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        lo[i] = hi[i] = s[i];
+#pragma unroll
+    for (int c = 4; c + 8 <= kChunkTileTok; c += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = max3f(hi[i], s[c + i], s[c + 4 + i]);
+            lo[i] = min3f(lo[i], s[c + i], s[c + 4 + i]);
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        hi[i] = fmaxf(hi[i], s[kChunkTileTok - 4 + i]);
+        lo[i] = fminf(lo[i], s[kChunkTileTok - 4 + i]);
+    }
+    return make_float2(min3f(fminf(lo[0], lo[1]), lo[2], lo[3]), max3f(fmaxf(hi[0], hi[1]), hi[2], hi[3]));
+}
+
 // grid = (partitions, num_kv_heads * m_tiles, num_seqs); kChunkThreads threads over
 // f16 caches, kChunkThreadsConv over E4M3 (NRAW > 0) and bf16 caches.  T: query /
 // native output type.  Over E4M3 caches (value = code * per-kv-head scale) the
@@ -675,6 +722,20 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         if (lane == 0)
             mbar_arrive(q_full);
 
+        // Capped scores, fast form: for |y| <= 1/2, y = s kk, tanh y = y P(y^2) with the
+        // four-term P below (relative error at most 5.5e-7 there, the Chebyshev-like best fit;
+        // the probabilities are rounded to f16, 2^-11, right after), so the score is
+        // s (kp0 + kp1 s^2 + kp2 s^4 + kp3 s^6): three packed multiply-adds more than an
+        // uncapped score, and no MUFU work beyond its one exp2.  Taken by a warp's tile that
+        // all its rows see whole and whose scores lie in that range; other tiles take
+        // cap_score.  kk outside [10^-6, 8] would take kp3 out of fp32's normal range.
+        const float kk = MODE == kMod ? sl2 * p.mods.inv_cap : 0.f;
+        const bool cap_fast = MODE == kMod && p.mods.cap > 0.f && !p.mods.slopes &&
+                              __all_sync(kFullMask, kk >= 1e-6f && kk <= 8.f);
+        const float k2 = kk * kk;
+        const float kp[4] = {0.99999946f * sl2, -0.33326318f * sl2 * k2, 0.13190297f * sl2 * k2 * k2,
+                             -0.04440223f * sl2 * k2 * k2 * k2};
+        auto poly_at = [&](float z) { return fmaf(fmaf(fmaf(kp[3], z, kp[2]), z, kp[1]), z, kp[0]); };
         const bool warp_live = __any_sync(kFullMask, row_valid);
         const uint32_t lane_t = tbase + ((uint32_t)(32 * wq) << 16);
         const uint32_t o_col = lane_t + q * 128;
@@ -701,49 +762,67 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 tmem_ld64(sp_col, s);
             if (warp_live) {
                 const int lim = row_valid ? pos - tb : -1;   // columns c <= lim are visible
+                float mul = sl2;                 // scores are s * mul (base 2), or, capped, the
+                bool poly = false;               // polynomial of s below
+                float smax;
                 if constexpr (MODE == kMod) {
-                    // from here on s holds the modified scores in base-2 units
+                    // column c is visible when c < gl, or lo <= c <= lim (rows past the
+                    // chunk are all zeros and never stored: let them see everything)
+                    const int gl = seen.glob - tb, lo = low - tb;
+                    const bool whole = __all_sync(
+                        kFullMask, !row_valid || gl >= NT || (lim >= NT - 1 && lo <= 0));
+                    if (whole && cap_fast) {
+                        const float2 mm = row_range(s);
+                        smax = mm.y;
+                        poly = __all_sync(kFullMask, fmaxf(fabsf(mm.x), fabsf(mm.y)) * kk <= 0.5f);
+                    }
+                    if (!poly) {
+                        if (p.mods.cap > 0.f) {
+                            mul = 1.f;
 #pragma unroll
-                    for (int c = 0; c < NT; ++c)
-                        s[c] *= sl2;
-                    if (p.mods.cap > 0.f) {
+                            for (int c = 0; c < NT; ++c)
+                                s[c] = cap_score(s[c] * sl2, p.mods);
+                        }
+                        if (p.mods.slopes) {
+                            // |pos - t| = pos - t while no column lies behind pos
+                            const float far0 = (float)(pos - tb);
+                            if (lim >= NT - 1 || !row_valid) {
+                                const float2 base = make_float2(-slope * far0, -slope * far0);
+#pragma unroll
+                                for (int c = 0; c < NT; c += 2) {
+                                    const float2 d = ffma2(make_float2(slope, slope),
+                                                           make_float2((float)c, (float)(c + 1)), base);
+                                    const float2 x = ffma2(make_float2(s[c], s[c + 1]),
+                                                           make_float2(mul, mul), d);
+                                    s[c] = x.x;
+                                    s[c + 1] = x.y;
+                                }
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < NT; ++c)
+                                    s[c] = fmaf(-slope, fabsf(far0 - (float)c), s[c] * mul);
+                            }
+                            mul = 1.f;
+                        }
+                        if (!whole) {
+                            const int g0 = row_valid ? gl : NT;
+#pragma unroll
+                            for (int c = 0; c < NT; ++c)
+                                s[c] = (c < g0 || (c >= lo && c <= lim)) ? s[c] : -INFINITY;
+                        }
+                        smax = row_max(s);
+                    }
+                } else {
+                    if (lim < NT - 1) {
 #pragma unroll
                         for (int c = 0; c < NT; ++c)
-                            s[c] = cap_score(s[c], p.mods);
+                            s[c] = c <= lim ? s[c] : -INFINITY;
                     }
-                    if (p.mods.slopes) {
-#pragma unroll
-                        for (int c = 0; c < NT; ++c)
-                            s[c] = fmaf(-slope, (float)abs(pos - tb - c), s[c]);
-                    }
-                    // column c is visible when c < gl, or lo <= c <= lim
-                    const int gl = row_valid ? seen.glob - tb : 0, lo = low - tb;
-                    if (gl < NT && (lim < NT - 1 || lo > 0)) {
-#pragma unroll
-                        for (int c = 0; c < NT; ++c)
-                            s[c] = (c < gl || (c >= lo && c <= lim)) ? s[c] : -INFINITY;
-                    }
-                } else if (lim < NT - 1) {
-#pragma unroll
-                    for (int c = 0; c < NT; ++c)
-                        s[c] = c <= lim ? s[c] : -INFINITY;
+                    smax = row_max(s);
                 }
-                float mx[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    mx[i] = s[i];
-#pragma unroll
-                for (int c = 8; c + 16 <= NT; c += 16)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mx[i] = max3f(mx[i], s[c + i], s[c + 8 + i]);
-#pragma unroll
-                for (int c = 8 + (NT - 8) / 16 * 16; c < NT; ++c)
-                    mx[c & 7] = fmaxf(mx[c & 7], s[c]);
-                const float smax = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]),
-                                         fmaxf(mx[6], mx[7]));
-                const float mul = MODE == kMod ? 1.f : sl2;
-                const float tmax = smax == -INFINITY ? -INFINITY : smax * mul;
+                float tmax = smax == -INFINITY ? -INFINITY : smax * mul;
+                if (MODE == kMod && poly)
+                    tmax = smax * poly_at(smax * smax);
                 const bool need = tmax > m_ref + 8.f;
                 if (it > 0 && __any_sync(kFullMask, need)) {
                     // O holds P.V of tiles 0 .. it-1: wait for the last, then rescale the
@@ -779,8 +858,14 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                                  make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < NT; c += 2) {
-                    const float2 x = ffma2(make_float2(s[c], s[c + 1]), make_float2(mul, mul),
-                                           make_float2(nm, nm));
+                    float2 f = make_float2(mul, mul);
+                    if (MODE == kMod && poly) {
+                        const float2 z = fmul2(make_float2(s[c], s[c + 1]), make_float2(s[c], s[c + 1]));
+                        f = ffma2(z, make_float2(kp[3], kp[3]), make_float2(kp[2], kp[2]));
+                        f = ffma2(z, f, make_float2(kp[1], kp[1]));
+                        f = ffma2(z, f, make_float2(kp[0], kp[0]));
+                    }
+                    const float2 x = ffma2(make_float2(s[c], s[c + 1]), f, make_float2(nm, nm));
                     s[c] = ex2_approx(x.x);
                     s[c + 1] = ex2_approx(x.y);
                     acc[(c >> 1) & 3] = ffma2(make_float2(s[c], s[c + 1]), make_float2(1.f, 1.f),
