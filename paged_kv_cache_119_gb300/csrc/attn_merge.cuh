@@ -3,65 +3,129 @@
 //   M = max m_k,  w_k = 2^(m_k - M) l_k,  o = sum w_k o_k / sum w_k.
 // A part that saw no visible token has m = -inf and weighs nothing; a poisoned part is NaN
 // and makes the row NaN; no visible token at all gives 0.
+//
+// Bound: reading the parts (a few MB that the passes have just left in L2), so latency.  One
+// warp per (row, head): its lanes read the (m, l) of 32 parts at once and a 16-byte piece of
+// the row each, four parts in flight; the sequence or group that owns the row is found by a
+// 33-way search of all lanes.  (One CTA per row with a serial search and serial (m, l) reads
+// took 15.6 us for 6144 rows of 14 parts and 8.7 us for 4096 rows of 2; this form is in the
+// table of the design notes.)
 #pragma once
 
 #include "decode_kernel.cuh"
 
 namespace pa {
 
+constexpr int kMergeWarps = 8;
 
-// Head dim d of the merged row: parts first .. first + count - 1 of ml [part][2] and
-// po [part][D], then count2 parts from second on.
-template <int D>
-__device__ __forceinline__ float merge_parts(const float* ml, const float* po, int first, int count,
-                                             int second, int count2)
+// The largest i in [0, n) with start[i] <= x (0 when there is none); start non-decreasing.
+// All lanes of a warp call it together.
+__device__ __forceinline__ int owner_of(const int32_t* start, int n, int64_t x, int lane)
 {
-    float M = -INFINITY;
-    for (int k = 0; k < count + count2; ++k)
-        M = fmaxf(M, ml[2 * (k < count ? first + k : second + k - count)]);
-    float num = 0.f, den = 0.f;
-    for (int k = 0; k < count + count2; ++k) {
-        const int i = k < count ? first + k : second + k - count;
-        const float mk = ml[2 * i];
-        const float w = mk == -INFINITY ? 0.f : exp2f(mk - M) * ml[2 * i + 1];
-        num = fmaf(w, po[(int64_t)i * D], num);
-        den += w;
+    int lo = 0, hi = n;                            // the answer is in [lo, hi)
+    while (hi - lo > 1) {
+        const int span = hi - lo;
+        const int at = span <= 32 ? lo + lane : lo + (int)((int64_t)span * (lane + 1) / 33);
+        const bool le = at < hi && start[at] <= x;
+        const int c = __popc(__ballot_sync(kFullMask, le));   // probes at or below the answer
+        if (span <= 32)
+            return max(lo, lo + c - 1);
+        const int next = c == 32 ? hi : lo + (int)((int64_t)span * (c + 1) / 33);
+        if (c > 0)
+            lo = lo + (int)((int64_t)span * c / 33);
+        hi = next;
     }
-    return den > 0.f ? num / den : (den == 0.f ? 0.f : __int_as_float(0x7fc00000));
+    return lo;
 }
 
-// Modified scores: one CTA of D threads per (query row, query head); grid = (rows, Hq).
-// tile_tokens: the tile the launch cut its list of tiles in; p.rows_per_cta as launched.
-template <typename T, int D>
-__global__ void __launch_bounds__(D) mod_reduce_kernel(const DecodeParams p, int tile_tokens)
+// Head dims of a row one lane holds.
+template <int D>
+struct RowPiece {
+    static constexpr int E = D / 32;
+    float f[E];
+};
+
+// This lane's piece of the merged row: parts 0 .. count - 1 and second .. second + count2 - 1
+// of ml [part][2] and po [part][D].
+template <int D>
+__device__ __forceinline__ RowPiece<D> merge_parts(const float* ml, const float* po, int count,
+                                                   int second, int count2, int lane)
 {
-    const int64_t row = blockIdx.x;
-    const int h = blockIdx.y;
-    const int d = threadIdx.x;
+    constexpr int E = RowPiece<D>::E;
+    const int n = count + count2;
+    auto part = [&](int k) { return k < count ? k : second + k - count; };
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32)
+        M = fmaxf(M, ml[2 * part(k)]);
+#pragma unroll
+    for (int msk = 16; msk >= 1; msk >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(kFullMask, M, msk));
+    RowPiece<D> num;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        num.f[e] = 0.f;
+    float den = 0.f;
+    for (int base = 0; base < n; base += 32) {
+        float w = 0.f;
+        if (base + lane < n) {
+            const float2 v = *reinterpret_cast<const float2*>(ml + 2 * part(base + lane));
+            w = v.x == -INFINITY ? 0.f : exp2f(v.x - M) * v.y;
+        }
+        den += w;
+        const int m = min(32, n - base);
+#pragma unroll 4
+        for (int k = 0; k < m; ++k) {
+            const float wk = __shfl_sync(kFullMask, w, k);
+            float o[E];
+            Load<float, E>::run(po + (int64_t)part(base + k) * D + lane * E, o);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                num.f[e] = fmaf(wk, o[e], num.f[e]);
+        }
+    }
+#pragma unroll
+    for (int msk = 16; msk >= 1; msk >>= 1)
+        den += __shfl_xor_sync(kFullMask, den, msk);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        num.f[e] = den > 0.f ? num.f[e] / den : (den == 0.f ? 0.f : __int_as_float(0x7fc00000));
+    return num;
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void store_piece(const DecodeParams& p, int64_t out_row, const RowPiece<D>& r,
+                                            bool nan_out, int lane)
+{
+#pragma unroll
+    for (int e = 0; e < RowPiece<D>::E; ++e)
+        store_out<T>(p, out_row * D + lane * RowPiece<D>::E + e,
+                     nan_out ? __int_as_float(0x7fc00000) : r.f[e]);
+}
+
+// Modified scores: one warp per (query row, query head), head fastest.  tile_tokens: the tile
+// the launch cut its list of tiles in; p.rows_per_cta as launched.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) mod_reduce_kernel(const DecodeParams p, int tile_tokens)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t out_row = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    if (out_row >= p.num_rows * p.num_q_heads)
+        return;
+    const int64_t row = out_row / p.num_q_heads;
+    const int h = (int)(out_row - row * p.num_q_heads);
     int s = (int)row, qs0 = (int)row, n = 1;
     if (p.query_start) {
-        // the sequence owning the row: query_start[s] <= row < query_start[s + 1]
-        int lo = 0, hi = p.num_seqs;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (p.query_start[mid] <= row)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        s = lo;
+        s = owner_of(p.query_start, p.num_seqs, row, lane);
         qs0 = p.query_start[s];
         n = p.query_start[s + 1] - qs0;
     }
     const int L = p.context_lens[s];
-    const int64_t out_row = row * p.num_q_heads + h;
     const bool bad = L < 0 || L > p.max_context_len ||
                      (p.query_start && (row < qs0 || row >= (int64_t)qs0 + n || n > L ||
                                         n > p.max_query_len));
-    float out;
+    RowPiece<D> out{};
     if (bad) {
-        out = __int_as_float(0x7fc00000);
-        if (d == 0 && h == 0)
+        if (lane == 0 && h == 0)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
     } else {
         // the rows of the CTA that served this one decide which tiles it read
@@ -71,47 +135,38 @@ __global__ void __launch_bounds__(D) mod_reduce_kernel(const DecodeParams p, int
         const TileOrder t =
             seen_tiles(seen_by(p.mods, s, L, L - n + R0 / p.group, L - n + last), tile_tokens);
         const int per = p.partition_tokens / tile_tokens;
-        out = merge_parts<D>(p.part_ml + out_row * p.max_parts * 2,
-                             p.part_o + out_row * p.max_parts * D + d, 0, (t.count + per - 1) / per, 0, 0);
+        out = merge_parts<D>(p.part_ml + out_row * p.max_parts * 2, p.part_o + out_row * p.max_parts * D,
+                             (t.count + per - 1) / per, 0, 0, lane);
     }
-    store_out<T>(p, out_row * D + d, out);
+    store_piece<T, D>(p, out_row, out, bad, lane);
 }
 
-// Shared prefix: one CTA of D threads per (sequence, query head); grid = (sequences, Hq).
-// The prefix pass wrote parts 0 .. of partitions of prefix_part tokens (0: one part), the
-// suffix pass parts p.part_base .. of p.partition_tokens.  Checks what the two passes could
-// not see together: every sequence belongs to exactly one group, of at most max_group
-// sequences, whose members agree on the length they share.
+// Shared prefix: one warp per (sequence, query head), head fastest.  The prefix pass wrote
+// parts 0 .. of partitions of prefix_part tokens (0: one part), the suffix pass parts
+// p.part_base .. of p.partition_tokens.  Checks what the two passes could not see together:
+// every sequence belongs to exactly one group, of at most max_group sequences, whose members
+// agree on the length they share.
 template <typename T, int D>
-__global__ void __launch_bounds__(D)
+__global__ void __launch_bounds__(32 * kMergeWarps)
     prefix_reduce_kernel(const DecodeParams p, const int32_t* group_start, int num_groups,
                          int max_group, int prefix_part)
 {
-    const int s = blockIdx.x;
-    const int h = blockIdx.y;
-    const int d = threadIdx.x;
-    // the group owning s: group_start[g] <= s < group_start[g + 1]
-    int lo = 0, hi = num_groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (group_start[mid] <= s)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    const int g0 = group_start[lo], g1 = group_start[lo + 1];
+    const int lane = threadIdx.x & 31;
+    const int64_t out_row = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    if (out_row >= (int64_t)p.num_seqs * p.num_q_heads)
+        return;
+    const int s = (int)(out_row / p.num_q_heads);
+    const int g = owner_of(group_start, num_groups, s, lane);
+    const int g0 = group_start[g], g1 = group_start[g + 1];
     const int L = p.context_lens[s];
     const int P = p.prefix_lens[s];
     const bool in_group = g0 >= 0 && g0 <= s && s < g1 && g1 <= p.num_seqs && g1 - g0 <= max_group;
-    const bool bad = !in_group || P < 0 || P > p.max_prefix_len || L < P ||
-                     L > p.max_context_len ||
+    const bool bad = !in_group || P < 0 || P > p.max_prefix_len || L < P || L > p.max_context_len ||
                      L - P > p.max_suffix_len || p.prefix_lens[in_group ? g0 : s] != P ||
                      P % p.tile_align != 0;
-    const int64_t out_row = (int64_t)s * p.num_q_heads + h;
-    float out;
+    RowPiece<D> out{};
     if (bad) {
-        out = __int_as_float(0x7fc00000);
-        if (d == 0 && h == 0)
+        if (lane == 0 && out_row == (int64_t)s * p.num_q_heads)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
     } else {
         const int npre = P == 0 ? 0 : (prefix_part > 0 ? (P + prefix_part - 1) / prefix_part : 1);
@@ -120,10 +175,10 @@ __global__ void __launch_bounds__(D)
                                   : (p.partition_tokens > 0
                                          ? (own + p.partition_tokens - 1) / p.partition_tokens
                                          : 1);
-        out = merge_parts<D>(p.part_ml + out_row * p.max_parts * 2,
-                             p.part_o + out_row * p.max_parts * D + d, 0, npre, p.part_base, nsuf);
+        out = merge_parts<D>(p.part_ml + out_row * p.max_parts * 2, p.part_o + out_row * p.max_parts * D,
+                             npre, p.part_base, nsuf, lane);
     }
-    store_out<T>(p, out_row * D + d, out);
+    store_piece<T, D>(p, out_row, out, bad, lane);
 }
 
 }  // namespace pa

@@ -400,7 +400,7 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
     e = launch(s, kMod, pl, d, c, tk, tv,
                dim3(d.max_parts, s.num_kv_heads * pl.chunks, num_seqs), st);
     if (e == cudaSuccess && pl.partition > 0)
-        e = launch_mod_merge(d, s.q_dtype, s.head_dim, num_query_tokens, pl.tile, st);
+        e = launch_mod_merge(d, s.q_dtype, s.head_dim, pl.tile, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

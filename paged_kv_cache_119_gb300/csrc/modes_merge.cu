@@ -24,12 +24,15 @@ cudaError_t by_type(pa_dtype q_dtype, int head_dim, F&& f)
 
 }  // namespace
 
-cudaError_t launch_mod_merge(const DecodeParams& p, pa_dtype q_dtype, int head_dim, int64_t rows,
-                             int tile_tokens, cudaStream_t stream)
+cudaError_t launch_mod_merge(const DecodeParams& p, pa_dtype q_dtype, int head_dim, int tile_tokens,
+                             cudaStream_t stream)
 {
+    const int64_t ctas = (p.num_rows * p.num_q_heads + kMergeWarps - 1) / kMergeWarps;
+    if (ctas > INT32_MAX)
+        return cudaErrorInvalidValue;
     return by_type<true>(q_dtype, head_dim, [&](auto t, auto d) {
         mod_reduce_kernel<decltype(t), d.value>
-            <<<dim3((unsigned)rows, p.num_q_heads), d.value, 0, stream>>>(p, tile_tokens);
+            <<<(unsigned)ctas, 32 * kMergeWarps, 0, stream>>>(p, tile_tokens);
         return cudaGetLastError();
     });
 }
@@ -38,9 +41,10 @@ cudaError_t launch_prefix_merge(const DecodeParams& p, pa_dtype q_dtype, int hea
                                 const int32_t* group_start, int num_groups, int max_group,
                                 int prefix_part, cudaStream_t stream)
 {
+    const int64_t ctas = ((int64_t)p.num_seqs * p.num_q_heads + kMergeWarps - 1) / kMergeWarps;
     return by_type<false>(q_dtype, head_dim, [&](auto t, auto d) {
         prefix_reduce_kernel<decltype(t), d.value>
-            <<<dim3((unsigned)p.num_seqs, p.num_q_heads), d.value, 0, stream>>>(
+            <<<(unsigned)ctas, 32 * kMergeWarps, 0, stream>>>(
                 p, group_start, num_groups, max_group, prefix_part);
         return cudaGetLastError();
     });

@@ -368,8 +368,8 @@ cudaError_t launch_chunk_bf16_fp8(const ChunkParams& p, AttnMode mode, int head_
                        cudaStream_t stream);
 int occupancy_chunk_bf16_fp8(AttnMode mode, int head_dim, int block_size);
 // Merges of their partial rows (attn_merge.cuh).
-cudaError_t launch_mod_merge(const DecodeParams& p, pa_dtype q_dtype, int head_dim, int64_t rows,
-                             int tile_tokens, cudaStream_t stream);
+cudaError_t launch_mod_merge(const DecodeParams& p, pa_dtype q_dtype, int head_dim, int tile_tokens,
+                             cudaStream_t stream);
 cudaError_t launch_prefix_merge(const DecodeParams& p, pa_dtype q_dtype, int head_dim,
                                 const int32_t* group_start, int num_groups, int max_group,
                                 int prefix_part, cudaStream_t stream);
