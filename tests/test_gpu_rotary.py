@@ -253,3 +253,29 @@ def test_same_as_reshape_where_nothing_turns():
                           P.pa_rotary_frequencies(128))
     P.pa_reshape_and_cache(k, v, a[2], a[3], st)
     assert torch.equal(a[0], a[2]) and torch.equal(a[1], a[3]) and torch.equal(qo, q)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_codes_are_those_of_the_plain_cache_write(dtype):
+    """V's codes, and K's where nothing turns, are pa_reshape_and_cache_fp8's bit for bit: the
+    fp32 quotient is the one IEEE division gives, for values over the whole range of the type
+    and scales from ordinary to extreme."""
+    T, Hkv, D = 512, 12, 128
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x = torch.randn((T, Hkv, D), generator=g, device="cuda") * 8
+    span = 15.0 if dtype == torch.float16 else 126.0
+    x[::2] *= torch.exp2((torch.rand((T // 2, Hkv, D), generator=g, device="cuda") * 2 - 1) * span)
+    x = x.to(dtype)
+    x[5, 0, :4] = torch.tensor([float("inf"), float("-inf"), float("nan"), 0.0], device="cuda")
+    y = x.flip(0).contiguous()
+    scale = torch.tensor([0.013, 1.0, 0.02, 3.7e-3, 448.0, 1e-20, 1e20, 2.0 ** -120, 2.0 ** 120, 1e-44, 0.0,
+                          -0.5], device="cuda")
+    slots = torch.randperm(T, generator=g, device="cuda")
+    pools = [torch.zeros((T // 16, Hkv, 16, D), device="cuda", dtype=torch.uint8) for _ in range(4)]
+    P.pa_rotary_and_cache_fp8(torch.empty_like(x), x, x, y, pools[0], pools[1], slots,
+                              torch.zeros(T, dtype=torch.int32, device="cuda"), [0.0] * 64, scale, scale)
+    P.pa_reshape_and_cache_fp8(x, y, pools[2], pools[3], slots, scale, scale)
+    assert torch.equal(pools[1], pools[3])
+    # turning by nothing leaves every finite value; an infinity meets 0 * inf = NaN
+    keep = torch.isfinite(x.float()).all(-1)[slots.argsort()].view(T // 16, 16, Hkv).transpose(1, 2)
+    assert torch.equal(pools[0][keep], pools[2][keep])
