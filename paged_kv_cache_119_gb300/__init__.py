@@ -34,5 +34,6 @@ __all__ = list(_API) + ["workloads", "build"]
 def __getattr__(name):
     if name in _API:
         from . import api
-        return getattr(api, name)
+        globals()[name] = fn = getattr(api, name)   # found at once the next time
+        return fn
     raise AttributeError(name)

@@ -25,14 +25,21 @@ def _dtype(t: torch.Tensor) -> int:
 
 
 def _cuda(name: str, t: torch.Tensor) -> None:
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
+# The current stream's handle without the Stream object that torch.cuda.current_stream()
+# builds around it (3 us a call on the GPU host, a tenth of this).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -174,34 +181,35 @@ def pa_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str =
     return out
 
 
-def _rows(name: str, t: torch.Tensor) -> None:
-    """A CUDA tensor [T, H, D] whose token rows [H, D] are dense (the token stride is free)."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+def _rows(name: str, t: torch.Tensor) -> int:
+    """Checks a CUDA tensor [T, H, D] whose token rows [H, D] are dense (the token stride is
+    free); returns that stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or (t.shape[0] and (t.stride(2) != 1 or
-                                        (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
-        raise ValueError(f"{name} must be [T, H, D] with dense rows [H, D]")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, H, D]")
+    (T, H, D), (st, sh, sd) = t.shape, t.stride()
+    if T and ((sd != 1 and D > 1) or (H > 1 and sh != D)):
+        raise ValueError(f"{name} must have dense rows [H, D]")
+    return st if T > 1 else H * D
 
 
 def _one_device(q: torch.Tensor, *others: torch.Tensor) -> None:
     """Every tensor on q's device, and that device current: the launch goes there."""
-    if any(t is not None and t.device != q.device for t in others):
-        raise ValueError("all tensors must be on one device")
-    if q.device.index != torch.cuda.current_device():
+    dev = q.get_device()
+    for t in others:
+        if t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+    if dev != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {q.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
 def _rotary(fn, q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_freq, scales,
             interleaved, magnitude, stream):
-    for name, t in (("q_out", q_out), ("q", q), ("k", k), ("v", v)):
-        _rows(name, t)
-    for name, t in (("slot_mapping", slot_mapping), ("positions", positions)):
-        _cuda(name, t)
+    so, sq, sk, sv = _rows("q_out", q_out), _rows("q", q), _rows("k", k), _rows("v", v)
+    _cuda("slot_mapping", slot_mapping)
+    _cuda("positions", positions)
     if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int32:
         raise TypeError("slot_mapping must be int64 and positions int32")
     T, Hq, D = q.shape
@@ -220,8 +228,8 @@ def _rotary(fn, q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_f
     if freq.ndim != 1:
         raise ValueError("inv_freq must be a host sequence of rotary_dim / 2 numbers")
     status = getattr(N.load(), fn)(
-        q_out.data_ptr(), _row_stride(q_out), q.data_ptr(), _row_stride(q), k.data_ptr(),
-        _row_stride(k), v.data_ptr(), _row_stride(v), _dtype(q), k_cache.data_ptr(),
+        q_out.data_ptr(), so, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, _dtype(q),
+        k_cache.data_ptr(),
         v_cache.data_ptr(), *[t.data_ptr() for t in scales], slot_mapping.data_ptr(),
         positions.data_ptr(), T, Hq, Hkv, D, k_cache.shape[2], k_cache.shape[0],
         freq.ctypes.data, 2 * freq.size, int(bool(interleaved)), float(magnitude),

@@ -205,12 +205,12 @@ __global__ void __launch_bounds__(kDecodeThreads)
         jb = t0 / BS;                             // partitions start on block boundaries
         ntiles = (t1 > t0) ? (t1 + BS - 1) / BS - jb : 0;
     }
-    // the cache block of tile it
+    // the cache block of tile it, as an index into bt_row below
     auto block_of = [&](int it) -> int {
         if constexpr (MODE == kMod)
             return order(jb + it);
         else
-            return jb + it;
+            return it;
     };
 
     if (threadIdx.x == 0) {
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
         // ------------------------------------------------------------------ producer
         if (fault)
             return;
-        const int32_t* bt_row = p.block_tables + (int64_t)seq * p.bt_stride;
+        const int32_t* bt_row = p.block_tables + (int64_t)seq * p.bt_stride + (MODE == kMod ? 0 : jb);
         const TK* kpool = reinterpret_cast<const TK*>(p.k_cache) + (int64_t)kvh * kTile;
         const TK* vpool = reinterpret_cast<const TK*>(p.v_cache) + (int64_t)kvh * kTile;
         const int64_t blk_stride = (int64_t)p.num_kv_heads * kTile;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
         }
         const TK* Ks = ring + stage * 2 * kTile;
         const TK* Vs = Ks + kTile;
-        const int tb = block_of(it) * BS;          // first token of the tile
+        const int tb = (MODE == kMod ? block_of(it) : jb + it) * BS;   // first token of the tile
         const int nvalid = min(BS, t1 - tb);
         // kMod: bit t is set when token tb + t is visible (the others' rows may hold
         // anything, and 0 * NaN is NaN: P.V skips them)

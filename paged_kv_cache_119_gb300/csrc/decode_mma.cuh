@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
         nblk = (t1 > t0) ? (t1 + BS - 1) / BS - jb : 0;
         ntiles = (nblk + BPT - 1) / BPT;          // tile it: blocks jb + BPT it .. + BPT - 1
     }
-    // first token of tile it, and the cache block of the CTA's i-th block
+    // first token of tile it, and the CTA's i-th block as an index into bt_row below
     auto tile_token = [&](int it) -> int {
         if constexpr (MODE == kMod)
             return order(jb + it) * TB;
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
         if constexpr (MODE == kMod)
             return order(jb + i / BPT) * BPT + i % BPT;
         else
-            return jb + i;
+            return i;
     };
     // kMod: whether block b of the context holds a seen token (the others are neither read
     // nor checked: an engine may have freed them)
@@ -368,22 +368,16 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
 
     if (warp == NCW) {
         // ------------------------------------------------------------------ producer
-        const int32_t* bt_row = p.block_tables + (int64_t)tseq * p.bt_stride;
+        const int32_t* bt_row = p.block_tables + (int64_t)tseq * p.bt_stride + (MODE == kMod ? 0 : jb);
         const uint64_t policy = l2_evict_first_policy();
-        auto entry = [&](int i) -> int {           // the i-th block's table entry
-            if (i >= nblk)
-                return 0;
-            const int b = block_of(i);
-            return block_seen(b) ? __ldg(bt_row + b) : 0;
-        };
-        int next = entry(lane);
+        int next = (lane < nblk && block_seen(block_of(lane))) ? __ldg(bt_row + block_of(lane)) : 0;
         bool aborted = false;
         // block-table entries 32 at a time (BPT divides 32, so no tile straddles two
         // batches), the next 32 in flight while the current ones are used
         for (int base = 0; base < nblk && !aborted; base += 32) {
             const int cur = next;
-            if (base + 32 + lane < nblk)
-                next = entry(base + 32 + lane);
+            if (base + 32 + lane < nblk && block_seen(block_of(base + 32 + lane)))
+                next = __ldg(bt_row + block_of(base + 32 + lane));
             const int cnt = min(32, nblk - base);
             for (int i = 0; i < cnt; i += BPT) {
                 int pbn[BPT];
@@ -391,10 +385,9 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                 for (int b = 0; b < BPT; ++b)
                     pbn[b] = __shfl_sync(kFullMask, cur, i + b);   // i + b <= 31
                 const int nb = min(BPT, cnt - i);                  // blocks of the tile in range
-                bool want[BPT];                                    // of those, the ones to read
-#pragma unroll
-                for (int b = 0; b < BPT; ++b)
-                    want[b] = b < nb && block_seen(block_of(base + i + b));
+                auto want = [&](int b) -> bool {                   // of those, the ones to read
+                    return b < nb && block_seen(block_of(base + i + b));
+                };
                 const int it = (base + i) / BPT;
                 const int stage = it % NSTAGE;
                 int ok = 1;
@@ -408,8 +401,8 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                         uint32_t tx = 0;
 #pragma unroll
                         for (int b = 0; b < BPT; ++b) {
-                            const bool valid = want[b] && pbn[b] >= 0 && (int64_t)pbn[b] < p.num_blocks;
-                            all_valid = all_valid && (!want[b] || valid);
+                            const bool valid = want(b) && pbn[b] >= 0 && (int64_t)pbn[b] < p.num_blocks;
+                            all_valid = all_valid && (!want(b) || valid);
                             tx += valid ? 2u * (kFp8 ? BS * D : BS * D * 2) : 0u;
                         }
                         stage_ok[stage] = all_valid ? 1 : 0;
@@ -422,7 +415,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                             mbar_arrive_expect_tx(&full[stage], tx);
 #pragma unroll
                             for (int b = 0; b < BPT; ++b) {
-                                if (!want[b] || pbn[b] < 0 || (int64_t)pbn[b] >= p.num_blocks)
+                                if (!want(b) || pbn[b] < 0 || (int64_t)pbn[b] >= p.num_blocks)
                                     continue;
                                 unsigned char* bdst = dst + b * (BS * 128);   // rows of block b
                                 if constexpr (kDirect) {

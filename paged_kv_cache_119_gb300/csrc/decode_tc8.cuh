@@ -356,24 +356,18 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         const uint64_t policy = l2_evict_first_policy();
         const int blk_first = t0 / BS;             // partitions start on block boundaries
         const int nblk = MODE == kMod ? ntiles * BPT : (t1 + BS - 1) / BS - blk_first;
-        // whether the CTA's i-th block is to be read, and which block of the context it is:
-        // kMod reads (and checks) only blocks that hold a seen token
-        auto block_of = [&](int i) -> int {
-            if constexpr (MODE == kMod)
-                return order(c0 + i / BPT) * BPT + i % BPT;
-            else
-                return blk_first + i;
-        };
+        // the table entry of the CTA's i-th block; kMod reads (and checks) only blocks that
+        // hold a seen token
         auto wanted = [&](int i) -> bool {
-            if (i >= nblk)
-                return false;
-            if constexpr (MODE == kMod) {
-                const int b = block_of(i);
-                return any_seen(seen, b * BS, min(b * BS + BS, t1));
-            }
-            return true;
+            const int b = order(c0 + i / BPT) * BPT + i % BPT;
+            return i < nblk && any_seen(seen, b * BS, min(b * BS + BS, t1));
         };
-        auto entry = [&](int i) -> int { return wanted(i) ? __ldg(bt_row + block_of(i)) : -1; };
+        auto entry = [&](int i) -> int {
+            if constexpr (MODE == kMod)
+                return wanted(i) ? __ldg(bt_row + order(c0 + i / BPT) * BPT + i % BPT) : -1;
+            else
+                return i < nblk ? __ldg(bt_row + blk_first + i) : -1;
+        };
         // block-table entries 32 at a time (4 or 8 tiles), the next 32 in flight while the
         // current ones are used
         int cur = entry(lane);
@@ -386,11 +380,15 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                 cur = nxt;
                 nxt = entry(lb + 32 + lane);
             }
+            int nb = min(BPT, nblk - lb);
             const int e = __shfl_sync(kFullMask, cur, ((lb & 31) + lane) & 31);
-            const bool want = lane < BPT && wanted(lb + lane);
-            const int nb = __popc(__ballot_sync(kFullMask, want));
             int pbn = -1;
             bool valid = false;
+            bool want = lane < nb;
+            if constexpr (MODE == kMod) {
+                want = lane < BPT && wanted(lb + lane);
+                nb = __popc(__ballot_sync(kFullMask, want));
+            }
             if (want) {
                 pbn = e;
                 valid = pbn >= 0 && (int64_t)pbn < p.num_blocks;

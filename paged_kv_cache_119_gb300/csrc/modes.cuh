@@ -3,9 +3,13 @@
 // one kernel family.
 #pragma once
 
+#include <atomic>
+
 #include "pa_internal.h"
 
 namespace pa {
+
+constexpr int kMaxCachedDevices = 64;
 
 // Launches one kernel variant V (kernel(), configure(), smem_bytes, threads) over
 // (partitions, kv heads * chunks, sequences or groups).
@@ -19,15 +23,28 @@ cudaError_t launch_mode_variant(dim3 grid, cudaStream_t stream, const Args&... a
     return cudaGetLastError();
 }
 
-// Resident CTAs per SM of variant V (0 if unknown).
+// Resident CTAs per SM of variant V (0 if unknown).  Asked once per device: the query costs
+// about a microsecond of host time, and a call asks for one or two kernels.
 template <typename V>
 int occupancy_mode_variant()
 {
+    static std::atomic<int> known[kMaxCachedDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return 0;
+    const bool cached = dev >= 0 && dev < kMaxCachedDevices;
+    if (cached) {
+        const int n = known[dev].load(std::memory_order_relaxed);
+        if (n > 0)
+            return n;
+    }
     int n = 0;
     if (V::configure() != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, V::kernel(), V::kThreads, V::kSmem) !=
             cudaSuccess)
         return 0;
+    if (cached)
+        known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

@@ -835,10 +835,10 @@ static uint64_t turn_fraction(double f)
     const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
     const double t = f * hi;
     const double e = std::fma(f, hi, -t) + f * lo;
-    const double part = std::ldexp(t - std::floor(t), 64);      // exact, in [0, 2^64]
+    const double part = (t - std::floor(t)) * 0x1p64;           // exact, in [0, 2^64]
     const double whole = std::floor(part);
     const uint64_t w = whole >= 0x1p64 ? 0u : (uint64_t)whole;
-    return w + (uint64_t)std::llrint((part - whole) + std::ldexp(e, 64));
+    return w + (uint64_t)std::llrint((part - whole) + e * 0x1p64);
 }
 
 // Whether two sets of `rows` rows (wa / wb bytes each, sa / sb bytes apart) share a byte:
