@@ -75,11 +75,29 @@ void choose_split(Plan& pl, const Shape& s, AttnMode mode, int64_t count, int le
         pl.partition = choose_partition(partition_size, length, pl.units, pl.slots, 64);
 }
 
+// Rows of a kv head that a mma.sync CTA serves when there are `rows` of them: 4 or 8
+// (decode_mma_kernel), 16, 32 or 64 (decode_rows_kernel; E4M3 at head_dim 64, whose tiles are
+// converted warp by warp, stays at 8).
+int rows_per_cta(const Shape& s, int64_t rows)
+{
+    if (rows <= 4)
+        return 4;
+    if (rows <= 8 || (s.fp8() && s.head_dim == 64))
+        return 8;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+// Tokens of a mma.sync kernel's tile.
+int rows_tile(const Shape& s, int per)
+{
+    return per > 8 || (s.fp8() && s.head_dim == 128) ? 32 : s.block_size;
+}
+
 // Kernel of a pass with one row per query head of a sequence (decode, or the suffix of the
 // shared-prefix decode).  Up to two heads per kv head the CUDA-core kernel streams faster
 // than a 16-row matrix fragment that is mostly empty (the rule of pa_decode); E4M3 codes at
 // head_dim 128 go to the tensor core as they are for up to four rows.  Other groups take
-// the next of 4 or 8 rows, padded, so that a K/V byte is read once per 8 heads whatever the
+// the next of 4, 8, 16, 32 or 64 rows, padded, so that a K/V byte is read once whatever the
 // group.
 Plan plan_heads(const Shape& s)
 {
@@ -107,9 +125,9 @@ Plan plan_heads(const Shape& s)
         return pl;
     }
     pl.family = Family::kRows;
-    pl.per = G <= 4 ? 4 : 8;
+    pl.per = rows_per_cta(s, G);
     pl.chunks = (G + pl.per - 1) / pl.per;
-    pl.tile = s.fp8() && s.head_dim == 128 && s.block_size == 16 ? 32 : s.block_size;
+    pl.tile = rows_tile(s, pl.per);
     return pl;
 }
 
@@ -121,12 +139,10 @@ Plan plan_rows(const Shape& s, int64_t tokens, int few_rows)
     Plan pl{};
     const int64_t rows = tokens * s.group();
     if (rows <= few_rows || (s.fp8() && s.head_dim != 128)) {
-        pl.per = rows <= 4 ? 4 : 8;
+        pl.per = rows_per_cta(s, rows);
         pl.family = s.fp8() && use_tc8(s.head_dim, pl.per) ? Family::kTc8 : Family::kRows;
         pl.chunks = (int)std::min<int64_t>((rows + pl.per - 1) / pl.per, INT32_MAX);
-        pl.tile = pl.family == Family::kTc8 ? 128
-                  : s.fp8() && s.head_dim == 128 && s.block_size == 16 ? 32
-                                                                       : s.block_size;
+        pl.tile = pl.family == Family::kTc8 ? 128 : rows_tile(s, pl.per);
         return pl;
     }
     pl.family = Family::kChunk;
@@ -404,6 +420,10 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// (sequence, head) rows per kv head up to which the pass over a shared prefix runs on a decode
+// kernel's row mode.
+constexpr int kPrefixRowsMax = 64;
+
 // The two passes of a shared-prefix decode.
 struct PrefixPlan {
     Plan prefix, suffix;
@@ -414,7 +434,7 @@ PrefixPlan prefix_plan(const Shape& s, int num_seqs, int num_groups, int max_gro
                        int max_prefix_len, int max_suffix_len, int partition_size)
 {
     PrefixPlan p{};
-    p.prefix = plan_rows(s, max_group_size, 16);
+    p.prefix = plan_rows(s, max_group_size, kPrefixRowsMax);
     choose_split(p.prefix, s, kPrefix, num_groups, max_prefix_len, partition_size);
     p.suffix = plan_heads(s);
     choose_split(p.suffix, s, kSuffix, num_seqs, max_suffix_len, partition_size);

@@ -1,22 +1,35 @@
-// modes_rows.cuh -- decode_mma_kernel (mma.sync, 4 or 8 rows of a kv head per CTA) in the
-// other modes; instantiated per query and cache type by modes_rows_*.cu.
+// modes_rows.cuh -- decode_mma_kernel (mma.sync; 4 or 8 rows of a kv head per CTA) and
+// decode_rows_kernel (16, 32 or 64) in the other modes; instantiated per query and cache type
+// by modes_rows_*.cu.
 #pragma once
 
 #include "decode_mma.cuh"
+#include "decode_rows.cuh"
 #include "modes.cuh"
 
 namespace pa {
 
+// Up to 8 rows per CTA on decode_mma_kernel, 16, 32 or 64 on decode_rows_kernel.
 template <typename T, typename TK, int D, int BS, int NH, int MODE>
 struct RowsMode {
     static constexpr int kBPT = mma_blocks_per_tile<TK, D, BS>();
-    static constexpr int kStages = MmaStages<TK, D, BS * kBPT>::value;
-    using Sm = MmaSmem<TK, D, BS * kBPT, kStages>;
+    // a row kernel's 32-token tiles: four stages (64 KB over 16-bit caches at head_dim 128)
+    static constexpr int kStages = NH <= 8 ? MmaStages<TK, D, BS * kBPT>::value : kDecodeConsumerWarps;
     static constexpr int kThreads = kDecodeThreads;
-    static constexpr int kSmem = Sm::kAlloc;
+    static constexpr int smem_bytes()
+    {
+        if constexpr (NH <= 8)
+            return MmaSmem<TK, D, BS * kBPT, kStages>::kAlloc;
+        else
+            return RowsSmem<TK, D, kStages, NH / kRowsGroup>::kAlloc;
+    }
+    static constexpr int kSmem = smem_bytes();
     static constexpr auto kernel()
     {
-        return decode_mma_kernel<T, TK, D, BS, NH, kStages, true, kBPT, MODE>;
+        if constexpr (NH <= 8)
+            return decode_mma_kernel<T, TK, D, BS, NH, kStages, true, kBPT, MODE>;
+        else
+            return decode_rows_kernel<T, TK, D, BS, kStages, MODE, NH / kRowsGroup>;
     }
     static cudaError_t configure()
     {
@@ -25,7 +38,7 @@ struct RowsMode {
 };
 
 // Calls f with the variant's type; false when it is not built (E4M3 caches at head_dim 128
-// take 4 rows on decode_tc8_kernel).
+// take 4 rows on decode_tc8_kernel, at head_dim 64 no more than 8).
 template <typename T, typename TK, int MODE, typename F>
 bool rows_variant(int head_dim, int block_size, int nh, F&& f)
 {
@@ -36,8 +49,12 @@ bool rows_variant(int head_dim, int block_size, int nh, F&& f)
     }
     PA_ROWS_MODE(128, 16, 8) PA_ROWS_MODE(128, 32, 8) PA_ROWS_MODE(64, 16, 8) PA_ROWS_MODE(64, 32, 8)
     PA_ROWS_MODE(64, 16, 4) PA_ROWS_MODE(64, 32, 4)
+    PA_ROWS_MODE(128, 16, 16) PA_ROWS_MODE(128, 32, 16) PA_ROWS_MODE(128, 16, 32) PA_ROWS_MODE(128, 32, 32)
+    PA_ROWS_MODE(128, 16, 64) PA_ROWS_MODE(128, 32, 64)
     if constexpr (sizeof(TK) != 1) {
         PA_ROWS_MODE(128, 16, 4) PA_ROWS_MODE(128, 32, 4)
+        PA_ROWS_MODE(64, 16, 16) PA_ROWS_MODE(64, 32, 16) PA_ROWS_MODE(64, 16, 32) PA_ROWS_MODE(64, 32, 32)
+        PA_ROWS_MODE(64, 16, 64) PA_ROWS_MODE(64, 32, 64)
     }
 #undef PA_ROWS_MODE
     return false;

@@ -328,7 +328,7 @@ cudaError_t launch_core_mode(const DecodeParams& p, AttnMode mode, pa_dtype q_dt
                              int head_dim, int block_size, int gc, dim3 grid, cudaStream_t stream);
 int occupancy_core_mode(AttnMode mode, pa_dtype q_dtype, pa_dtype kv_dtype, int head_dim, int block_size,
                         int gc);
-// decode_mma_kernel, nh (4 or 8) rows per CTA:
+// decode_mma_kernel (nh = 4 or 8 rows per CTA) and decode_rows_kernel (16, 32 or 64):
 cudaError_t launch_rows_f16(const DecodeParams& p, AttnMode mode, int head_dim, int block_size,
                        int nh, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                        cudaStream_t stream);

@@ -67,6 +67,7 @@ MODS = [dict(), dict(window=1), dict(window=16), dict(window=37), dict(window=50
     (4, 4, 128, 16, torch.float16, False), (6, 2, 64, 32, torch.bfloat16, False),
     (8, 2, 128, 16, torch.bfloat16, False), (8, 1, 128, 32, torch.float16, False),
     (14, 2, 128, 16, torch.bfloat16, False), (24, 2, 64, 16, torch.float16, False),
+    (40, 1, 128, 16, torch.float16, False), (30, 1, 128, 16, torch.bfloat16, True),
     (3, 3, 64, 16, torch.float32, False), (8, 1, 128, 32, torch.float32, False),
     (2, 2, 128, 16, torch.bfloat16, True), (4, 2, 128, 32, torch.float16, True),
     (6, 2, 128, 16, torch.bfloat16, True), (8, 2, 128, 16, torch.float16, True),

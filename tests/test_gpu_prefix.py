@@ -60,6 +60,7 @@ def compare(c, **kw):
 
 
 SMALL = [(64, [1, 5, 70]), (0, [40]), (160, [0, 33]), (32, [9])]
+MEDIUM = [(320, [5, 0, 90, 33, 17, 1, 64]), (48, [2, 2, 2]), (0, [100])]     # up to 32 rows at G = 4
 WIDE = [(192, [int(x) for x in np.random.default_rng(1).integers(0, 90, 37)]), (96, [20, 1])]
 SHAPES = [(4, 4, 128, 16, torch.float16, False), (8, 2, 64, 32, torch.bfloat16, False),
           (8, 1, 128, 16, torch.bfloat16, False), (14, 2, 128, 32, torch.float16, False),
@@ -69,9 +70,10 @@ SHAPES = [(4, 4, 128, 16, torch.float16, False), (8, 2, 64, 32, torch.bfloat16, 
           (2, 2, 64, 16, torch.float16, True), (8, 1, 64, 32, torch.bfloat16, True)]
 
 
-@pytest.mark.parametrize("groups", [SMALL, WIDE], ids=["small", "wide"])
+@pytest.mark.parametrize("groups", [SMALL, MEDIUM, WIDE], ids=["small", "medium", "wide"])
 @pytest.mark.parametrize("Hq,Hkv,D,B,dtype,fp8", SHAPES)
 def test_against_the_reference(Hq, Hkv, D, B, dtype, fp8, groups):
+    groups = [(p // B * B, tails) for p, tails in groups]
     c = make(Hq + D, groups, Hq, Hkv, D, B, dtype, fp8)
     for part in (0, -1, 128):
         compare(c, partition_size=part)
