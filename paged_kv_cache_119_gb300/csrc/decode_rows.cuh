@@ -37,8 +37,10 @@ struct RowsSmem {
     static constexpr int kHalfBytes = TB * 128;                          // one 128-byte-row box
     static constexpr int kStageBytes = 2 * kTileBytes;
     static constexpr int kRingBytes = NSTAGE * kStageBytes;
-    // merge area (over the ring, once every tile is consumed): 16 rows of each warp
-    static constexpr int kMergeAcc = kDecodeConsumerWarps * kRowsGroup * D * 4;
+    // merge area (over the ring, once every tile is consumed): 16 rows of each warp, D + 8
+    // floats apart so that the 8-byte stores of a fragment meet no bank twice
+    static constexpr int kMergeRow = D + 8;
+    static constexpr int kMergeAcc = kDecodeConsumerWarps * kRowsGroup * kMergeRow * 4;
     static constexpr int kMergeBytes = kMergeAcc + kDecodeConsumerWarps * kRowsGroup * 2 * 4;
     static constexpr int kDataBytes = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
     static constexpr int kBarOffset = (kDataBytes + 7) / 8 * 8;
@@ -135,9 +137,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     TileOrder order{0, 0, 0};
     int t0 = start, t1 = L;
     int jb = 0, nblk = 0, ntiles = 0;
+    // kMod: positions of the CTA's first and last row; the window's start for the last
+    const int first_pos = L - n + R0 / p.group, last_pos = L - n + min(n - 1, (R0 + NR - 1) / p.group);
+    const int low_max = MODE == kMod && p.mods.window > 0 ? max(0, last_pos - p.mods.window + 1) : 0;
     if constexpr (MODE == kMod) {
         // partitions cut the list of tiles to read; jb counts tiles of that list
-        seen = seen_by(p.mods, seq, L, L - n + R0 / p.group, L - n + min(n - 1, (R0 + NR - 1) / p.group));
+        seen = seen_by(p.mods, seq, L, first_pos, last_pos);
         order = seen_tiles(seen, TB);
         t1 = seen.end;
         jb = split ? part * (p.partition_tokens / TB) : 0;
@@ -394,22 +399,39 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 #pragma unroll
         for (int h = 0; h < 4; ++h)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = k >> 1;
-                const int tt = 8 * h + 2 * c + (k & 1);
-                float x = s[h][k] * sl2;
-                if constexpr (MODE == kMod) {
-                    const int t = tb + tt;
-                    if (p.mods.cap > 0.f)
-                        x = cap_score(x, p.mods);
-                    if (p.mods.slopes)
-                        x = fmaf(-slope[j], fabsf((float)(lim[j] - t)), x);
-                    x = (t < glob[j] || (t >= low[j] && t <= lim[j])) ? x : -INFINITY;
-                } else {
-                    x = tt < nvalid ? x : -INFINITY;
-                }
-                s[h][k] = x;
+            for (int k = 0; k < 4; ++k)
+                s[h][k] *= sl2;
+        bool ragged = nvalid < TB;                // some tokens are outside, or seen by no row
+        bool mask = ragged;                       // some row does not see some token
+        if constexpr (MODE == kMod) {
+            ragged = ragged || (tb < seen.lo && tb + TB > seen.glob);
+            mask = !(tb + TB <= seen.glob || (tb + TB - 1 <= first_pos && tb >= low_max));
+            if (p.mods.cap > 0.f) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        s[h][k] = cap_score(s[h][k], p.mods);
             }
+            if (p.mods.slopes) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        s[h][k] = fmaf(-slope[k >> 1],
+                                       fabsf((float)(lim[k >> 1] - (tb + 8 * h + 2 * c + (k & 1)))), s[h][k]);
+            }
+        }
+        if (mask) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int tt = 8 * h + 2 * c + (k & 1), t = tb + tt, j = k >> 1;
+                    const bool sees = MODE == kMod ? t < glob[j] || (t >= low[j] && t <= lim[j]) : tt < nvalid;
+                    s[h][k] = sees ? s[h][k] : -INFINITY;
+                }
+        }
         // A row's reference maximum moves only when a tile's maximum exceeds it by more than
         // 2^8 in probability (O / l is exact for any reference), so that after the first tiles
         // O is hardly ever rescaled: with 16 rows a warp some row's true maximum rises in most
@@ -453,9 +475,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         }
         // ---- O += P . V over the two 16-token halves; V rows of tokens outside the range, or
         // that no row sees, count 0
-        bool ragged = nvalid < TB;
-        if constexpr (MODE == kMod)
-            ragged = ragged || (tb < seen.lo && tb + TB > seen.glob);
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
             // P (hi + lo) as A fragments: rows g, g + 8 of the low 8 tokens, then of the high
@@ -527,65 +546,77 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 
     // ------------------------------------------------------------- merge the warps
     named_barrier(1, NCW * 32);            // every tile consumed: the ring is free
-    float* mrg_acc = reinterpret_cast<float*>(smem);                    // [NCW][16][D]
-    float* mrg_ml = mrg_acc + NCW * kRowsGroup * D;                      // [NCW][16][2]
+    constexpr int MR = Sm::kMergeRow;
+    float* mrg_acc = reinterpret_cast<float*>(smem);                    // [NCW][16][MR]
+    float* mrg_ml = mrg_acc + NCW * kRowsGroup * MR;                     // [NCW][16][2]
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         float l = lsum[j];
         l += __shfl_xor_sync(kFullMask, l, 1);
         l += __shfl_xor_sync(kFullMask, l, 2);
         const int row = warp * kRowsGroup + g + 8 * j;
-        if (c == 0) {
-            mrg_ml[row * 2 + 0] = m[j];
-            mrg_ml[row * 2 + 1] = l;
-        }
+        if (c == 0)
+            *reinterpret_cast<float2*>(mrg_ml + row * 2) = make_float2(m[j], l);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const int d0 = kFp8 ? 32 * (i / 4) + 8 * c + i % 4 : 8 * i + 2 * c;
-            const int d1 = kFp8 ? d0 + 4 : d0 + 1;
-            mrg_acc[row * D + d0] = o[i][2 * j];
-            mrg_acc[row * D + d1] = o[i][2 * j + 1];
+            if constexpr (kFp8) {
+                mrg_acc[row * MR + 32 * (i / 4) + 8 * c + i % 4] = o[i][2 * j];
+                mrg_acc[row * MR + 32 * (i / 4) + 8 * c + i % 4 + 4] = o[i][2 * j + 1];
+            } else {
+                *reinterpret_cast<float2*>(mrg_acc + row * MR + 8 * i + 2 * c) =
+                    make_float2(o[i][2 * j], o[i][2 * j + 1]);
+            }
         }
     }
     if (poisoned)
         *poison = 1;
     named_barrier(1, NCW * 32);
 
+    // TPR threads a row, each every TPR-th 4-dim piece of it
+    constexpr int TPR = NCW * 32 / NR;
     const bool bad = *poison != 0;
+    const int h = threadIdx.x / TPR;
+    if ((R0 + h) / p.group >= n)
+        return;                                        // a padding row
+    // the row's warps: wt RW + (row group)
+    auto part_row = [&](int wt) { return (wt * RW + h / kRowsGroup) * kRowsGroup + h % kRowsGroup; };
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < TW; ++w)
+        M = fmaxf(M, mrg_ml[part_row(w) * 2]);
+    float cw[TW], den = 0.f;
+#pragma unroll
+    for (int w = 0; w < TW; ++w) {
+        const float2 ml = *reinterpret_cast<const float2*>(mrg_ml + part_row(w) * 2);
+        cw[w] = M == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+        den = fmaf(cw[w], ml.y, den);
+    }
+    // no visible token gives 0; a poisoned CTA, or NaN scores, NaN
     const float vs = kFp8 ? p.v_scale[kvh] : 1.f;
-    for (int idx = threadIdx.x; idx < NR * D; idx += NCW * 32) {
-        const int h = idx / D;
-        const int d = idx - h * D;
-        if ((R0 + h) / p.group >= n)
-            break;                                     // rows past the last (h only grows)
-        // the row's warps: wt RW + (row group)
-        auto part_row = [&](int wt) { return (wt * RW + h / kRowsGroup) * kRowsGroup + h % kRowsGroup; };
-        float M = -INFINITY;
+    const float mul = bad || den != den ? __int_as_float(0x7fc00000) : den > 0.f ? vs / den : 0.f;
+    const int64_t row = out_row(R0 + h);
+    const int64_t prow = row * p.max_parts + (MODE == kSuffix ? p.part_base : 0) + part;
+    if (split && threadIdx.x % TPR == 0)
+        *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, den);
 #pragma unroll
-        for (int w = 0; w < TW; ++w)
-            M = fmaxf(M, mrg_ml[part_row(w) * 2]);
-        float num = 0.f, den = 0.f;
-        if (M != -INFINITY) {
+    for (int i = 0; i < D / 4 / TPR; ++i) {
+        const int d = 4 * (threadIdx.x % TPR + i * TPR);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < TW; ++w) {
-                const float cw = exp2f(mrg_ml[part_row(w) * 2] - M);
-                num = fmaf(cw, mrg_acc[part_row(w) * D + d], num);
-                den = fmaf(cw, mrg_ml[part_row(w) * 2 + 1], den);
-            }
+        for (int w = 0; w < TW; ++w) {
+            const float4 a = *reinterpret_cast<const float4*>(mrg_acc + part_row(w) * MR + d);
+            v.x = fmaf(cw[w], a.x, v.x);
+            v.y = fmaf(cw[w], a.y, v.y);
+            v.z = fmaf(cw[w], a.z, v.z);
+            v.w = fmaf(cw[w], a.w, v.w);
         }
-        float out = (den > 0.f ? num / den : 0.f) * vs;
-        if (bad || den != den)
-            out = __int_as_float(0x7fc00000);
-        const int64_t row = out_row(R0 + h);
-        if (split) {
-            const int64_t prow = row * p.max_parts + (MODE == kSuffix ? p.part_base : 0) + part;
-            p.part_o[prow * D + d] = out;
-            if (d == 0) {
-                p.part_ml[prow * 2 + 0] = M;
-                p.part_ml[prow * 2 + 1] = den;
-            }
+        v = make_float4(v.x * mul, v.y * mul, v.z * mul, v.w * mul);
+        if (split || p.out_f32) {
+            float* dst = split ? p.part_o + prow * D : static_cast<float*>(p.out) + row * D;
+            *reinterpret_cast<float4*>(dst + d) = v;
         } else {
-            store_out<T>(p, row * D + d, out);
+            *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D + d) =
+                make_uint2(Mma<T>::pack(v.x, v.y), Mma<T>::pack(v.z, v.w));
         }
     }
 }
