@@ -722,19 +722,17 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         if (lane == 0)
             mbar_arrive(q_full);
 
-        // Capped scores, fast form: for |y| <= 1/2, y = s kk, tanh y = y P(y^2) with the
-        // four-term P below (relative error at most 5.5e-7 there, the Chebyshev-like best fit;
-        // the probabilities are rounded to f16, 2^-11, right after), so the score is
-        // s (kp0 + kp1 s^2 + kp2 s^4 + kp3 s^6): three packed multiply-adds more than an
-        // uncapped score, and no MUFU work beyond its one exp2.  Taken by a warp's tile that
-        // all its rows see whole and whose scores lie in that range; other tiles take
-        // cap_score.  kk outside [10^-6, 8] would take kp3 out of fp32's normal range.
+        // Capped scores, fast form: for |y| <= kCapNear, y = s kk, tanh y = y P(y^2) (see
+        // cap_score_near), so the score is s (kp0 + kp1 s^2 + kp2 s^4 + kp3 s^6): three packed
+        // multiply-adds more than an uncapped score, and no MUFU work beyond its one exp2.
+        // Taken by a warp's tile that all its rows see whole and whose scores lie in that
+        // range; other tiles take cap_score.  kk outside [10^-6, 8] would take kp3 out of fp32's normal range.
         const float kk = MODE == kMod ? sl2 * p.mods.inv_cap : 0.f;
         const bool cap_fast = MODE == kMod && p.mods.cap > 0.f && !p.mods.slopes &&
                               __all_sync(kFullMask, kk >= 1e-6f && kk <= 8.f);
         const float k2 = kk * kk;
-        const float kp[4] = {0.99999946f * sl2, -0.33326318f * sl2 * k2, 0.13190297f * sl2 * k2 * k2,
-                             -0.04440223f * sl2 * k2 * k2 * k2};
+        const float kp[4] = {kCapP0 * sl2, kCapP1 * sl2 * k2, kCapP2 * sl2 * k2 * k2,
+                             kCapP3 * sl2 * k2 * k2 * k2};
         auto poly_at = [&](float z) { return fmaf(fmaf(fmaf(kp[3], z, kp[2]), z, kp[1]), z, kp[0]); };
         const bool warp_live = __any_sync(kFullMask, row_valid);
         const uint32_t lane_t = tbase + ((uint32_t)(32 * wq) << 16);
@@ -774,7 +772,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     if (whole && cap_fast) {
                         const float2 mm = row_range(s);
                         smax = mm.y;
-                        poly = __all_sync(kFullMask, fmaxf(fabsf(mm.x), fabsf(mm.y)) * kk <= 0.5f);
+                        poly = __all_sync(kFullMask, fmaxf(fabsf(mm.x), fabsf(mm.y)) * kk <= kCapNear);
                     }
                     if (!poly) {
                         if (p.mods.cap > 0.f) {

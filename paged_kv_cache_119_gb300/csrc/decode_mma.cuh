@@ -619,11 +619,22 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             const int tok_a = 16 * mb + g, tok_b = tok_a + 8;
             float x[4];
             if constexpr (MODE == kMod) {
+                // scores well within the cap (the usual case): the short form of tanh
+                bool near_cap = false;
+                if (p.mods.cap > 0.f) {
+                    const float far0 = fmaxf(fmaxf(fabsf(s[0]), fabsf(s[1])), fmaxf(fabsf(s[2]), fabsf(s[3])));
+                    near_cap = __all_sync(kFullMask, far0 * fabsf(sl2) * p.mods.inv_cap <= kCapNear);
+                    if (near_cap) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            s[j] = cap_score_near(s[j] * sl2, p.mods);
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = j & 1, t = tb + (j < 2 ? tok_a : tok_b);
-                    x[j] = s[j] * sl2;
-                    if (p.mods.cap > 0.f)
+                    x[j] = near_cap ? s[j] : s[j] * sl2;
+                    if (p.mods.cap > 0.f && !near_cap)
                         x[j] = cap_score(x[j], p.mods);
                     x[j] = fmaf(-slope[r], (float)abs(lim[r] - t), x[j]);
                     const bool sees = t < glob[r] || (t >= low[r] && t <= lim[r]);
@@ -784,6 +795,54 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     named_barrier(1, NCW * 32);
 
     const bool bad = *poison != 0;
+    if constexpr (MODE != kPlain) {
+        // TPR threads a row, each every TPR-th 4-dim piece of it: the row's weights are worked
+        // out once a thread (the short passes of these modes feel the merge)
+        constexpr int TPR = NCW * 32 / NH;
+        const int h = threadIdx.x / TPR;
+        const int j = (R0 + h) / p.group;
+        if (j >= n)
+            return;                                    // a padding row
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NCW; ++w)
+            M = fmaxf(M, mrg_ml[(w * 8 + h) * 2]);
+        float cw[NCW], den = 0.f;
+#pragma unroll
+        for (int w = 0; w < NCW; ++w) {
+            const float2 ml = *reinterpret_cast<const float2*>(mrg_ml + (w * 8 + h) * 2);
+            cw[w] = M == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+            den = fmaf(cw[w], ml.y, den);
+        }
+        // no visible token gives 0; a poisoned CTA, or NaN scores, NaN
+        const float vs = kFp8 ? p.v_scale[kvh] : 1.f;
+        const float mul = bad || den != den ? __int_as_float(0x7fc00000) : den > 0.f ? vs / den : 0.f;
+        const int64_t row = (int64_t)(qs0 + j) * p.num_q_heads + kvh * p.group + (R0 + h - j * p.group);
+        const int64_t prow = row * p.max_parts + (MODE == kSuffix ? p.part_base : 0) + part;
+        if (split && threadIdx.x % TPR == 0)
+            *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, den);
+#pragma unroll
+        for (int d = 4 * (threadIdx.x % TPR); d < D; d += 4 * TPR) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NCW; ++w) {
+                const float4 a = *reinterpret_cast<const float4*>(mrg_acc + (w * 8 + h) * D + d);
+                v.x = fmaf(cw[w], a.x, v.x);
+                v.y = fmaf(cw[w], a.y, v.y);
+                v.z = fmaf(cw[w], a.z, v.z);
+                v.w = fmaf(cw[w], a.w, v.w);
+            }
+            v = make_float4(v.x * mul, v.y * mul, v.z * mul, v.w * mul);
+            if (split || p.out_f32) {
+                float* dst = split ? p.part_o + prow * D : static_cast<float*>(p.out) + row * D;
+                *reinterpret_cast<float4*>(dst + d) = v;
+            } else {
+                *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * D + d) =
+                    make_uint2(Mma<T>::pack(v.x, v.y), Mma<T>::pack(v.z, v.w));
+            }
+        }
+        return;
+    }
     for (int idx = threadIdx.x; idx < NH * D; idx += NCW * 32) {
         const int h = idx / D;
         const int d = idx - h * D;

@@ -407,11 +407,26 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             ragged = ragged || (tb < seen.lo && tb + TB > seen.glob);
             mask = !(tb + TB <= seen.glob || (tb + TB - 1 <= first_pos && tb >= low_max));
             if (p.mods.cap > 0.f) {
+                float far0 = 0.f;
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        s[h][k] = cap_score(s[h][k], p.mods);
+                        far0 = fmaxf(far0, fabsf(s[h][k]));
+                // scores well within the cap (the usual case): the short form of tanh
+                if (__all_sync(kFullMask, far0 * p.mods.inv_cap <= kCapNear)) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            s[h][k] = cap_score_near(s[h][k], p.mods);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            s[h][k] = cap_score(s[h][k], p.mods);
+                }
             }
             if (p.mods.slopes) {
 #pragma unroll

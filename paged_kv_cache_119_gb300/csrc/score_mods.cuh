@@ -39,6 +39,17 @@ __device__ __forceinline__ float cap_score(float x, const ScoreMods& m)
     return m.cap * (z < 0.0625f ? near0 : far0);
 }
 
+// The same where |x / c| <= kCapNear: tanh y = y P(y^2) with the four-term P of least relative
+// error on [0, kCapNear^2] (5.5e-7), fitted numerically.
+constexpr float kCapNear = 0.5f;
+constexpr float kCapP0 = 0.99999946f, kCapP1 = -0.33326318f, kCapP2 = 0.13190297f, kCapP3 = -0.04440223f;
+__device__ __forceinline__ float cap_score_near(float x, const ScoreMods& m)
+{
+    const float y = x * m.inv_cap;
+    const float z = y * y;
+    return x * fmaf(fmaf(fmaf(kCapP3, z, kCapP2), z, kCapP1), z, kCapP0);
+}
+
 // Tokens some row of a set sees: [0, glob) and [lo, end), 0 <= glob <= end, lo <= end.
 struct Seen {
     int glob, lo, end;
