@@ -216,6 +216,34 @@ __device__ __forceinline__ float2 row_range(const float (&s)[kChunkTileTok])
     return make_float2(min3f(fminf(lo[0], lo[1]), lo[2], lo[3]), max3f(fmaxf(hi[0], hi[1]), hi[2], hi[3]));
 }
 
+// Caps a row's 64 scores (s * mul in base-2 units, in place).  Rows of a warp that stay within
+// the cap itself (|y| <= 1, y = x / cap) take the six-term odd polynomial of tanh (least relative
+// error there, 5.9e-7, fitted numerically); others cap_score.
+__device__ __forceinline__ void cap_row(float (&s)[kChunkTileTok], float mul, const ScoreMods& m)
+{
+    const float k = mul * m.inv_cap;
+    const float2 mm = row_range(s);
+    if (__all_sync(kFullMask, fmaxf(fabsf(mm.x), fabsf(mm.y)) * fabsf(k) <= 1.f)) {
+        constexpr float q[6] = {0.99999941f, -0.33329042f, 0.13281434f, -0.05160568f, 0.01674312f, -0.00306706f};
+#pragma unroll
+        for (int c = 0; c < kChunkTileTok; c += 2) {
+            const float2 y = fmul2(make_float2(s[c], s[c + 1]), make_float2(k, k));
+            const float2 z = fmul2(y, y);
+            float2 f = ffma2(z, make_float2(q[5], q[5]), make_float2(q[4], q[4]));
+#pragma unroll
+            for (int i = 3; i >= 0; --i)
+                f = ffma2(z, f, make_float2(q[i], q[i]));
+            const float2 x = fmul2(fmul2(y, make_float2(m.cap, m.cap)), f);
+            s[c] = x.x;
+            s[c + 1] = x.y;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < kChunkTileTok; ++c)
+            s[c] = cap_score(s[c] * mul, m);
+    }
+}
+
 // grid = (partitions, num_kv_heads * m_tiles, num_seqs); kChunkThreads threads over
 // f16 caches, kChunkThreadsConv over E4M3 (NRAW > 0) and bf16 caches.  T: query /
 // native output type.  Over E4M3 caches (value = code * per-kv-head scale) the
@@ -229,7 +257,7 @@ __device__ __forceinline__ float2 row_range(const float (&s)[kChunkTileTok])
 template <typename T, int NRAW, int MODE>
 constexpr int chunk_threads()
 {
-    return (NRAW > 0 || std::is_same_v<T, __nv_bfloat16> || MODE == kMod) ? kChunkThreadsConv
+    return (NRAW > 0 || std::is_same_v<T, __nv_bfloat16> || is_mod(MODE)) ? kChunkThreadsConv
                                                                           : kChunkThreads;
 }
 
@@ -240,9 +268,10 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
 {
     using Sm = ChunkSmem<D, NST, NRAW>;
     constexpr bool kF8 = NRAW > 0;
+    constexpr bool kIsMod = is_mod(MODE), kCap = has_cap(MODE), kSlope = has_slope(MODE);
     constexpr bool kVConv = !kF8 && std::is_same_v<T, __nv_bfloat16>;   // bf16 V -> f16 in place
-    constexpr bool kVHand = kVConv || (!kF8 && MODE == kMod);           // V handed over (vconv)
-    constexpr bool kVZero = !kVConv && MODE != kMod;    // softmax warps zero the last tile's V rows
+    constexpr bool kVHand = kVConv || (!kF8 && kIsMod);           // V handed over (vconv)
+    constexpr bool kVZero = !kVConv && !kIsMod;    // softmax warps zero the last tile's V rows
     using TM = std::conditional_t<kF8, __half, T>;   // operand type of the score product
     constexpr int NT = kChunkTileTok;
     constexpr int BPT = NT / BS;                 // cache blocks per K/V tile
@@ -317,7 +346,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     Seen seen{0, 0, 0};
     TileOrder order{0, 0, 0};
     int c0 = 0;                                  // kMod: first tile of the list to read
-    if constexpr (MODE == kMod) {
+    if constexpr (kIsMod) {
         seen = seen_by(p.mods, seq, L, pos_first, pos_first + ntok - 1);
         order = seen_tiles(seen, NT);
         t_end = seen.end;
@@ -327,7 +356,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         ntiles = split ? min(order.count - c0, p.partition_tokens / NT) : order.count;
     }
     int t1 = t_end;
-    if constexpr (MODE != kMod) {
+    if constexpr (!kIsMod) {
         if (p.partition_tokens > 0) {
             t0 = part * p.partition_tokens;
             t1 = min(t_end, t0 + p.partition_tokens);
@@ -338,7 +367,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     }
     // first token of tile it
     auto tile_token = [&](int it) -> int {
-        if constexpr (MODE == kMod)
+        if constexpr (kIsMod)
             return order(c0 + it) * NT;
         else
             return t0 + it * NT;
@@ -400,7 +429,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
             const int st = it % NP;
             const int b0 = tile_token(it) / BS;
             bool want = lane < min(BPT, blk_end - b0);
-            if constexpr (MODE == kMod)          // only blocks that hold a seen token
+            if constexpr (kIsMod)          // only blocks that hold a seen token
                 want = want && any_seen(seen, (b0 + lane) * BS, min((b0 + lane) * BS + BS, t1));
             const int nb = __popc(__ballot_sync(kFullMask, want));
             int pbn = -1;
@@ -479,7 +508,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                         const int c = item & 7;
                         uint4 w = *reinterpret_cast<const uint4*>(
                             raw + kv * Sm::kRawTile + t * 128 + ((c ^ (t & 7)) << 4));
-                        if (MODE == kMod && kv == 1 && !is_seen(seen, tb + t))
+                        if (kIsMod && kv == 1 && !is_seen(seen, tb + t))
                             w = make_uint4(0u, 0u, 0u, 0u);
                         unsigned char* row =
                             dst + kv * Sm::kKBytes + (c >> 2) * Sm::kKVHalf + t * 128;
@@ -529,7 +558,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     uint4* chunk = reinterpret_cast<uint4*>(vt + (item / (NT * 8)) * Sm::kKVHalf +
                                                             w * 16);
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if ((w >> 3) < nv && (MODE != kMod || is_seen(seen, tb + (w >> 3)))) {
+                    if ((w >> 3) < nv && (!kIsMod || is_seen(seen, tb + (w >> 3)))) {
                         const uint4 b = *chunk;
                         const uint32_t in[4] = {b.x, b.y, b.z, b.w};
                         uint32_t o[4];
@@ -652,10 +681,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         const bool row_valid = tok < ntok;               // (r >= TT * G gives tok >= TT)
         const int pos = MODE == kPrefix ? L - 1 : pos_first + tok;
         // kMod: first visible position past the global tokens, base-2 distance slope
-        const int low = MODE == kMod && p.mods.window > 0 ? max(0, pos - p.mods.window + 1) : 0;
-        const float slope = MODE == kMod && p.mods.slopes
-                                ? p.mods.slopes[kvh * G + g] * 1.4426950408889634f
-                                : 0.f;
+        const int low = kIsMod && p.mods.window > 0 ? max(0, pos - p.mods.window + 1) : 0;
+        const float slope = kSlope ? p.mods.slopes[kvh * G + g] * 1.4426950408889634f : 0.f;
         const int64_t qrow = (int64_t)(qs0 + j0 + tok) * p.num_q_heads + (int64_t)kvh * G + g;
         // scores are used as s * sl2 with sl2 > 0: a negative scale flips the sign of q
         // (exact), a zero scale makes q zero (every score 0); over E4M3 caches the K scale
@@ -727,9 +754,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         // multiply-adds more than an uncapped score, and no MUFU work beyond its one exp2.
         // Taken by a warp's tile that all its rows see whole and whose scores lie in that
         // range; other tiles take cap_score.  kk outside [10^-6, 8] would take kp3 out of fp32's normal range.
-        const float kk = MODE == kMod ? sl2 * p.mods.inv_cap : 0.f;
-        const bool cap_fast = MODE == kMod && p.mods.cap > 0.f && !p.mods.slopes &&
-                              __all_sync(kFullMask, kk >= 1e-6f && kk <= 8.f);
+        const float kk = kCap ? sl2 * p.mods.inv_cap : 0.f;
+        const bool cap_fast = kCap && !kSlope && __all_sync(kFullMask, kk >= 1e-6f && kk <= 8.f);
         const float k2 = kk * kk;
         const float kp[4] = {kCapP0 * sl2, kCapP1 * sl2 * k2, kCapP2 * sl2 * k2 * k2,
                              kCapP3 * sl2 * k2 * k2 * k2};
@@ -763,25 +789,25 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 float mul = sl2;                 // scores are s * mul (base 2), or, capped, the
                 bool poly = false;               // polynomial of s below
                 float smax;
-                if constexpr (MODE == kMod) {
+                if constexpr (kIsMod) {
                     // column c is visible when c < gl, or lo <= c <= lim (rows past the
                     // chunk are all zeros and never stored: let them see everything)
                     const int gl = seen.glob - tb, lo = low - tb;
                     const bool whole = __all_sync(
                         kFullMask, !row_valid || gl >= NT || (lim >= NT - 1 && lo <= 0));
-                    if (whole && cap_fast) {
-                        const float2 mm = row_range(s);
-                        smax = mm.y;
-                        poly = __all_sync(kFullMask, fmaxf(fabsf(mm.x), fabsf(mm.y)) * kk <= kCapNear);
+                    if constexpr (kCap && !kSlope) {
+                        if (whole && cap_fast) {
+                            const float2 mm = row_range(s);
+                            smax = mm.y;
+                            poly = __all_sync(kFullMask, fmaxf(fabsf(mm.x), fabsf(mm.y)) * kk <= kCapNear);
+                        }
                     }
                     if (!poly) {
-                        if (p.mods.cap > 0.f) {
+                        if constexpr (kCap) {
                             mul = 1.f;
-#pragma unroll
-                            for (int c = 0; c < NT; ++c)
-                                s[c] = cap_score(s[c] * sl2, p.mods);
+                            cap_row(s, sl2, p.mods);
                         }
-                        if (p.mods.slopes) {
+                        if constexpr (kSlope) {
                             // |pos - t| = pos - t while no column lies behind pos
                             const float far0 = (float)(pos - tb);
                             if (lim >= NT - 1 || !row_valid) {
@@ -819,7 +845,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     smax = row_max(s);
                 }
                 float tmax = smax == -INFINITY ? -INFINITY : smax * mul;
-                if (MODE == kMod && poly)
+                if (kCap && poly)
                     tmax = smax * poly_at(smax * smax);
                 const bool need = tmax > m_ref + 8.f;
                 if (it > 0 && __any_sync(kFullMask, need)) {
@@ -857,7 +883,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
 #pragma unroll
                 for (int c = 0; c < NT; c += 2) {
                     float2 f = make_float2(mul, mul);
-                    if (MODE == kMod && poly) {
+                    if (kCap && poly) {
                         const float2 z = fmul2(make_float2(s[c], s[c + 1]), make_float2(s[c], s[c + 1]));
                         f = ffma2(z, make_float2(kp[3], kp[3]), make_float2(kp[2], kp[2]));
                         f = ffma2(z, f, make_float2(kp[1], kp[1]));

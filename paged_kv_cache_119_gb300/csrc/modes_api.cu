@@ -296,9 +296,12 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
         max_global_len = 0;
     const int qlen = decode ? 1 : max_query_len;
     Plan pl = decode ? plan_heads(s) : plan_rows(s, qlen, kChunkRowsMax);
+    AttnMode mode = kMod;
+    if (pl.family == Family::kChunk)             // the one kernel built for each set of modifiers
+        mode = softcap > 0.f ? (alibi_slopes ? kModBoth : kModCap) : (alibi_slopes ? kModSlope : kMod);
     const int length =
         (int)std::min<int64_t>(seen_bound(max_context_len, window, max_global_len, qlen, pl.tile), INT32_MAX);
-    choose_split(pl, s, kMod, num_seqs, length, partition_size);
+    choose_split(pl, s, mode, num_seqs, length, partition_size);
     if ((int64_t)s.num_kv_heads * pl.chunks > 65535)
         return PA_ERR_INVALID;
 
@@ -413,7 +416,7 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
             return PA_ERR_CUDA;
         d.seq_order = order;
     }
-    e = launch(s, kMod, pl, d, c, tk, tv,
+    e = launch(s, mode, pl, d, c, tk, tv,
                dim3(d.max_parts, s.num_kv_heads * pl.chunks, num_seqs), st);
     if (e == cudaSuccess && pl.partition > 0)
         e = launch_mod_merge(d, s.q_dtype, s.head_dim, pl.tile, st);

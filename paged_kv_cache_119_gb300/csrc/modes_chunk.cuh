@@ -41,8 +41,13 @@ bool chunk_variant(int head_dim, int block_size, F&& f)
 template <typename T, bool F8, typename F>
 bool chunk_any_mode(AttnMode mode, int head_dim, int block_size, F&& f)
 {
-    if (mode == kMod)
-        return chunk_variant<T, F8, kMod>(head_dim, block_size, f);
+    switch (mode) {
+    case kMod: return chunk_variant<T, F8, kMod>(head_dim, block_size, f);
+    case kModCap: return chunk_variant<T, F8, kModCap>(head_dim, block_size, f);
+    case kModSlope: return chunk_variant<T, F8, kModSlope>(head_dim, block_size, f);
+    case kModBoth: return chunk_variant<T, F8, kModBoth>(head_dim, block_size, f);
+    default: break;
+    }
     return mode == kPrefix && chunk_variant<T, F8, kPrefix>(head_dim, block_size, f);
 }
 

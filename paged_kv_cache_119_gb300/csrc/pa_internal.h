@@ -33,7 +33,21 @@ constexpr int kAutoPartitionTokens = 512;
 //            group's first sequence) attend over the tokens they share, no causal limit;
 //            writes partial rows only
 //   kSuffix  each sequence's own tokens after its shared prefix; writes partial rows only
-enum AttnMode : int { kPlain = 0, kMod = 1, kPrefix = 2, kSuffix = 3 };
+//   kModCap, kModSlope, kModBoth   chunk_attn_kernel only: kMod with a cap, slopes or both,
+//            where its kMod has neither (code for all at once spilled registers: 648 against
+//            523 us on 4 x 512 tokens of 8192 without a cap or slopes)
+enum AttnMode : int {
+    kPlain = 0,
+    kMod = 1,
+    kPrefix = 2,
+    kSuffix = 3,
+    kModCap = 4,
+    kModSlope = 5,
+    kModBoth = 6
+};
+__host__ __device__ constexpr bool is_mod(int mode) { return mode == kMod || mode >= kModCap; }
+__host__ __device__ constexpr bool has_cap(int mode) { return mode == kModCap || mode == kModBoth; }
+__host__ __device__ constexpr bool has_slope(int mode) { return mode == kModSlope || mode == kModBoth; }
 
 // Modified scores (score_mods.cuh), in base-2 units.
 struct ScoreMods {
