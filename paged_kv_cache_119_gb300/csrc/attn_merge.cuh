@@ -130,6 +130,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mod_reduce_kernel(const Deco
     } else {
         // the rows of the CTA that served this one decide which tiles it read
         const int R = (int)(row - qs0) * p.group + h % p.group;
+        if (((int64_t)s * p.num_kv_heads + h / p.group) * p.chunks + R / p.rows_per_cta < p.whole_units)
+            return;                                // one CTA did it all and wrote the output
         const int R0 = R / p.rows_per_cta * p.rows_per_cta;
         const int last = min(n - 1, (R0 + p.rows_per_cta - 1) / p.group);
         const TileOrder t =

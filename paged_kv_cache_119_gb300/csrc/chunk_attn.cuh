@@ -299,11 +299,22 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int seq = blockIdx.z;
-    const int kvh = blockIdx.y / p.m_tiles;
-    const int mt = blockIdx.y - kvh * p.m_tiles;
-    const int part = blockIdx.x;
-    const bool split = MODE == kPrefix || p.partition_tokens > 0;
+    // Unit (sequence, kv head, row tile) and partition of the CTA.  With modified scores the grid
+    // is one-dimensional: the first p.whole_units units are one CTA each, the others are cut
+    // into partitions (p.max_parts CTAs each).
+    int unit_y = blockIdx.y, seq = blockIdx.z, part = blockIdx.x;
+    bool split = MODE == kPrefix || p.partition_tokens > 0;
+    if constexpr (kIsMod) {
+        const int b = (int)blockIdx.x, cut = b - p.whole_units;
+        const int per_seq = p.num_kv_heads * p.m_tiles;
+        const int unit = cut < 0 ? b : p.whole_units + cut / p.max_parts;
+        split = split && cut >= 0;
+        part = split ? cut % p.max_parts : 0;
+        seq = unit / per_seq;
+        unit_y = unit - seq * per_seq;
+    }
+    const int kvh = unit_y / p.m_tiles;
+    const int mt = unit_y - kvh * p.m_tiles;
     const int G = p.group;
     const int TT = p.rows_tokens;
 
@@ -316,7 +327,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     const int L = MODE == kPrefix ? p.prefix_lens[tseq] : p.context_lens[seq];
     if (!rows_sane || L < 0 || L > p.max_context_len || n > p.max_query_len ||
         (MODE == kPrefix ? L % BS != 0 : n > L)) {
-        if (part == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+        if (part == 0 && unit_y == 0 && threadIdx.x == 0)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
         if (!split && rows_sane && part == 0 && mt == 0) {
             // the sequence's rows of this kv head's query heads become NaN
@@ -333,7 +344,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         }
         return;
     }
-    if (seq == p.num_seqs - 1 && part == 0 && blockIdx.y == 0 && threadIdx.x == 0 &&
+    if (seq == p.num_seqs - 1 && part == 0 && unit_y == 0 && threadIdx.x == 0 &&
         (int64_t)qs1 != p.num_rows)
         atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);   // rows after the last chunk belong to no one
     const int j0 = mt * TT;
@@ -500,6 +511,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 const unsigned char* raw = smem + Sm::kRawOff + r * Sm::kRawStage;
                 unsigned char* dst = smem + Sm::kStageOff + st * Sm::kStageBytes;
                 const int tb = tile_token(it);
+                const bool all_seen = !kIsMod || tile_seen(seen, tb, NT);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll 4
@@ -508,7 +520,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                         const int c = item & 7;
                         uint4 w = *reinterpret_cast<const uint4*>(
                             raw + kv * Sm::kRawTile + t * 128 + ((c ^ (t & 7)) << 4));
-                        if (kIsMod && kv == 1 && !is_seen(seen, tb + t))
+                        if (kIsMod && kv == 1 && !all_seen && !is_seen(seen, tb + t))
                             w = make_uint4(0u, 0u, 0u, 0u);
                         unsigned char* row =
                             dst + kv * Sm::kKBytes + (c >> 2) * Sm::kKVHalf + t * 128;
@@ -550,6 +562,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 }
                 const int tb = tile_token(it);
                 const int nv = min(NT, t1 - tb);              // rows inside the range
+                const bool all_seen = kIsMod && tile_seen(seen, tb, NT);
                 unsigned char* vt = smem + Sm::kStageOff + st * Sm::kStageBytes + Sm::kKBytes;
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
@@ -558,7 +571,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     uint4* chunk = reinterpret_cast<uint4*>(vt + (item / (NT * 8)) * Sm::kKVHalf +
                                                             w * 16);
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if ((w >> 3) < nv && (!kIsMod || is_seen(seen, tb + (w >> 3)))) {
+                    if (kIsMod ? all_seen || is_seen(seen, tb + (w >> 3)) : (w >> 3) < nv) {
                         const uint4 b = *chunk;
                         const uint32_t in[4] = {b.x, b.y, b.z, b.w};
                         uint32_t o[4];
@@ -588,7 +601,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     break;
                 }
                 const int tb = tile_token(it);
-                if (tb + NT > t1 || (tb < seen.lo && tb + NT > seen.glob)) {
+                if (!tile_seen(seen, tb, NT)) {
                     unsigned char* vt = smem + Sm::kStageOff + st * Sm::kStageBytes + Sm::kKBytes;
                     for (int item = ct; item < NT * 8 * Sm::kHalves; item += 32 * kChunkConvWarps) {
                         const int w = item % (NT * 8);
@@ -829,10 +842,14 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                             mul = 1.f;
                         }
                         if (!whole) {
-                            const int g0 = row_valid ? gl : NT;
+                            // bits of the visible columns (a row past the chunk: all)
+                            auto below = [](int n) -> uint64_t {      // bits 0 .. n - 1
+                                return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+                            };
+                            const uint64_t vis = row_valid ? below(gl) | (below(lim + 1) & ~below(lo)) : ~0ull;
 #pragma unroll
                             for (int c = 0; c < NT; ++c)
-                                s[c] = (c < g0 || (c >= lo && c <= lim)) ? s[c] : -INFINITY;
+                                s[c] = (vis >> c) & 1ull ? s[c] : -INFINITY;
                         }
                         smax = row_max(s);
                     }

@@ -104,6 +104,7 @@ struct DecodeParams {
     int part_base;
     int tile_align;              // merge of the shared prefix: block_size
     int rows_per_cta;            // kMod: (token, head) rows of a kv head one CTA serves
+    int whole_units;             // kMod merge: (sequence, kv head, row tile) units without parts
 };
 
 // Longest-first dispatch of a one-pass CUDA-core decode with more CTAs than one wave:
@@ -300,6 +301,7 @@ struct ChunkParams {
     int out_f32;
     float scale_log2;
     ScoreMods mods;              // kMod
+    int whole_units;             // kMod: (sequence, kv head, row tile) units that are not split
     const int32_t* prefix_lens;  // kPrefix: shared tokens of each sequence
 };
 cudaError_t launch_chunk_attention(const ChunkParams& p, pa_dtype dtype, int head_dim,

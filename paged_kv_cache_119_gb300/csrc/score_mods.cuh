@@ -91,4 +91,10 @@ __device__ __forceinline__ bool is_seen(const Seen& s, int t)
     return t < s.glob || (t >= s.lo && t < s.end);
 }
 
+// Whether every token of [a, a + n) is seen.
+__device__ __forceinline__ bool tile_seen(const Seen& s, int a, int n)
+{
+    return a + n <= s.glob || (a >= s.lo && a + n <= s.end);
+}
+
 }  // namespace pa

@@ -192,6 +192,19 @@ def test_chunk_long_window_automatic_split():
         compare(c, False, CHUNK_TOL, softcap=30.0)
 
 
+@pytest.mark.parametrize("mods", [dict(), dict(window=600, glob=100)], ids=str)
+@pytest.mark.parametrize("dtype,fp8", [(torch.float16, False), (torch.bfloat16, False), (torch.bfloat16, True)])
+def test_chunk_last_wave_is_cut(dtype, fp8, mods):
+    """168 units of one CTA each on 152 SMs: the last ones are split and merged, the others
+    write their rows themselves; an empty chunk and a short context among the split ones."""
+    lens = [1100 + 3 * i for i in range(17)] + [1300, 40, 1250, 1030]
+    new = [40 - i % 3 for i in range(17)] + [40, 40, 0, 37]
+    glob = [mods["glob"]] * len(lens) if "glob" in mods else None
+    c = build(21, lens, new, 8, 8, 128, 16, dtype, fp8, mods.get("window", 0), glob)
+    compare(c, False, CHUNK_TOL, softcap=30.0, max_global=mods.get("glob"))
+    compare(c, False, CHUNK_TOL, slopes=slopes_for(8), max_global=mods.get("glob"))
+
+
 @pytest.mark.parametrize("softcap", [0.01, 5.0, 1e6])
 def test_chunk_caps_and_scales(softcap):
     for fp8 in (False, True):
