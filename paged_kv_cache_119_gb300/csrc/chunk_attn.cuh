@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     constexpr bool kBf16 = DType<TM>::id == PA_BF16;
     static_assert(NT % BS == 0 && D % 64 == 0, "block_size 16/32, head_dim 64/128");
 
+    overlap_passes<MODE>(p.num_seqs);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

@@ -145,6 +145,8 @@ __global__ void __launch_bounds__(kDecodeThreads)
     // copy a tile to registers and release its stage early when K + V take <= 64 registers
     constexpr bool kEarlyRelease = 2 * BS * E * (int)sizeof(TK) / 4 <= 64;
 
+    if (overlap_passes<MODE>(p.num_seqs))
+        return;
     extern __shared__ __align__(128) unsigned char smem[];
     TK* ring = reinterpret_cast<TK*>(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Smem::kBarOffset);

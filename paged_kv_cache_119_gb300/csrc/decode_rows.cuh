@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     static_assert(NCW % RW == 0 && NSTAGE % NCW == 0, "each ring stage belongs to one warp of a row group");
     static_assert((BS == 16 || BS == 32) && D % 64 == 0, "block_size 16/32, head_dim 64/128");
 
+    if (overlap_passes<MODE>(p.num_seqs))
+        return;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

@@ -193,6 +193,8 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
     constexpr int BPT = kTc8Tok / BS;           // cache blocks per tile
     static_assert(BS == 16 || BS == 32, "block_size 16 or 32");
 
+    if (overlap_passes<MODE>(p.num_seqs))
+        return;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

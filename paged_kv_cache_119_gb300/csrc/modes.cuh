@@ -11,6 +11,14 @@ namespace pa {
 
 constexpr int kMaxCachedDevices = 64;
 
+// Whether the kernel may start while the one before it in the stream still runs.
+inline bool may_overlap(const DecodeParams& p) { return p.overlap != 0; }
+template <typename T>
+bool may_overlap(const T&)
+{
+    return false;
+}
+
 // Launches one kernel variant V (kernel(), configure(), smem_bytes, threads) over
 // (partitions, kv heads * chunks, sequences or groups).
 template <typename V, typename... Args>
@@ -19,8 +27,19 @@ cudaError_t launch_mode_variant(dim3 grid, cudaStream_t stream, const Args&... a
     cudaError_t err = V::configure();
     if (err != cudaSuccess)
         return err;
-    V::kernel()<<<grid, V::kThreads, V::kSmem, stream>>>(args...);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(V::kThreads);
+    cfg.dynamicSmemBytes = V::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    if ((may_overlap(args) || ...)) {
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, V::kernel(), args...);
 }
 
 // Resident CTAs per SM of variant V (0 if unknown).  Asked once per device: the query costs

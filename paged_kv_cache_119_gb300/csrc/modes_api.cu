@@ -483,7 +483,8 @@ int prefix_impl(void* out, pa_dtype out_dtype, const void* q, const Shape& s, co
                                scale, partition_size);
     if (ok <= 0)
         return ok;
-    if (s.group() > 128 || max_prefix_len < 0 || max_suffix_len < 0 ||
+    // (the suffix grid has one z-slice more than sequences)
+    if (s.group() > 128 || num_seqs > 65534 || max_prefix_len < 0 || max_suffix_len < 0 ||
         (int64_t)max_prefix_len + max_suffix_len > kMaxContext)
         return PA_ERR_INVALID;
     if (max_prefix_len % s.block_size != 0 || max_prefix_len > block_table_stride * s.block_size)
@@ -598,9 +599,10 @@ int prefix_impl(void* out, pa_dtype out_dtype, const void* q, const Shape& s, co
     }
     d.chunks = pl.suffix.chunks;
     d.partition_tokens = pl.suffix.partition;
+    d.overlap = pl.prefix_parts > 0 ? 1 : 0;
     if (pl.suffix_parts > 0) {
         e = launch(s, kSuffix, pl.suffix, d, ChunkParams{}, tk, tv,
-                   dim3(pl.suffix_parts, s.num_kv_heads * pl.suffix.chunks, num_seqs), st);
+                   dim3(pl.suffix_parts, s.num_kv_heads * pl.suffix.chunks, num_seqs + d.overlap), st);
         if (e != cudaSuccess)
             return PA_ERR_CUDA;
     }

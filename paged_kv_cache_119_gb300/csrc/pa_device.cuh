@@ -173,6 +173,18 @@ __device__ __forceinline__ float ex2_approx(float x)
     return y;
 }
 
+// Programmatic launches: lets the next kernel of the stream start while this grid still runs
+// (once every CTA has called this or left), and waits for the grids this one was allowed to
+// overlap.
+__device__ __forceinline__ void grid_launch_dependents()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait_prerequisites()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Named barrier over a subset of the CTA's warps.
 __device__ __forceinline__ void named_barrier(int id, int threads)
 {

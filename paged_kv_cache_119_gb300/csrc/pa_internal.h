@@ -102,6 +102,7 @@ struct DecodeParams {
     int max_prefix_len;
     int max_suffix_len;
     int part_base;
+    int overlap;                 // host: launch beside the kernel before (kSuffix)
     int tile_align;              // merge of the shared prefix: block_size
     int rows_per_cta;            // kMod: (token, head) rows of a kv head one CTA serves
     int whole_units;             // kMod merge: (sequence, kv head, row tile) units without parts

@@ -14,6 +14,26 @@
 
 namespace pa {
 
+// The two passes of a shared-prefix decode overlap: neither needs the other.  The prefix pass
+// lets the suffix pass start as soon as all its CTAs have; the suffix grid has one z-slice more
+// than sequences, whose first CTA waits for the prefix pass, so that the suffix grid does not
+// complete before it and the merge, an ordinary launch behind the suffix pass, sees both.
+// Returns true for a CTA of that slice, which has nothing else to do.
+template <int MODE>
+__device__ __forceinline__ bool overlap_passes(int num_seqs)
+{
+    if constexpr (MODE == kPrefix)
+        grid_launch_dependents();
+    if constexpr (MODE == kSuffix) {
+        if ((int)blockIdx.z >= num_seqs) {
+            if (blockIdx.x == 0 && blockIdx.y == 0)
+                grid_wait_prerequisites();
+            return true;
+        }
+    }
+    return false;
+}
+
 // 1 / x on the MUFU unit (relative error about 2^-23; 1 / inf = 0).
 __device__ __forceinline__ float rcp_approx(float x)
 {
