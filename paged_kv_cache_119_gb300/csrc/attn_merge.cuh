@@ -107,6 +107,7 @@ __device__ __forceinline__ void store_piece(const DecodeParams& p, int64_t out_r
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) mod_reduce_kernel(const DecodeParams p, int tile_tokens)
 {
+    grid_wait_prerequisites();                     // the parts are in place
     const int lane = threadIdx.x & 31;
     const int64_t out_row = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
     if (out_row >= p.num_rows * p.num_q_heads)
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     prefix_reduce_kernel(const DecodeParams p, const int32_t* group_start, int num_groups,
                          int max_group, int prefix_part)
 {
+    grid_wait_prerequisites();                     // the parts are in place
     const int lane = threadIdx.x & 31;
     const int64_t out_row = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
     if (out_row >= (int64_t)p.num_seqs * p.num_q_heads)

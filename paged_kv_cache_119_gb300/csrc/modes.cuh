@@ -11,6 +11,25 @@ namespace pa {
 
 constexpr int kMaxCachedDevices = 64;
 
+// Launches a kernel; with overlap it may start before the kernel in front of it has completed
+// (as soon as all CTAs of that one have allowed it or left) and has to wait for what it needs.
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, bool overlap,
+                          cudaStream_t stream, const Args&... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Whether the kernel may start while the one before it in the stream still runs.
 inline bool may_overlap(const DecodeParams& p) { return p.overlap != 0; }
 template <typename T>
@@ -27,19 +46,8 @@ cudaError_t launch_mode_variant(dim3 grid, cudaStream_t stream, const Args&... a
     cudaError_t err = V::configure();
     if (err != cudaSuccess)
         return err;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(V::kThreads);
-    cfg.dynamicSmemBytes = V::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    if ((may_overlap(args) || ...)) {
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-    }
-    return cudaLaunchKernelEx(&cfg, V::kernel(), args...);
+    return launch_behind(V::kernel(), grid, dim3(V::kThreads), V::kSmem, (may_overlap(args) || ...),
+                         stream, args...);
 }
 
 // Resident CTAs per SM of variant V (0 if unknown).  Asked once per device: the query costs

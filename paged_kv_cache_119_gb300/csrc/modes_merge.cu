@@ -1,5 +1,6 @@
 // modes_merge.cu -- launches the merges of attn_merge.cuh.
 #include "attn_merge.cuh"
+#include "modes.cuh"
 
 namespace pa {
 
@@ -31,9 +32,8 @@ cudaError_t launch_mod_merge(const DecodeParams& p, pa_dtype q_dtype, int head_d
     if (ctas > INT32_MAX)
         return cudaErrorInvalidValue;
     return by_type<true>(q_dtype, head_dim, [&](auto t, auto d) {
-        mod_reduce_kernel<decltype(t), d.value>
-            <<<(unsigned)ctas, 32 * kMergeWarps, 0, stream>>>(p, tile_tokens);
-        return cudaGetLastError();
+        return launch_behind(mod_reduce_kernel<decltype(t), d.value>, dim3((unsigned)ctas),
+                             dim3(32 * kMergeWarps), 0, true, stream, p, tile_tokens);
     });
 }
 
@@ -43,10 +43,9 @@ cudaError_t launch_prefix_merge(const DecodeParams& p, pa_dtype q_dtype, int hea
 {
     const int64_t ctas = ((int64_t)p.num_seqs * p.num_q_heads + kMergeWarps - 1) / kMergeWarps;
     return by_type<false>(q_dtype, head_dim, [&](auto t, auto d) {
-        prefix_reduce_kernel<decltype(t), d.value>
-            <<<(unsigned)ctas, 32 * kMergeWarps, 0, stream>>>(
-                p, group_start, num_groups, max_group, prefix_part);
-        return cudaGetLastError();
+        return launch_behind(prefix_reduce_kernel<decltype(t), d.value>, dim3((unsigned)ctas),
+                             dim3(32 * kMergeWarps), 0, true, stream, p, group_start, num_groups,
+                             max_group, prefix_part);
     });
 }
 

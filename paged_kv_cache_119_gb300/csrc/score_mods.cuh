@@ -17,7 +17,7 @@ namespace pa {
 // The two passes of a shared-prefix decode overlap: neither needs the other.  The prefix pass
 // lets the suffix pass start as soon as all its CTAs have; the suffix grid has one z-slice more
 // than sequences, whose first CTA waits for the prefix pass, so that the suffix grid does not
-// complete before it and the merge, an ordinary launch behind the suffix pass, sees both.
+// complete before it and the merge, which waits for the suffix grid, sees both.
 // Returns true for a CTA of that slice, which has nothing else to do.
 template <int MODE>
 __device__ __forceinline__ bool overlap_passes(int num_seqs)
