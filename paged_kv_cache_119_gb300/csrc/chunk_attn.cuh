@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     // Unit (sequence, kv head, row tile) and partition of the CTA.  With modified scores the grid
     // is one-dimensional: the first p.whole_units units are one CTA each, the others are cut
     // into partitions (p.max_parts CTAs each).
-    int unit_y = blockIdx.y, seq = blockIdx.z, part = blockIdx.x;
+    unsigned unit_y = blockIdx.y;
+    int seq = blockIdx.z, part = blockIdx.x;
     bool split = MODE == kPrefix || p.partition_tokens > 0;
     if constexpr (kIsMod) {
         const int b = (int)blockIdx.x, cut = b - p.whole_units;
@@ -369,12 +370,14 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     }
     int t1 = t_end;
     if constexpr (!kIsMod) {
+        if (MODE == kPrefix && t_end <= 0)
+            return;                              // an empty shared prefix
         if (p.partition_tokens > 0) {
             t0 = part * p.partition_tokens;
+            if (t0 >= t_end)
+                return;
             t1 = min(t_end, t0 + p.partition_tokens);
         }
-        if (t0 >= t_end)
-            return;                              // (unsplit: an empty shared prefix)
         ntiles = (t1 - t0 + NT - 1) / NT;        // >= 1
     }
     // first token of tile it
@@ -440,10 +443,12 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         for (int it = 0; it < ntiles; ++it) {
             const int st = it % NP;
             const int b0 = tile_token(it) / BS;
-            bool want = lane < min(BPT, blk_end - b0);
-            if constexpr (kIsMod)          // only blocks that hold a seen token
+            int nb = min(BPT, blk_end - b0);
+            bool want = lane < nb;
+            if constexpr (kIsMod) {        // only blocks that hold a seen token
                 want = want && any_seen(seen, (b0 + lane) * BS, min((b0 + lane) * BS + BS, t1));
-            const int nb = __popc(__ballot_sync(kFullMask, want));
+                nb = __popc(__ballot_sync(kFullMask, want));
+            }
             int pbn = -1;
             bool valid = false;
             if (want) {

@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
     Seen seen{0, 0, 0};
     TileOrder order{0, 0, 0};
     if constexpr (CH) {
-        if (MODE != kSuffix && seq == (int)gridDim.z - 1 && part == 0 && blockIdx.y == 0 &&
+        if (MODE != kSuffix && seq == (MODE == kPrefix ? (int)gridDim.z : p.num_seqs) - 1 && part == 0 && blockIdx.y == 0 &&
             threadIdx.x == 0 && (int64_t)qs0 + n != p.num_rows)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);   // rows after the last chunk belong to no one
         if (R0 / p.group >= n)
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         ntiles = split ? min(order.count - c0, p.partition_tokens / kTc8Tok) : order.count;
     } else {
         if (p.partition_tokens > 0) {
-            t0 += part * p.partition_tokens;
+            t0 = start + part * p.partition_tokens;
             if (t0 >= t_end)
                 return;
             t1 = min(t_end, t0 + p.partition_tokens);
@@ -365,22 +365,28 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
             return i < nblk && any_seen(seen, b * BS, min(b * BS + BS, t1));
         };
         auto entry = [&](int i) -> int {
-            if constexpr (MODE == kMod)
-                return wanted(i) ? __ldg(bt_row + order(c0 + i / BPT) * BPT + i % BPT) : -1;
-            else
-                return i < nblk ? __ldg(bt_row + blk_first + i) : -1;
+            return wanted(i) ? __ldg(bt_row + order(c0 + i / BPT) * BPT + i % BPT) : -1;
         };
         // block-table entries 32 at a time (4 or 8 tiles), the next 32 in flight while the
         // current ones are used
-        int cur = entry(lane);
-        int nxt = entry(32 + lane);
+        int cur, nxt;
+        if constexpr (MODE == kMod) {
+            cur = entry(lane);
+            nxt = entry(32 + lane);
+        } else {
+            cur = lane < nblk ? __ldg(bt_row + blk_first + lane) : -1;
+            nxt = 32 + lane < nblk ? __ldg(bt_row + blk_first + 32 + lane) : -1;
+        }
         int issued = 0;
         for (int it = 0; it < ntiles; ++it) {
             const int st = it % NST;
             const int lb = it * BPT;               // first block of the tile, CTA-relative
             if (it > 0 && (lb & 31) == 0) {
                 cur = nxt;
-                nxt = entry(lb + 32 + lane);
+                if constexpr (MODE == kMod)
+                    nxt = entry(lb + 32 + lane);
+                else
+                    nxt = lb + 32 + lane < nblk ? __ldg(bt_row + blk_first + lb + 32 + lane) : -1;
             }
             int nb = min(BPT, nblk - lb);
             const int e = __shfl_sync(kFullMask, cur, ((lb & 31) + lane) & 31);
@@ -701,7 +707,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                         if (!is_seen(seen, tb + j / 8))
                             vt[j] = make_uint4(0u, 0u, 0u, 0u);
                 }
-                const int nv = min(kTc8Tok, t1 - tb);    // rows of the range
+                const int nv = MODE == kMod ? min(kTc8Tok, t1 - tb) : t1 - tb;   // rows of the range
                 uint4* vz = reinterpret_cast<uint4*>(smem + st * Sm::kStage + Sm::kTile + nv * 128);
                 for (int j = tl; j < (kTc8Tok - nv) * 8; j += kTc8Tok)
                     vz[j] = make_uint4(0u, 0u, 0u, 0u);
