@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     Seen seen{0, 0, 0};
     TileOrder order{0, 0, 0};
     if constexpr (CH) {
-        if (MODE != kSuffix && seq == (int)gridDim.z - 1 && part == 0 && blockIdx.y == 0 &&
+        if (MODE != kSuffix && seq == (MODE == kPrefix ? (int)gridDim.z : p.num_seqs) - 1 && part == 0 && blockIdx.y == 0 &&
             threadIdx.x == 0 && (int64_t)qs0 + n != p.num_rows)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);   // rows after the last chunk belong to no one
         if (R0 / p.group >= n)
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
         nblk = ntiles * BPT;
     } else {
         if (p.partition_tokens > 0) {
-            t0 += part * p.partition_tokens;
+            t0 = start + part * p.partition_tokens;
             if (t0 >= t_end)
                 return;
             t1 = min(t_end, t0 + p.partition_tokens);
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     // kMod: whether block b of the context holds a seen token (the others are neither read
     // nor checked: an engine may have freed them)
     auto block_seen = [&](int b) -> bool {
-        return MODE != kMod || any_seen(seen, b * BS, min(b * BS + BS, t1));
+        return any_seen(seen, b * BS, min(b * BS + BS, t1));
     };
 
     if (threadIdx.x == 0) {
@@ -372,14 +372,19 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
         // ------------------------------------------------------------------ producer
         const int32_t* bt_row = p.block_tables + (int64_t)tseq * p.bt_stride + (MODE == kMod ? 0 : jb);
         const uint64_t policy = l2_evict_first_policy();
-        int next = (lane < nblk && block_seen(block_of(lane))) ? __ldg(bt_row + block_of(lane)) : 0;
+        int next = (lane < nblk && (MODE != kMod || block_seen(block_of(lane)))) ? __ldg(bt_row + block_of(lane))
+                                                                                  : 0;
         bool aborted = false;
         // block-table entries 32 at a time (BPT divides 32, so no tile straddles two
         // batches), the next 32 in flight while the current ones are used
         for (int base = 0; base < nblk && !aborted; base += 32) {
             const int cur = next;
-            if (base + 32 + lane < nblk && block_seen(block_of(base + 32 + lane)))
-                next = __ldg(bt_row + block_of(base + 32 + lane));
+            if constexpr (MODE == kMod) {
+                if (base + 32 + lane < nblk && block_seen(block_of(base + 32 + lane)))
+                    next = __ldg(bt_row + block_of(base + 32 + lane));
+            } else if (base + 32 + lane < nblk) {
+                next = __ldg(bt_row + base + 32 + lane);
+            }
             const int cnt = min(32, nblk - base);
             for (int i = 0; i < cnt; i += BPT) {
                 int pbn[BPT];
@@ -388,7 +393,10 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                     pbn[b] = __shfl_sync(kFullMask, cur, i + b);   // i + b <= 31
                 const int nb = min(BPT, cnt - i);                  // blocks of the tile in range
                 auto want = [&](int b) -> bool {                   // of those, the ones to read
-                    return b < nb && block_seen(block_of(base + i + b));
+                    if constexpr (MODE == kMod)
+                        return b < nb && block_seen(block_of(base + i + b));
+                    else
+                        return b < nb;
                 };
                 const int it = (base + i) / BPT;
                 const int stage = it % NSTAGE;
@@ -698,7 +706,10 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                 ragged = ragged || (tb + 16 * mb < seen.lo && tb + 16 * mb + 16 > seen.glob);
             // token t of the tile is in range and seen
             auto live_tok = [&](int t) -> bool {
-                return t < nvalid && (MODE != kMod || is_seen(seen, tb + t));
+                if constexpr (MODE == kMod)
+                    return t < nvalid && is_seen(seen, tb + t);
+                else
+                    return t < nvalid;
             };
             uint32_t vpair[8];   // direct E4M3: the two m-blocks 2j, 2j+1 read together
 #pragma unroll
