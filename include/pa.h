@@ -457,7 +457,12 @@ int pa_chunk_attention_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtyp
  * All other arguments, kinds of cache, output types, checks and errors are those of
  * pa_decode, pa_decode_fp8, pa_chunk_attention and pa_chunk_attention_fp8;
  * max_context_len is at most 2^30.  Workspace: pa_decode_workspace_bytes /
- * pa_chunk_workspace_bytes of the same sizes.  out overlaps no input.
+ * pa_chunk_workspace_bytes of the same sizes; with a window, in place of max_context_len, of
+ * the tokens that a sequence's rows can have to read, in tiles of 128:
+ *   128 * (ceil(max_global_len / 128) + (window + max_query_len + 125) / 128 + 1),
+ * where that is less (max_query_len 1 in a decode call; integer division).  A chunk call's
+ * rounding may depend on whether it has a workspace: with one, a last wave that would leave
+ * most SMs idle is split.  out overlaps no input.
  */
 int pa_decode_mod(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
                   const void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,

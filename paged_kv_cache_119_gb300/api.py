@@ -561,16 +561,18 @@ def _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_
 
 
 def _scratch(need, workspace, q, stream):
-    """(workspace to keep alive, pointer, bytes): the caller's, or `need` fresh bytes that a
-    call on another stream than the current one may go on using."""
+    """(workspace to keep alive, pointer, bytes): the caller's, or `need` fresh bytes that
+    belong to the stream of the call (memory of another stream could still be in use there)."""
     if workspace is None:
         if not need:
             return None, 0, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(_stream(stream), device=q.device)
-            workspace.record_stream(stream)
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif workspace.device != q.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -606,12 +608,17 @@ def _mod(fn, out, q, k_cache, v_cache, scales, block_tables, context_lens, query
             max_global_len = W * block_size
     if max_context_len is None:
         max_context_len = W * block_size
-    if query_start is None:
-        need = pa_decode_workspace_bytes(S, Hq, D, max_context_len, block_size, partition_size) \
-            if partition_size >= 0 else 0
+    read = max_context_len                       # tokens a sequence's rows can have to read
+    if window > 0:                               # in whole tiles of at most 128
+        run = window + (1 if query_start is None else int(max_query_len)) - 1
+        first = min(int(max_global_len or 0), read)
+        read = min(read, 128 * (-(-first // 128) + (run + 126) // 128 + 1))
+    if partition_size < 0 or workspace is not None:
+        need = 0
+    elif query_start is None:
+        need = pa_decode_workspace_bytes(S, Hq, D, read, block_size, partition_size)
     else:
-        need = pa_chunk_workspace_bytes(R, Hq, D, max_context_len, partition_size) \
-            if partition_size >= 0 else 0
+        need = pa_chunk_workspace_bytes(R, Hq, D, read, partition_size)
     workspace, ws_ptr, ws_bytes = _scratch(need, workspace, q, stream)
     args = [out.data_ptr(), _dtype(out), q.data_ptr()]
     if scales:

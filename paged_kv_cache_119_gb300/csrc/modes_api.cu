@@ -386,6 +386,9 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
         d.part_o = static_cast<float*>(workspace);
         d.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_off);
     }
+    const int64_t ctas = whole_units + (pl.units - whole_units) * d.max_parts;
+    if (ctas > INT32_MAX)                        // (one-dimensional grid of the chunk kernel)
+        return PA_ERR_INVALID;
     d.err = device_error_word();
     if (!d.err)
         return PA_ERR_CUDA;
@@ -438,7 +441,7 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
         d.seq_order = order;
     }
     const dim3 grid = pl.family == Family::kChunk
-                          ? dim3((unsigned)(whole_units + (pl.units - whole_units) * d.max_parts))
+                          ? dim3((unsigned)ctas)
                           : dim3(d.max_parts, s.num_kv_heads * pl.chunks, num_seqs);
     e = launch(s, mode, pl, d, c, tk, tv, grid, st);
     if (e == cudaSuccess && pl.partition > 0)
@@ -607,7 +610,7 @@ int prefix_impl(void* out, pa_dtype out_dtype, const void* q, const Shape& s, co
             return PA_ERR_CUDA;
     }
     e = launch_prefix_merge(d, s.q_dtype, s.head_dim, group_start, num_groups, max_group_size,
-                            pl.prefix.partition, st);
+                            pl.prefix.partition, pl.prefix_parts + pl.suffix_parts > 0, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

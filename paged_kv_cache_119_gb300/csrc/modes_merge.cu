@@ -39,12 +39,12 @@ cudaError_t launch_mod_merge(const DecodeParams& p, pa_dtype q_dtype, int head_d
 
 cudaError_t launch_prefix_merge(const DecodeParams& p, pa_dtype q_dtype, int head_dim,
                                 const int32_t* group_start, int num_groups, int max_group,
-                                int prefix_part, cudaStream_t stream)
+                                int prefix_part, bool behind, cudaStream_t stream)
 {
     const int64_t ctas = ((int64_t)p.num_seqs * p.num_q_heads + kMergeWarps - 1) / kMergeWarps;
     return by_type<false>(q_dtype, head_dim, [&](auto t, auto d) {
         return launch_behind(prefix_reduce_kernel<decltype(t), d.value>, dim3((unsigned)ctas),
-                             dim3(32 * kMergeWarps), 0, true, stream, p, group_start, num_groups,
+                             dim3(32 * kMergeWarps), 0, behind, stream, p, group_start, num_groups,
                              max_group, prefix_part);
     });
 }

@@ -389,7 +389,7 @@ cudaError_t launch_mod_merge(const DecodeParams& p, pa_dtype q_dtype, int head_d
                              cudaStream_t stream);
 cudaError_t launch_prefix_merge(const DecodeParams& p, pa_dtype q_dtype, int head_dim,
                                 const int32_t* group_start, int num_groups, int max_group,
-                                int prefix_part, cudaStream_t stream);
+                                int prefix_part, bool behind, cudaStream_t stream);
 
 // Sets the dynamic shared-memory limit of a kernel once per device and process.
 inline cudaError_t configure_once(const void* kernel, int smem_bytes)
