@@ -28,10 +28,17 @@ cudaError_t by_type(pa_dtype q_dtype, int head_dim, F&& f)
 cudaError_t launch_mod_merge(const DecodeParams& p, pa_dtype q_dtype, int head_dim, int tile_tokens,
                              cudaStream_t stream)
 {
-    const int64_t ctas = (p.num_rows * p.num_q_heads + kMergeWarps - 1) / kMergeWarps;
+    const bool cut = p.whole_units > 0;
+    const int64_t rows = cut ? ((int64_t)p.num_seqs * p.num_kv_heads * p.chunks - p.whole_units) * p.rows_per_cta
+                             : p.num_rows * p.num_q_heads;
+    const int64_t ctas = (rows + kMergeWarps - 1) / kMergeWarps;
     if (ctas > INT32_MAX)
         return cudaErrorInvalidValue;
     return by_type<true>(q_dtype, head_dim, [&](auto t, auto d) {
+        if constexpr (!std::is_same_v<decltype(t), float>)       // (the chunk kernel's types)
+            if (cut)
+                return launch_behind(mod_reduce_cut_kernel<decltype(t), d.value>, dim3((unsigned)ctas),
+                                     dim3(32 * kMergeWarps), 0, true, stream, p, tile_tokens);
         return launch_behind(mod_reduce_kernel<decltype(t), d.value>, dim3((unsigned)ctas),
                              dim3(32 * kMergeWarps), 0, true, stream, p, tile_tokens);
     });

@@ -22,7 +22,7 @@ namespace pa {
 template <int MODE>
 __device__ __forceinline__ bool overlap_passes(int num_seqs)
 {
-    if constexpr (MODE == kPrefix)
+    if constexpr (MODE != kPlain)
         grid_launch_dependents();
     if constexpr (MODE == kSuffix) {
         if ((int)blockIdx.z >= num_seqs) {

@@ -319,3 +319,36 @@ def test_captured_and_replayed_on_another_stream():
     torch.cuda.synchronize()
     eager = run(c, True, softcap=30.0, max_context_len=3000)
     assert torch.equal(out, eager) and torch.equal(out[1], want[1])
+
+
+@pytest.mark.parametrize("dtype,fp8", [(torch.float16, False), (torch.bfloat16, True)])
+def test_rows_without_a_sequence_stay_in_a_split_call(dtype, fp8):
+    c = build(22, [500, 800], [10, 20], 4, 1, 128, 16, dtype, fp8)
+    good = run(c, False, partition_size=128)
+    c.query_start[2] = 25
+    out = torch.full(c.q.shape, 7.0, dtype=torch.float32, device="cuda")
+    f = P.pa_chunk_attention_mod_fp8 if fp8 else P.pa_chunk_attention_mod
+    f(out, c.q, *c.pools, c.table, c.context_lens, c.query_start, c.scale, 1, 16, max_query_len=20,
+      max_context_len=800, partition_size=128)
+    torch.cuda.synchronize()
+    assert (out[25:] == 7.0).all() and torch.isfinite(out[:25]).all()
+    assert torch.equal(out[:10], good[:10])
+    assert P.pa_get_device_error() == 2
+
+
+def test_bad_sequences_in_a_cut_last_wave():
+    """As test_chunk_last_wave_is_cut, with lengths out of range among the units of one CTA and
+    among the split ones: their rows become NaN, all others stay as they are."""
+    lens = [1100 + 3 * i for i in range(17)] + [1300, 40, 1250, 1030]
+    new = [40 - i % 3 for i in range(17)] + [40, 40, 0, 37]
+    c = build(21, lens, new, 8, 8, 128, 16, torch.bfloat16)
+    good = run(c, False, softcap=30.0)
+    start = c.query_start.tolist()
+    bad = [2, 18, 20]
+    for s, L in zip(bad, (1301, -1, 36)):
+        c.context_lens[s] = L
+    out = run(c, False, softcap=30.0)
+    assert P.pa_get_device_error() == 2
+    for s in range(len(lens)):
+        rows = slice(start[s], start[s + 1])
+        assert torch.isnan(out[rows]).all() if s in bad else torch.equal(out[rows], good[rows])
