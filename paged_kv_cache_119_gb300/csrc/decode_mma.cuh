@@ -202,7 +202,7 @@ constexpr int mma_min_blocks() { return (sizeof(TK) == 1 && BS == 32) ? 3 : 4; }
 // verification, short chunks) -- instead of NH query heads of one token.
 // BPT: cache blocks per tile (a ring stage); the tile is TB = BS * BPT tokens.
 // MODE (with CH): kMod, chunk rows with modified scores (query_start null: one row per query
-// head of each sequence's last token); kPrefix, the rows of a group of sequences over the
+// head of each sequence's last token), kModBoth when they have a cap or slopes; kPrefix, the rows of a group of sequences over the
 // tokens they share (blockIdx.z = group); kSuffix, each sequence's query heads over its
 // tokens after the shared prefix.  kPrefix and kSuffix write partial rows only.
 template <typename T, typename TK, int D, int BS, int NH, int NSTAGE, bool CH = false, int BPT = 1,
@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     constexpr int TB = BS * BPT;      // tokens per tile
     using Sm = MmaSmem<TK, D, TB, NSTAGE>;
     constexpr bool kFp8 = Sm::kFp8;
+    constexpr bool kIsMod = is_mod(MODE);
     // tensor-core operand type: the query type for 16-bit caches; f16 for E4M3 caches
     // (an E4M3 code converts to f16 exactly in one instruction per pair)
     using TM = std::conditional_t<kFp8, __half, T>;
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     int qs0 = 0, n = 1, R0 = 0;
     if constexpr (CH) {
         R0 = (blockIdx.y % p.chunks) * NH;
-        if (MODE == kSuffix || (MODE == kMod && !p.query_start)) {
+        if (MODE == kSuffix || (kIsMod && !p.query_start)) {
             qs0 = seq;
         } else {
             qs0 = p.query_start[seq];
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                       L > p.max_context_len ||
                       L - start > p.max_suffix_len;
         }
-        if (MODE == kMod && !p.query_start)
+        if (kIsMod && !p.query_start)
             bad_len = L < 0 || L > p.max_context_len;      // an empty context is a zero row
     }
     if (bad_len || !rows_sane) {
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
         const int last = L - n + min(n - 1, (R0 + NH - 1) / p.group);   // last row's position
         if constexpr (MODE == kPlain)
             t_end = last + 1;
-        if constexpr (MODE == kMod) {
+        if constexpr (kIsMod) {
             seen = seen_by(p.mods, seq, L, L - n + R0 / p.group, last);
             order = seen_tiles(seen, TB);
             t_end = seen.end;
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     }
     int t0 = start, t1 = t_end;
     int jb = 0, nblk = 0, ntiles = 0;
-    if constexpr (MODE == kMod) {
+    if constexpr (kIsMod) {
         // partitions cut the list of tiles to read; jb counts tiles of that list
         jb = split ? part * (p.partition_tokens / TB) : 0;
         if (split && jb >= order.count)
@@ -336,21 +337,16 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     }
     // first token of tile it, and the CTA's i-th block as an index into bt_row below
     auto tile_token = [&](int it) -> int {
-        if constexpr (MODE == kMod)
+        if constexpr (kIsMod)
             return order(jb + it) * TB;
         else
             return jb * BS + it * TB;
     };
     auto block_of = [&](int i) -> int {
-        if constexpr (MODE == kMod)
+        if constexpr (kIsMod)
             return order(jb + i / BPT) * BPT + i % BPT;
         else
             return i;
-    };
-    // kMod: whether block b of the context holds a seen token (the others are neither read
-    // nor checked: an engine may have freed them)
-    auto block_seen = [&](int b) -> bool {
-        return any_seen(seen, b * BS, min(b * BS + BS, t1));
     };
 
     if (threadIdx.x == 0) {
@@ -370,18 +366,31 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
 
     if (warp == NCW) {
         // ------------------------------------------------------------------ producer
-        const int32_t* bt_row = p.block_tables + (int64_t)tseq * p.bt_stride + (MODE == kMod ? 0 : jb);
+        const int32_t* bt_row = p.block_tables + (int64_t)tseq * p.bt_stride + (kIsMod ? 0 : jb);
         const uint64_t policy = l2_evict_first_policy();
-        int next = (lane < nblk && (MODE != kMod || block_seen(block_of(lane)))) ? __ldg(bt_row + block_of(lane))
-                                                                                  : 0;
+        // kMod: the table entry of the CTA's i-th block (negative ids are one -1), or kUnseen when
+        // it holds no seen token (such blocks are neither read nor checked: an engine may have
+        // freed them).  Worked out 32 at a time: the lane that issues the copies is on the
+        // critical path of every tile (doing it there cost 8 us of 86, 48 windows of 4096).
+        constexpr int kUnseen = -2;
+        auto entry = [&](int i) -> int {
+            if (i >= nblk)
+                return kUnseen;
+            const int b = block_of(i);
+            return any_seen(seen, b * BS, min(b * BS + BS, t1)) ? max(__ldg(bt_row + b), -1) : kUnseen;
+        };
+        int next;
+        if constexpr (kIsMod)
+            next = entry(lane);
+        else
+            next = (lane < nblk) ? __ldg(bt_row + lane) : 0;
         bool aborted = false;
         // block-table entries 32 at a time (BPT divides 32, so no tile straddles two
         // batches), the next 32 in flight while the current ones are used
         for (int base = 0; base < nblk && !aborted; base += 32) {
             const int cur = next;
-            if constexpr (MODE == kMod) {
-                if (base + 32 + lane < nblk && block_seen(block_of(base + 32 + lane)))
-                    next = __ldg(bt_row + block_of(base + 32 + lane));
+            if constexpr (kIsMod) {
+                next = entry(base + 32 + lane);
             } else if (base + 32 + lane < nblk) {
                 next = __ldg(bt_row + base + 32 + lane);
             }
@@ -393,8 +402,8 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                     pbn[b] = __shfl_sync(kFullMask, cur, i + b);   // i + b <= 31
                 const int nb = min(BPT, cnt - i);                  // blocks of the tile in range
                 auto want = [&](int b) -> bool {                   // of those, the ones to read
-                    if constexpr (MODE == kMod)
-                        return b < nb && block_seen(block_of(base + i + b));
+                    if constexpr (kIsMod)
+                        return pbn[b] != kUnseen;
                     else
                         return b < nb;
                 };
@@ -536,6 +545,14 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     // kMod: first visible position past the global tokens, the global tokens, base-2 slope
     int low[2] = {0, 0}, glob[2] = {0, 0};
     float slope[2] = {0.f, 0.f};
+    // kMod: the first row's last visible position, and where the last row's window starts
+    int first_pos = 0, low_max = 0;
+    if constexpr (kIsMod) {
+        first_pos = L - n + R0 / p.group;
+        low_max = p.mods.window > 0
+                      ? max(0, L - n + min(n - 1, (R0 + NH - 1) / p.group) - p.mods.window + 1)
+                      : 0;
+    }
     if constexpr (CH) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -543,11 +560,11 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             const int tk = R / p.group;
             const bool live = 2 * c + j < NH && tk < n;
             lim[j] = !live ? -1 : (MODE == kPrefix || MODE == kSuffix) ? L - 1 : L - n + tk;
-            if constexpr (MODE == kMod) {
+            if constexpr (kIsMod) {
                 if (live) {
                     low[j] = p.mods.window > 0 ? max(0, lim[j] - p.mods.window + 1) : 0;
                     glob[j] = seen.glob;
-                    if (p.mods.slopes)
+                    if (has_slope(MODE) && p.mods.slopes)
                         slope[j] = p.mods.slopes[kvh * p.group + (R - tk * p.group)] * 1.4426950408889634f;
                 }
             }
@@ -597,7 +614,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
         for (int mb = 0; mb < MB; ++mb) {
             if (16 * mb >= nvalid)
                 break;                         // the rest of the tile lies past the context
-            if (MODE == kMod && !any_seen(seen, tb + 16 * mb, tb + 16 * mb + 16))
+            if (kIsMod && !any_seen(seen, tb + 16 * mb, tb + 16 * mb + 16))
                 continue;                      // no row sees any of these 16 tokens
             // ---- S^T = K . Q^T for tokens 16mb .. 16mb+15
             float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -628,10 +645,10 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             // ---- online softmax: s[0], s[1] = token 16mb+g; s[2], s[3] = token 16mb+g+8
             const int tok_a = 16 * mb + g, tok_b = tok_a + 8;
             float x[4];
-            if constexpr (MODE == kMod) {
+            if constexpr (kIsMod) {
                 // scores well within the cap (the usual case): the short form of tanh
                 bool near_cap = false;
-                if (p.mods.cap > 0.f) {
+                if (has_cap(MODE) && p.mods.cap > 0.f) {
                     const float far0 = fmaxf(fmaxf(fabsf(s[0]), fabsf(s[1])), fmaxf(fabsf(s[2]), fabsf(s[3])));
                     near_cap = __all_sync(kFullMask, far0 * fabsf(sl2) * p.mods.inv_cap <= kCapNear);
                     if (near_cap) {
@@ -642,13 +659,24 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int r = j & 1, t = tb + (j < 2 ? tok_a : tok_b);
                     x[j] = near_cap ? s[j] : s[j] * sl2;
-                    if (p.mods.cap > 0.f && !near_cap)
+                    if (has_cap(MODE) && p.mods.cap > 0.f && !near_cap)
                         x[j] = cap_score(x[j], p.mods);
-                    x[j] = fmaf(-slope[r], (float)abs(lim[r] - t), x[j]);
-                    const bool sees = t < glob[r] || (t >= low[r] && t <= lim[r]);
-                    x[j] = sees ? x[j] : -INFINITY;
+                }
+                if (has_slope(MODE) && p.mods.slopes) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = fmaf(-slope[j & 1], (float)abs(lim[j & 1] - (tb + (j < 2 ? tok_a : tok_b))), x[j]);
+                }
+                // all rows see all 16 tokens, but at a window's ends and the last tokens
+                const int b0 = tb + 16 * mb;
+                if (!(b0 + 16 <= seen.glob || (b0 + 15 <= first_pos && b0 >= low_max))) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = j & 1, t = tb + (j < 2 ? tok_a : tok_b);
+                        const bool sees = t < glob[r] || (t >= low[r] && t <= lim[r]);
+                        x[j] = sees ? x[j] : -INFINITY;
+                    }
                 }
             } else {
                 x[0] = tok_a < nvalid ? s[0] * sl2 : -INFINITY;
@@ -702,11 +730,11 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             // ---- O^T += V^T . P^T over tokens 16mb .. 16mb+15
             const int vr = 16 * mb + (lane & 7) + 8 * (lane >> 4);            // token row
             bool ragged = nvalid < 16 * (mb + 1);
-            if constexpr (MODE == kMod)              // some of the 16 tokens are seen by no row
+            if constexpr (kIsMod)              // some of the 16 tokens are seen by no row
                 ragged = ragged || (tb + 16 * mb < seen.lo && tb + 16 * mb + 16 > seen.glob);
             // token t of the tile is in range and seen
             auto live_tok = [&](int t) -> bool {
-                if constexpr (MODE == kMod)
+                if constexpr (kIsMod)
                     return t < nvalid && is_seen(seen, tb + t);
                 else
                     return t < nvalid;

@@ -18,7 +18,8 @@
 // decode_mma_kernel.  A CTA serves RW row groups of 16 rows; consumer warp w takes row group
 // w % RW of the tiles w / RW, w / RW + 4 / RW, .., so RW warps share a tile, and up to 64 rows
 // share one read of K and V.  The warps of a row group merge through shared memory at the end.
-// Modes: kMod (chunk rows, or with query_start null the heads of each sequence's last token),
+// Modes: kMod (chunk rows, or with query_start null the heads of each sequence's last token;
+// kModBoth when the scores have a cap or slopes),
 // kPrefix and kSuffix, which write partial rows only.
 #pragma once
 
@@ -69,7 +70,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     constexpr int NR = kRowsGroup * RW;
     constexpr int KS = D / 16;        // k-steps of the score product
     constexpr int NB = D / 8;         // 8-dim column blocks of O
-    static_assert(MODE == kMod || MODE == kPrefix || MODE == kSuffix, "the plain mode has its own kernels");
+    constexpr bool kIsMod = is_mod(MODE);
+    static_assert(kIsMod || MODE == kPrefix || MODE == kSuffix, "the plain mode has its own kernels");
     static_assert(NCW % RW == 0 && NSTAGE % NCW == 0, "each ring stage belongs to one warp of a row group");
     static_assert((BS == 16 || BS == 32) && D % 64 == 0, "block_size 16/32, head_dim 64/128");
 
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 
     // the sequence's (or group's) rows of q / out are qs0 .. qs0 + n - 1
     int qs0 = seq, n = 1;
-    if (MODE == kPrefix || (MODE == kMod && p.query_start)) {
+    if (MODE == kPrefix || (kIsMod && p.query_start)) {
         qs0 = p.query_start[seq];
         n = p.query_start[seq + 1] - qs0;
     }
@@ -141,8 +143,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     int jb = 0, nblk = 0, ntiles = 0;
     // kMod: positions of the CTA's first and last row; the window's start for the last
     const int first_pos = L - n + R0 / p.group, last_pos = L - n + min(n - 1, (R0 + NR - 1) / p.group);
-    const int low_max = MODE == kMod && p.mods.window > 0 ? max(0, last_pos - p.mods.window + 1) : 0;
-    if constexpr (MODE == kMod) {
+    const int low_max = kIsMod && p.mods.window > 0 ? max(0, last_pos - p.mods.window + 1) : 0;
+    if constexpr (kIsMod) {
         // partitions cut the list of tiles to read; jb counts tiles of that list
         seen = seen_by(p.mods, seq, L, first_pos, last_pos);
         order = seen_tiles(seen, TB);
@@ -164,21 +166,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         ntiles = (nblk + BPT - 1) / BPT;
     }
     auto tile_token = [&](int it) -> int {        // first token of tile it
-        return MODE == kMod ? order(jb + it) * TB : jb * BS + it * TB;
+        return kIsMod ? order(jb + it) * TB : jb * BS + it * TB;
     };
     auto block_of = [&](int i) -> int {           // block of the context: the CTA's i-th
-        return MODE == kMod ? order(jb + i / BPT) * BPT + i % BPT : jb + i;
-    };
-    // whether the CTA's i-th block is to be read: kMod reads (and checks) only blocks that hold
-    // a seen token
-    auto wanted = [&](int i) -> bool {
-        if (i >= nblk)
-            return false;
-        if constexpr (MODE == kMod) {
-            const int b = block_of(i);
-            return any_seen(seen, b * BS, min(b * BS + BS, t1));
-        }
-        return true;
+        return kIsMod ? order(jb + i / BPT) * BPT + i % BPT : jb + i;
     };
 
     if (threadIdx.x == 0) {
@@ -200,13 +191,24 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         // ------------------------------------------------------------------ producer
         const int32_t* bt_row = p.block_tables + (int64_t)tseq * p.bt_stride;
         const uint64_t policy = l2_evict_first_policy();
-        // block-table entries 32 at a time (BPT divides 32), the next 32 in flight
-        int next = wanted(lane) ? __ldg(bt_row + block_of(lane)) : -1;
+        // the table entry of the CTA's i-th block (negative ids are one -1), or kUnseen: kMod
+        // reads (and checks) only blocks that hold a seen token
+        constexpr int kUnseen = -2;
+        auto entry = [&](int i) -> int {
+            if (i >= nblk)
+                return kUnseen;
+            const int b = block_of(i);
+            if constexpr (kIsMod)
+                if (!any_seen(seen, b * BS, min(b * BS + BS, t1)))
+                    return kUnseen;
+            return max(__ldg(bt_row + b), -1);
+        };
+        // entries 32 at a time (BPT divides 32), the next 32 in flight
+        int next = entry(lane);
         bool aborted = false;
         for (int base = 0; base < nblk && !aborted; base += 32) {
             const int cur = next;
-            if (wanted(base + 32 + lane))
-                next = __ldg(bt_row + block_of(base + 32 + lane));
+            next = entry(base + 32 + lane);
             const int cnt = min(32, nblk - base);
             for (int i = 0; i < cnt; i += BPT) {
                 int pbn[BPT];
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                         bool valid[BPT];
 #pragma unroll
                         for (int b = 0; b < BPT; ++b) {
-                            const bool want = wanted(base + i + b);
+                            const bool want = pbn[b] != kUnseen;
                             valid[b] = want && pbn[b] >= 0 && (int64_t)pbn[b] < p.num_blocks;
                             all_valid = all_valid && (!want || valid[b]);
                             tx += valid[b] ? 2u * BS * D * (uint32_t)sizeof(TK) : 0u;
@@ -281,14 +283,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         const int R = W0 + g + 8 * j;
         const int tok = R / p.group;
         live[j] = tok < n;
-        lim[j] = MODE == kMod ? L - n + tok : L - 1;
+        lim[j] = kIsMod ? L - n + tok : L - 1;
         low[j] = 0;
         glob[j] = 0;
         slope[j] = 0.f;
-        if (MODE == kMod && live[j]) {
+        if (kIsMod && live[j]) {
             low[j] = p.mods.window > 0 ? max(0, lim[j] - p.mods.window + 1) : 0;
             glob[j] = seen.glob;
-            if (p.mods.slopes)
+            if (has_slope(MODE) && p.mods.slopes)
                 slope[j] = p.mods.slopes[kvh * p.group + (R - tok * p.group)] * 1.4426950408889634f;
         }
         if (!live[j])
@@ -405,10 +407,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                 s[h][k] *= sl2;
         bool ragged = nvalid < TB;                // some tokens are outside, or seen by no row
         bool mask = ragged;                       // some row does not see some token
-        if constexpr (MODE == kMod) {
+        if constexpr (kIsMod) {
             ragged = ragged || (tb < seen.lo && tb + TB > seen.glob);
             mask = !(tb + TB <= seen.glob || (tb + TB - 1 <= first_pos && tb >= low_max));
-            if (p.mods.cap > 0.f) {
+            if (has_cap(MODE) && p.mods.cap > 0.f) {
                 float far0 = 0.f;
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                             s[h][k] = cap_score(s[h][k], p.mods);
                 }
             }
-            if (p.mods.slopes) {
+            if (has_slope(MODE) && p.mods.slopes) {
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
 #pragma unroll
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int tt = 8 * h + 2 * c + (k & 1), t = tb + tt, j = k >> 1;
-                    const bool sees = MODE == kMod ? t < glob[j] || (t >= low[j] && t <= lim[j]) : tt < nvalid;
+                    const bool sees = kIsMod ? t < glob[j] || (t >= low[j] && t <= lim[j]) : tt < nvalid;
                     s[h][k] = sees ? s[h][k] : -INFINITY;
                 }
         }
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             uint32_t m01 = 0xffffffffu, m23 = 0xffffffffu;
             if (ragged) {
                 auto live_tok = [&](int t) -> bool {
-                    return t < nvalid && (MODE != kMod || is_seen(seen, tb + t));
+                    return t < nvalid && (!kIsMod || is_seen(seen, tb + t));
                 };
                 const int t = 16 * mb + 2 * c;
                 m01 = (live_tok(t) ? 0x0000ffffu : 0u) | (live_tok(t + 1) ? 0xffff0000u : 0u);

@@ -358,14 +358,13 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         const uint64_t policy = l2_evict_first_policy();
         const int blk_first = t0 / BS;             // partitions start on block boundaries
         const int nblk = MODE == kMod ? ntiles * BPT : (t1 + BS - 1) / BS - blk_first;
-        // the table entry of the CTA's i-th block; kMod reads (and checks) only blocks that
-        // hold a seen token
-        auto wanted = [&](int i) -> bool {
-            const int b = order(c0 + i / BPT) * BPT + i % BPT;
-            return i < nblk && any_seen(seen, b * BS, min(b * BS + BS, t1));
-        };
+        // kMod: the table entry of the CTA's i-th block (negative ids are one -1), or kUnseen:
+        // only blocks that hold a seen token are read (and checked)
+        constexpr int kUnseen = -2;
         auto entry = [&](int i) -> int {
-            return wanted(i) ? __ldg(bt_row + order(c0 + i / BPT) * BPT + i % BPT) : -1;
+            const int b = order(c0 + i / BPT) * BPT + i % BPT;
+            return i < nblk && any_seen(seen, b * BS, min(b * BS + BS, t1)) ? max(__ldg(bt_row + b), -1)
+                                                                            : kUnseen;
         };
         // block-table entries 32 at a time (4 or 8 tiles), the next 32 in flight while the
         // current ones are used
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
             bool valid = false;
             bool want = lane < nb;
             if constexpr (MODE == kMod) {
-                want = lane < BPT && wanted(lb + lane);
+                want = lane < BPT && e != kUnseen;
                 nb = __popc(__ballot_sync(kFullMask, want));
             }
             if (want) {

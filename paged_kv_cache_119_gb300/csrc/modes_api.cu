@@ -297,8 +297,11 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
     const int qlen = decode ? 1 : max_query_len;
     Plan pl = decode ? plan_heads(s) : plan_rows(s, qlen, kChunkRowsMax);
     AttnMode mode = kMod;
-    if (pl.family == Family::kChunk)             // the one kernel built for each set of modifiers
-        mode = softcap > 0.f ? (alibi_slopes ? kModBoth : kModCap) : (alibi_slopes ? kModSlope : kMod);
+    const bool cap = softcap > 0.f, slope = alibi_slopes != nullptr;
+    if (pl.family == Family::kChunk)
+        mode = cap ? (slope ? kModBoth : kModCap) : (slope ? kModSlope : kMod);
+    else if (pl.family == Family::kRows)
+        mode = cap || slope ? kModBoth : kMod;
     const int length =
         (int)std::min<int64_t>(seen_bound(max_context_len, window, max_global_len, qlen, pl.tile), INT32_MAX);
     choose_split(pl, s, mode, num_seqs, length, partition_size);

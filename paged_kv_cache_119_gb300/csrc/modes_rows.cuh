@@ -65,6 +65,8 @@ bool rows_any_mode(AttnMode mode, int head_dim, int block_size, int nh, F&& f)
 {
     if (mode == kMod)
         return rows_variant<T, TK, kMod>(head_dim, block_size, nh, f);
+    if (mode == kModBoth)
+        return rows_variant<T, TK, kModBoth>(head_dim, block_size, nh, f);
     if (mode == kPrefix)
         return rows_variant<T, TK, kPrefix>(head_dim, block_size, nh, f);
     return mode == kSuffix && rows_variant<T, TK, kSuffix>(head_dim, block_size, nh, f);

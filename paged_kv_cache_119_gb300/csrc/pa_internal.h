@@ -33,9 +33,11 @@ constexpr int kAutoPartitionTokens = 512;
 //            group's first sequence) attend over the tokens they share, no causal limit;
 //            writes partial rows only
 //   kSuffix  each sequence's own tokens after its shared prefix; writes partial rows only
-//   kModCap, kModSlope, kModBoth   chunk_attn_kernel only: kMod with a cap, slopes or both,
-//            where its kMod has neither (code for all at once spilled registers: 648 against
-//            523 us on 4 x 512 tokens of 8192 without a cap or slopes)
+//   kModCap, kModSlope, kModBoth   kMod with a cap, slopes or both, where a kernel's kMod has
+//            neither: all three in chunk_attn_kernel (code for all at once spilled registers:
+//            648 against 508 us on 4 x 512 tokens of 8192 without a cap or slopes), kModBoth
+//            for any of them in decode_mma_kernel and decode_rows_kernel (tests for what a
+//            call does not have: 92 against 86 us on 48 windows of 4096 over an E4M3 cache)
 enum AttnMode : int {
     kPlain = 0,
     kMod = 1,
