@@ -50,11 +50,15 @@ bool rows_variant(int head_dim, int block_size, int nh, F&& f)
     PA_ROWS_MODE(128, 16, 8) PA_ROWS_MODE(128, 32, 8) PA_ROWS_MODE(64, 16, 8) PA_ROWS_MODE(64, 32, 8)
     PA_ROWS_MODE(64, 16, 4) PA_ROWS_MODE(64, 32, 4)
     PA_ROWS_MODE(128, 16, 16) PA_ROWS_MODE(128, 32, 16) PA_ROWS_MODE(128, 16, 32) PA_ROWS_MODE(128, 32, 32)
-    PA_ROWS_MODE(128, 16, 64) PA_ROWS_MODE(128, 32, 64)
     if constexpr (sizeof(TK) != 1) {
         PA_ROWS_MODE(128, 16, 4) PA_ROWS_MODE(128, 32, 4)
         PA_ROWS_MODE(64, 16, 16) PA_ROWS_MODE(64, 32, 16) PA_ROWS_MODE(64, 16, 32) PA_ROWS_MODE(64, 32, 32)
-        PA_ROWS_MODE(64, 16, 64) PA_ROWS_MODE(64, 32, 64)
+    }
+    if constexpr (MODE != kPrefix) {               // (a shared prefix takes the chunk kernel there)
+        PA_ROWS_MODE(128, 16, 64) PA_ROWS_MODE(128, 32, 64)
+        if constexpr (sizeof(TK) != 1) {
+            PA_ROWS_MODE(64, 16, 64) PA_ROWS_MODE(64, 32, 64)
+        }
     }
 #undef PA_ROWS_MODE
     return false;
