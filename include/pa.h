@@ -1,7 +1,7 @@
 /*
  * pa.h -- C ABI of the paged decode attention library (libpa.so), GB300 / sm_103a.
  *
- * Three operations over a paged KV cache, each a hand-written CUDA kernel:
+ * Operations over a paged KV cache, each a hand-written CUDA kernel:
  *
  *   pa_reshape_and_cache  write each new token's K/V rows into the cache slots
  *                         named by slot_mapping ("PagedAttention 完全拆解",
@@ -17,6 +17,15 @@
  *   pa_copy_blocks        copy whole blocks src -> dst for copy-on-write (first page,
  *                         section 原理详解（三） item 3: fused block copy; section
  *                         内存共享, Figure 8).
+ *   pa_chunk_attention    several new tokens of each sequence attend causally.
+ *   pa_swap_blocks        move blocks between the pool and a pinned host pool.
+ *   pa_rotary_and_cache   rotary positions of q and k fused with the cache write.
+ *   pa_decode_mod, pa_chunk_attention_mod
+ *                         the attention calls with capped scores, distance bias, a sliding
+ *                         window and tokens that every row sees.
+ *   pa_decode_prefix      pa_decode for sequences that share long prefixes, each prefix read
+ *                         once for its group.
+ * The cache writes and the attention calls have _fp8 forms over E4M3 caches.
  *
  * Layout (the pages leave the in-block layout to the backend; iaim.asia page,
  * section KV Cache 如何按块分配).  All tensors are dense, row-major, in device
@@ -37,7 +46,8 @@
  *   - Every call is asynchronous on the given stream (a cudaStream_t passed as
  *     void*; NULL = the legacy default stream).  The library never synchronises,
  *     never allocates device memory and keeps no state except a per-device SM
- *     count and a per-device error word (see pa_get_device_error).
+ *     count, kernel occupancies and a per-device error word (see
+ *     pa_get_device_error).
  *   - Host-side validation runs before any launch.  A failed check returns a
  *     negative pa_status and launches nothing.  A failed launch returns
  *     PA_ERR_CUDA.
@@ -239,7 +249,8 @@ int pa_rotary_frequencies(double* inv_freq, int32_t rotary_dim, double base,
  *   rotary_dim     even, 2 .. min(head_dim, 256)
  *   magnitude      factor on the turned dims of q and k (1 in the usual case)
  * head_dim * element size must be a multiple of 16 bytes (PA_ERR_UNSUPPORTED).  A slot
- * >= num_blocks * B is skipped and flags PA_DEVERR_SLOT.
+ * >= num_blocks * B is skipped and flags PA_DEVERR_SLOT.  Two tokens of one call must not
+ * name the same slot (which of them it then holds, vector by vector, is not defined).
  */
 int pa_rotary_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
                         const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -443,7 +454,7 @@ int pa_chunk_attention_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtyp
  * mask: tokens after pos are visible below g_s).
  *
  *   softcap        0 (none) or 1e-30 .. 1e30
- *   alibi_slopes   DEVICE float [num_q_heads], or NULL
+ *   alibi_slopes   DEVICE float [num_q_heads], finite, or NULL
  *   window         0 (none), or the number of tokens a row sees up to and with its own
  *   global_lens    DEVICE int32 [num_seqs], or NULL
  *   max_global_len host bound on global_lens (larger entries count as this); sizes the
@@ -515,9 +526,10 @@ int pa_chunk_attention_mod_fp8(void* out, pa_dtype out_dtype, const void* q, pa_
  * group shares: whole blocks (a multiple of block_size, equal within a group), whose table
  * entries are read from the group's first sequence; the others of the group name the same
  * blocks.  out is what pa_decode returns for the same tables and lengths (up to rounding:
- * the prefix of a group with more than 16 (sequence, head) rows per kv head runs on the
- * tcgen05 chunk kernel, whose probabilities are one f16 term; see pa_chunk_attention, also
- * for V elements without an f16 value over a bf16 cache, PA_DEVERR_RANGE).
+ * with max_group_size * num_q_heads / num_kv_heads > 32 the prefix runs on the tcgen05 chunk
+ * kernel, whose probabilities are one f16 term; see pa_chunk_attention, also for V elements
+ * without an f16 value over a bf16 cache, PA_DEVERR_RANGE.  E4M3 caches at head_dim 64 stay
+ * on the decode kernels).
  *
  *   prefix_lens      DEVICE int32 [num_seqs], 0 <= prefix_lens[s] <= context_lens[s]
  *   group_start      DEVICE int32 [num_groups + 1], non-decreasing
@@ -529,7 +541,7 @@ int pa_chunk_attention_mod_fp8(void* out, pa_dtype out_dtype, const void* q, pa_
  *   workspace        DEVICE scratch of pa_decode_prefix_workspace_bytes(...), 16-byte
  *                    aligned, always required; overlaps neither out nor any input
  * Other arguments as in pa_decode / pa_decode_fp8, kv_dtype PA_F16 or PA_BF16 (PA_F32 is
- * PA_ERR_UNSUPPORTED), num_q_heads / num_kv_heads <= 128.  A sequence in no group, a group
+ * PA_ERR_UNSUPPORTED), num_q_heads / num_kv_heads <= 128, num_seqs <= 65534.  A sequence in no group, a group
  * larger than max_group_size, lengths beyond their bounds, a prefix that is no whole number
  * of blocks or differs within its group, and a context longer than the table row or shorter
  * than its prefix set PA_DEVERR_CONTEXT_LEN; the sequence's rows become NaN.

@@ -1,8 +1,7 @@
 """paged_kv_cache_119_gb300 -- PagedAttention decode over a paged KV cache on GB300.
 
-A CUDA library (``libpa.so``, C ABI in ``include/pa.h``) with three operations,
-each one hand-written sm_103a kernel launch (plus a merge pass for split
-contexts), and this thin binding that passes PyTorch tensors to it:
+A CUDA library (``libpa.so``, C ABI in ``include/pa.h``) of hand-written sm_103a
+kernels, and this thin binding that passes PyTorch tensors to it:
 
     pa_reshape_and_cache(k, v, k_cache, v_cache, slot_mapping)
     pa_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale,
@@ -10,6 +9,13 @@ contexts), and this thin binding that passes PyTorch tensors to it:
     pa_copy_blocks(k_caches, v_caches, src_dst_pairs)
     pa_chunk_attention(out, q, k_cache, v_cache, block_tables, context_lens,
                        query_start, scale, num_kv_heads, block_size, max_query_len)
+    pa_rotary_and_cache(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions,
+                        inv_freq)
+    pa_decode_mod(..., softcap, alibi_slopes, window, global_lens, max_global_len)
+    pa_chunk_attention_mod(..., the same)
+    pa_decode_prefix(out, q, k_cache, v_cache, block_tables, context_lens, prefix_lens,
+                     group_start, scale, num_kv_heads, block_size, max_group_size,
+                     max_prefix_len)
 
 ``workloads`` builds seeded synthetic inputs.  The binding is imported lazily
 so the input generator works on machines without the built library; any call

@@ -9,9 +9,9 @@
 // Bound: reading the parts (a few MB that the passes have just left in L2), so latency.  One
 // warp per (row, head): its lanes read the (m, l) of 32 parts at once and a 16-byte piece of
 // the row each, four parts in flight; the sequence or group that owns the row is found by a
-// 33-way search of all lanes.  (One CTA per row with a serial search and serial (m, l) reads
-// took 15.6 us for 6144 rows of 14 parts and 8.7 us for 4096 rows of 2; this form is in the
-// table of the design notes.)
+// 33-way search of all lanes.  6144 rows of 8 parts take 9.8 us from a cold start and 4096 rows
+// of 2 or 3 parts 7.1; one CTA per row with a serial search and serial (m, l) reads took 15.6
+// and 8.7.
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -38,6 +38,12 @@ __device__ __forceinline__ int owner_of(const int32_t* start, int n, int64_t x, 
         hi = next;
     }
     return lo;
+}
+
+// x / d for 0 <= x, 0 < d; in 32 bits where they hold x.
+__device__ __forceinline__ int64_t quotient(int64_t x, int d)
+{
+    return x >> 32 == 0 ? (int64_t)((uint32_t)x / (uint32_t)d) : x / d;
 }
 
 // Head dims of a row one lane holds.
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mod_reduce_kernel(const Deco
     const int64_t out_row = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
     if (out_row >= p.num_rows * p.num_q_heads)
         return;
-    const int64_t row = out_row / p.num_q_heads;
+    const int64_t row = quotient(out_row, p.num_q_heads);
     const int h = (int)(out_row - row * p.num_q_heads);
     int s = (int)row, qs0 = (int)row, n = 1;
     if (p.query_start) {
@@ -160,31 +166,34 @@ template <typename T, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) mod_reduce_cut_kernel(const DecodeParams p, int tile_tokens)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t i = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    // (fewer units than SMs are cut, and all units are fewer than 2^31 / 64)
+    const int i = (int)blockIdx.x * kMergeWarps + (int)(threadIdx.x >> 5);
     const int per_seq = p.num_kv_heads * p.chunks;
-    const int64_t unit = p.whole_units + i / p.rows_per_cta;
-    if (unit >= (int64_t)p.num_seqs * per_seq)
+    const int nth = i / p.rows_per_cta;
+    const int unit = p.whole_units + nth;
+    if (unit >= p.num_seqs * per_seq)
         return;
-    const int s = (int)(unit / per_seq);
-    const int y = (int)(unit - (int64_t)s * per_seq);
+    const int s = unit / per_seq;
+    const int y = unit - s * per_seq;
     const int kvh = y / p.chunks;
     const int R0 = (y - kvh * p.chunks) * p.rows_per_cta;
-    const int R = R0 + (int)(i % p.rows_per_cta);
+    const int R = R0 + (i - nth * p.rows_per_cta);
     const int qs0 = p.query_start[s], n = p.query_start[s + 1] - qs0;
     const int L = p.context_lens[s];
     const bool sane = qs0 >= 0 && n >= 0 && (int64_t)qs0 + n <= p.num_rows;
     const bool bad = L < 0 || L > p.max_context_len || n > L || n > p.max_query_len;
     const bool here = sane && !bad && R / p.group < n;
     const int parts = here ? mod_parts(p, s, L, n, R0, tile_tokens) : 0;
-    auto out_row = [&](int64_t r) -> int64_t {
-        return (qs0 + r / p.group) * p.num_q_heads + kvh * p.group + r % p.group;
+    auto out_row = [&](int r) -> int64_t {
+        const int tok = r / p.group;
+        return (int64_t)(qs0 + tok) * p.num_q_heads + kvh * p.group + (r - tok * p.group);
     };
     grid_wait_prerequisites();                     // the parts are in place
     if (here)
         store_piece<T, D>(p, out_row(R), merge_row<D>(p, out_row(R), parts, lane), false, lane);
     if (sane && bad && R0 == 0)                    // (flagged by the pass; rows past the bound too)
-        for (int64_t r = R; r < (int64_t)n * p.group; r += p.rows_per_cta)
-            store_piece<T, D>(p, out_row(r), RowPiece<D>{}, true, lane);
+        for (int64_t r = R; r < min((int64_t)n * p.group, (int64_t)INT32_MAX); r += p.rows_per_cta)
+            store_piece<T, D>(p, out_row((int)r), RowPiece<D>{}, true, lane);
 }
 
 // Shared prefix: one warp per (sequence, query head), head fastest.  The prefix pass wrote
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     const int64_t out_row = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
     if (out_row >= (int64_t)p.num_seqs * p.num_q_heads)
         return;
-    const int s = (int)(out_row / p.num_q_heads);
+    const int s = (int)quotient(out_row, p.num_q_heads);
     const int g = owner_of(group_start, num_groups, s, lane);
     const int g0 = group_start[g], g1 = group_start[g + 1];
     const int L = p.context_lens[s];

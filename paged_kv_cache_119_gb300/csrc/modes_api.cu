@@ -358,8 +358,8 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
     }
     // A one-pass grid of the chunk kernel (one CTA per SM) whose last wave is at most half full
     // leaves the rest of the SMs idle for as long as a CTA runs: its units are then cut into as
-    // many parts as fill that wave.  4 x 512 tokens of 8192, 64/8 heads: 512 units on 152 SMs,
-    // the last 56 in two parts, 673 -> 608 us.  Without a workspace the call runs unsplit.
+    // many parts as fill that wave.  4 x 512 tokens of 8192, 64/8 heads, capped: 512 units on 152
+    // SMs, the last 56 in two parts, 673 -> 574 us.  Without a workspace the call runs unsplit.
     int64_t whole_units = 0;
     if (pl.family == Family::kChunk && pl.partition == 0 && partition_size == 0 && pl.slots > 0) {
         const int64_t rest = pl.units % pl.slots;
