@@ -8,6 +8,7 @@ kernels; there is no PyTorch or CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import numpy as np
 import torch
@@ -36,10 +37,11 @@ def _cuda(name: str, t: torch.Tensor) -> None:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, device: int | None = None) -> int:
+    """Handle of `stream`, or of the current one (device: the current device, where known)."""
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if device is None else device)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -194,6 +196,15 @@ def _rows(name: str, t: torch.Tensor) -> int:
     return st if T > 1 else H * D
 
 
+def _dense_on(dev: int, tensors) -> bool:
+    """Whether every tensor is a contiguous one of CUDA device `dev`: what _cuda and _one_device
+    check tensor by tensor, for the calls where all is well (they then cost a third of it)."""
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return True
+
+
 def _one_device(q: torch.Tensor, *others: torch.Tensor) -> None:
     """Every tensor on q's device, and that device current: the launch goes there."""
     dev = q.get_device()
@@ -208,8 +219,13 @@ def _one_device(q: torch.Tensor, *others: torch.Tensor) -> None:
 def _rotary(fn, q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_freq, scales,
             interleaved, magnitude, stream):
     so, sq, sk, sv = _rows("q_out", q_out), _rows("q", q), _rows("k", k), _rows("v", v)
-    _cuda("slot_mapping", slot_mapping)
-    _cuda("positions", positions)
+    dev = torch.cuda.current_device()
+    quick = _dense_on(dev, (k_cache, v_cache, slot_mapping, positions, *scales)) and \
+        q.get_device() == q_out.get_device() == k.get_device() == v.get_device() == dev
+    if not quick:
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("slot_mapping", slot_mapping),
+                        ("positions", positions)):
+            _cuda(name, t)
     if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int32:
         raise TypeError("slot_mapping must be int64 and positions int32")
     T, Hq, D = q.shape
@@ -223,7 +239,8 @@ def _rotary(fn, q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_f
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or \
             (k_cache.shape[1], k_cache.shape[3]) != (Hkv, D):
         raise ValueError(f"caches must be [N, {Hkv}, B, {D}]")
-    _one_device(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, *scales)
+    if not quick:
+        _one_device(q, q_out, k, v, k_cache, v_cache, slot_mapping, positions, *scales)
     freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
     if freq.ndim != 1:
         raise ValueError("inv_freq must be a host sequence of rotary_dim / 2 numbers")
@@ -232,8 +249,8 @@ def _rotary(fn, q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, inv_f
         k_cache.data_ptr(),
         v_cache.data_ptr(), *[t.data_ptr() for t in scales], slot_mapping.data_ptr(),
         positions.data_ptr(), T, Hq, Hkv, D, k_cache.shape[2], k_cache.shape[0],
-        freq.ctypes.data, 2 * freq.size, int(bool(interleaved)), float(magnitude),
-        _stream(stream))
+        freq.tobytes(), 2 * freq.size, int(bool(interleaved)), float(magnitude),
+        _stream(stream, dev))
     N.check(fn, status)
     return q_out
 
@@ -249,8 +266,8 @@ def pa_rotary_and_cache(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
     projection); q_out may be q.  positions int32 [T]; inv_freq: rotary_dim / 2 host numbers
     (pa_rotary_frequencies), radians per position; pairs are (i, i + rotary_dim / 2), or
     (2i, 2i + 1) when interleaved; magnitude multiplies the turned dims."""
-    _cuda("k_cache", k_cache)
-    _cuda("v_cache", v_cache)
+    if not (isinstance(k_cache, torch.Tensor) and isinstance(v_cache, torch.Tensor)):
+        raise ValueError("k_cache and v_cache must be CUDA tensors")
     if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
         raise TypeError("k, v and the caches must share a dtype")
     return _rotary("pa_rotary_and_cache", q_out, q, k, v, k_cache, v_cache, slot_mapping,
@@ -531,11 +548,14 @@ def pa_chunk_attention_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
 
 
 def _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_size):
-    """Checks shared by the calls below; returns (kv dtype arguments, scale pointers)."""
-    _cuda("out", out)
+    """Checks shared by the calls below; returns the device."""
     _cuda("q", q)
+    dev = torch.cuda.current_device()
+    quick = q.get_device() == dev and _dense_on(dev, (out, k_cache, v_cache, *scales, *[t for _, t in ints]))
+    if not quick:
+        for name, t in (("out", out), ("k_cache", k_cache), ("v_cache", v_cache), *ints):
+            _cuda(name, t)
     for name, t in ints:
-        _cuda(name, t)
         if t.dtype != torch.int32:
             raise TypeError(f"{name} must be int32")
     if q.dim() != 3 or out.shape != q.shape:
@@ -548,16 +568,30 @@ def _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_
         _scales(*scales, num_kv_heads)
         if q.dtype not in (torch.float16, torch.bfloat16):
             raise TypeError("q must be float16 or bfloat16 for an E4M3 cache")
-    else:
-        _cuda("k_cache", k_cache)
-        _cuda("v_cache", v_cache)
-        if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
-            raise TypeError("q, k_cache and v_cache must share a dtype")
+    elif k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
+        raise TypeError("q, k_cache and v_cache must share a dtype")
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or \
-            tuple(k_cache.shape[1:]) != (num_kv_heads, block_size, D):
+            k_cache.shape[1:] != (num_kv_heads, block_size, D):
         raise ValueError(f"k_cache/v_cache must be [N, {num_kv_heads}, {block_size}, {D}], "
                          f"got {tuple(k_cache.shape)}, {tuple(v_cache.shape)}")
-    _one_device(q, out, k_cache, v_cache, *scales, *[t for _, t in ints])
+    if not quick:
+        _one_device(q, out, k_cache, v_cache, *scales, *[t for _, t in ints])
+    return dev
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_need(*sizes) -> int:
+    return pa_decode_workspace_bytes(*sizes)
+
+
+@functools.lru_cache(maxsize=1024)
+def _chunk_need(*sizes) -> int:
+    return pa_chunk_workspace_bytes(*sizes)
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefix_need(*sizes) -> int:
+    return pa_decode_prefix_workspace_bytes(*sizes)
 
 
 def _scratch(need, workspace, q, stream):
@@ -567,7 +601,7 @@ def _scratch(need, workspace, q, stream):
         if not need:
             return None, 0, 0
         if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(need, dtype=torch.uint8)
         else:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(_stream(stream), device=q.device)
@@ -586,7 +620,7 @@ def _mod(fn, out, q, k_cache, v_cache, scales, block_tables, context_lens, query
         ints.append(("query_start", query_start))
     if global_lens is not None:
         ints.append(("global_lens", global_lens))
-    _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_size)
+    dev = _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_size)
     R, Hq, D = q.shape
     S = context_lens.shape[0]
     if context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != S:
@@ -616,9 +650,9 @@ def _mod(fn, out, q, k_cache, v_cache, scales, block_tables, context_lens, query
     if partition_size < 0 or workspace is not None:
         need = 0
     elif query_start is None:
-        need = pa_decode_workspace_bytes(S, Hq, D, read, block_size, partition_size)
+        need = _decode_need(S, Hq, D, read, block_size, partition_size)
     else:
-        need = pa_chunk_workspace_bytes(R, Hq, D, read, partition_size)
+        need = _chunk_need(R, Hq, D, read, partition_size)
     workspace, ws_ptr, ws_bytes = _scratch(need, workspace, q, stream)
     args = [out.data_ptr(), _dtype(out), q.data_ptr()]
     if scales:
@@ -631,7 +665,7 @@ def _mod(fn, out, q, k_cache, v_cache, scales, block_tables, context_lens, query
     args += [int(max_context_len), S, Hq, num_kv_heads, D, block_size, float(scale), float(softcap),
              0 if alibi_slopes is None else alibi_slopes.data_ptr(), int(window),
              0 if global_lens is None else global_lens.data_ptr(), int(max_global_len or 0),
-             int(partition_size), ws_ptr, ws_bytes, _stream(stream)]
+             int(partition_size), ws_ptr, ws_bytes, _stream(stream, dev)]
     N.check(fn, getattr(N.load(), fn)(*args))
     return out
 
@@ -715,10 +749,10 @@ def pa_decode_prefix_workspace_bytes(num_seqs: int, num_q_heads: int, head_dim: 
 def _prefix(fn, out, q, k_cache, v_cache, scales, block_tables, context_lens, prefix_lens,
             group_start, scale, num_kv_heads, block_size, max_group_size, max_prefix_len,
             max_suffix_len, partition_size, workspace, stream):
-    _attention_args(out, q, k_cache, v_cache, scales,
-                    [("block_tables", block_tables), ("context_lens", context_lens),
-                     ("prefix_lens", prefix_lens), ("group_start", group_start)],
-                    num_kv_heads, block_size)
+    dev = _attention_args(out, q, k_cache, v_cache, scales,
+                          [("block_tables", block_tables), ("context_lens", context_lens),
+                           ("prefix_lens", prefix_lens), ("group_start", group_start)],
+                          num_kv_heads, block_size)
     S, Hq, D = q.shape
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or \
             prefix_lens.shape != (S,) or group_start.dim() != 1 or group_start.shape[0] < 1:
@@ -727,8 +761,8 @@ def _prefix(fn, out, q, k_cache, v_cache, scales, block_tables, context_lens, pr
     W = block_tables.shape[1]
     if max_suffix_len is None:
         max_suffix_len = W * block_size
-    need = pa_decode_prefix_workspace_bytes(S, Hq, D, max_prefix_len, max_suffix_len,
-                                            partition_size)
+    need = 0 if workspace is not None else _prefix_need(S, Hq, D, max_prefix_len, max_suffix_len,
+                                                        partition_size)
     workspace, ws_ptr, ws_bytes = _scratch(need, workspace, q, stream)
     args = [out.data_ptr(), _dtype(out), q.data_ptr()]
     if scales:
@@ -738,7 +772,8 @@ def _prefix(fn, out, q, k_cache, v_cache, scales, block_tables, context_lens, pr
     args += [k_cache.shape[0], block_tables.data_ptr(), W, context_lens.data_ptr(),
              prefix_lens.data_ptr(), group_start.data_ptr(), group_start.shape[0] - 1,
              int(max_group_size), int(max_prefix_len), int(max_suffix_len), S, Hq, num_kv_heads, D,
-             block_size, float(scale), int(partition_size), ws_ptr, ws_bytes, _stream(stream)]
+             block_size, float(scale), int(partition_size), ws_ptr, ws_bytes,
+             _stream(stream, dev)]
     N.check(fn, getattr(N.load(), fn)(*args))
     return out
 

@@ -131,3 +131,17 @@ def test_prefix_workspace(lib):
     assert f(4, 8, 128, 1024, 512, -1) == 4 * 8 * 2 * row                # a part of each pass
     assert f(4, 8, 128, 1024, 512, 128) == 4 * 8 * 12 * row
     assert f(4, 8, 128, 1024, 513, 0) == 4 * 8 * 4 * row                 # parts of 512 at least
+
+
+def test_the_binding_refuses_host_tensors():
+    import torch
+
+    import paged_kv_cache_119_gb300 as P
+    q, pool = torch.zeros(2, 4, 64), torch.zeros(3, 2, 16, 64)
+    table, lens = torch.zeros(2, 1, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        P.pa_decode_mod(q, q, pool, pool, table, lens, 0.1, 2, 16)
+    with pytest.raises(ValueError):
+        P.pa_decode_prefix(q, q, pool, pool, table, lens, lens, lens, 0.1, 2, 16, max_group_size=1, max_prefix_len=0)
+    with pytest.raises(ValueError):
+        P.pa_rotary_and_cache(q, q, q, q, pool, pool, lens.long(), lens, [0.1] * 32)
