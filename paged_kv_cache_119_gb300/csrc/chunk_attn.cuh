@@ -773,11 +773,13 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         // multiply-adds more than an uncapped score, and no MUFU work beyond its one exp2.
         // Taken by a warp's tile that all its rows see whole and whose scores lie in that
         // range; other tiles take cap_score.  kk outside [10^-6, 8] would take kp3 out of fp32's normal range.
+        // Over E4M3 caches, where bf16 rows came in as 2^e q and kk is as small, the polynomial is
+        // of y itself, one multiply more (always cap_score: 798 against 628 us, 4 x 512 tokens of 8192).
         const float kk = kCap ? sl2 * p.mods.inv_cap : 0.f;
-        const bool cap_fast = kCap && !kSlope && __all_sync(kFullMask, kk >= 1e-6f && kk <= 8.f);
-        const float k2 = kk * kk;
-        const float kp[4] = {kCapP0 * sl2, kCapP1 * sl2 * k2, kCapP2 * sl2 * k2 * k2,
-                             kCapP3 * sl2 * k2 * k2 * k2};
+        const bool cap_fast = kCap && !kSlope && __all_sync(kFullMask, kF8 || (kk >= 1e-6f && kk <= 8.f));
+        const float k1 = kF8 ? p.mods.cap : sl2, k2 = kF8 ? 1.f : kk * kk;
+        const float kp[4] = {kCapP0 * k1, kCapP1 * k1 * k2, kCapP2 * k1 * k2 * k2,
+                             kCapP3 * k1 * k2 * k2 * k2};
         auto poly_at = [&](float z) { return fmaf(fmaf(fmaf(kp[3], z, kp[2]), z, kp[1]), z, kp[0]); };
         const bool warp_live = __any_sync(kFullMask, row_valid);
         const uint32_t lane_t = tbase + ((uint32_t)(32 * wq) << 16);
@@ -868,8 +870,10 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     smax = row_max(s);
                 }
                 float tmax = smax == -INFINITY ? -INFINITY : smax * mul;
-                if (kCap && poly)
-                    tmax = smax * poly_at(smax * smax);
+                if (kCap && poly) {
+                    const float y = kF8 ? smax * kk : smax;
+                    tmax = y * poly_at(y * y);
+                }
                 const bool need = tmax > m_ref + 8.f;
                 if (it > 0 && __any_sync(kFullMask, need)) {
                     // O holds P.V of tiles 0 .. it-1: wait for the last, then rescale the
@@ -903,20 +907,34 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 const float nm = (m_ref == -INFINITY ? 0.f : -m_ref) + kChunkPExp;
                 float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                  make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                // (one loop for either form of the scores: a test in one loop for both cost 13 %
+                // where the cap bites)
+                auto weights = [&](auto capped) {
 #pragma unroll
-                for (int c = 0; c < NT; c += 2) {
-                    float2 f = make_float2(mul, mul);
-                    if (kCap && poly) {
-                        const float2 z = fmul2(make_float2(s[c], s[c + 1]), make_float2(s[c], s[c + 1]));
-                        f = ffma2(z, make_float2(kp[3], kp[3]), make_float2(kp[2], kp[2]));
-                        f = ffma2(z, f, make_float2(kp[1], kp[1]));
-                        f = ffma2(z, f, make_float2(kp[0], kp[0]));
+                    for (int c = 0; c < NT; c += 2) {
+                        float2 f = make_float2(mul, mul), y = make_float2(s[c], s[c + 1]);
+                        if constexpr (capped.value) {
+                            if (kF8)
+                                y = fmul2(y, make_float2(kk, kk));
+                            const float2 z = fmul2(y, y);
+                            f = ffma2(z, make_float2(kp[3], kp[3]), make_float2(kp[2], kp[2]));
+                            f = ffma2(z, f, make_float2(kp[1], kp[1]));
+                            f = ffma2(z, f, make_float2(kp[0], kp[0]));
+                        }
+                        const float2 x = ffma2(y, f, make_float2(nm, nm));
+                        s[c] = ex2_approx(x.x);
+                        s[c + 1] = ex2_approx(x.y);
+                        acc[(c >> 1) & 3] = ffma2(make_float2(s[c], s[c + 1]), make_float2(1.f, 1.f),
+                                                  acc[(c >> 1) & 3]);
                     }
-                    const float2 x = ffma2(make_float2(s[c], s[c + 1]), f, make_float2(nm, nm));
-                    s[c] = ex2_approx(x.x);
-                    s[c + 1] = ex2_approx(x.y);
-                    acc[(c >> 1) & 3] = ffma2(make_float2(s[c], s[c + 1]), make_float2(1.f, 1.f),
-                                              acc[(c >> 1) & 3]);
+                };
+                if constexpr (kCap && !kSlope) {
+                    if (poly)
+                        weights(std::true_type{});
+                    else
+                        weights(std::false_type{});
+                } else {
+                    weights(std::false_type{});
                 }
                 lsum += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) +
                         ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y));
