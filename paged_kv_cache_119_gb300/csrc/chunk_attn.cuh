@@ -832,13 +832,21 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                             // |pos - t| = pos - t while no column lies behind pos
                             const float far0 = (float)(pos - tb);
                             if (lim >= NT - 1 || !row_valid) {
-                                const float2 base = make_float2(-slope * far0, -slope * far0);
+                                // the bias of columns c, c + 1 advances by eight columns at a time
+                                // (eight roundings a tile at most)
+                                const float2 one = make_float2(1.f, 1.f);
+                                const float2 step = make_float2(8.f * slope, 8.f * slope);
+                                float2 d[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    d[k] = make_float2(-slope * (far0 - (float)(2 * k)),
+                                                       -slope * (far0 - (float)(2 * k + 1)));
 #pragma unroll
                                 for (int c = 0; c < NT; c += 2) {
-                                    const float2 d = ffma2(make_float2(slope, slope),
-                                                           make_float2((float)c, (float)(c + 1)), base);
+                                    const int k = (c >> 1) & 3;
                                     const float2 x = ffma2(make_float2(s[c], s[c + 1]),
-                                                           make_float2(mul, mul), d);
+                                                           make_float2(mul, mul), d[k]);
+                                    d[k] = ffma2(step, one, d[k]);
                                     s[c] = x.x;
                                     s[c + 1] = x.y;
                                 }
