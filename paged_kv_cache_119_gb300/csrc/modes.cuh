@@ -27,7 +27,10 @@ cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, dim3 block, size
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = overlap ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (err != cudaSuccess)
+        (void)cudaGetLastError();                // reported to the caller: not left for a later call
+    return err;
 }
 
 // Whether the kernel may start while the one before it in the stream still runs.

@@ -369,7 +369,7 @@ cudaError_t launch_tc8_mode(const DecodeParams& p, AttnMode mode, pa_dtype q_dty
                             int rows, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                             cudaStream_t stream);
 int occupancy_tc8_mode(AttnMode mode, pa_dtype q_dtype, int block_size, int rows);
-// chunk_attn_kernel, kMod and kPrefix:
+// chunk_attn_kernel, modified scores and kPrefix:
 cudaError_t launch_chunk_f16(const ChunkParams& p, AttnMode mode, int head_dim, int block_size,
                        const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                        cudaStream_t stream);

@@ -1,7 +1,7 @@
 // score_mods.cuh -- what the attention kernels share beyond the plain causal softmax:
 // modified scores (tanh cap, distance bias, window, tokens every row sees) and the tile
-// order they leave to read, for decode_kernel, decode_mma_kernel, decode_tc8_kernel and
-// chunk_attn_kernel.
+// order they leave to read, for decode_kernel, decode_mma_kernel, decode_rows_kernel,
+// decode_tc8_kernel and chunk_attn_kernel.
 //
 // The score of a row at position pos and token t is, with x = scale q.k,
 //     cap tanh(x / cap) - slope |pos - t|,
@@ -14,10 +14,10 @@
 
 namespace pa {
 
-// The two passes of a shared-prefix decode overlap: neither needs the other.  The prefix pass
-// lets the suffix pass start as soon as all its CTAs have; the suffix grid has one z-slice more
-// than sequences, whose first CTA waits for the prefix pass, so that the suffix grid does not
-// complete before it and the merge, which waits for the suffix grid, sees both.
+// Every pass in a mode lets the launch behind it start as soon as all its CTAs have.  The two
+// passes of a shared-prefix decode overlap so: neither needs the other.  The suffix grid has one
+// z-slice more than sequences, whose first CTA waits for the prefix pass, so that the suffix
+// grid does not complete before it and the merge, which waits for the suffix grid, sees both.
 // Returns true for a CTA of that slice, which has nothing else to do.
 template <int MODE>
 __device__ __forceinline__ bool overlap_passes(int num_seqs)
