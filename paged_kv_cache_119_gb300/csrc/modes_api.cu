@@ -290,7 +290,8 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || (!decode && !query_start))
         return PA_ERR_INVALID;
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
-        !aligned4(alibi_slopes) || !aligned4(global_lens))
+        !aligned4(alibi_slopes) || !aligned4(global_lens) || !aligned4(block_tables) ||
+        !aligned4(context_lens) || !aligned4(query_start) || !aligned4(k_scale) || !aligned4(v_scale))
         return PA_ERR_INVALID;
     if (!global_lens)
         max_global_len = 0;
@@ -506,7 +507,9 @@ int prefix_impl(void* out, pa_dtype out_dtype, const void* q, const Shape& s, co
         return PA_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !prefix_lens || !group_start)
         return PA_ERR_INVALID;
-    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned4(block_tables) || !aligned4(context_lens) || !aligned4(prefix_lens) ||
+        !aligned4(group_start) || !aligned4(k_scale) || !aligned4(v_scale))
         return PA_ERR_INVALID;
     const PrefixPlan pl = prefix_plan(s, num_seqs, num_groups, max_group_size, max_prefix_len,
                                       max_suffix_len, partition_size);

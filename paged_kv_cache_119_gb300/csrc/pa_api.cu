@@ -899,6 +899,10 @@ static int rotary_impl(void* q_out, int64_t q_out_stride, const void* q, int64_t
             return PA_ERR_INVALID;
     if (!aligned16(k_cache) || !aligned16(v_cache))
         return PA_ERR_INVALID;
+    auto natural = [](const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+    if (!natural(slot_mapping, 8) || !natural(positions, 4) || !natural(inv_freq, 8) ||
+        !natural(k_scale, 4) || !natural(v_scale, 4))
+        return PA_ERR_INVALID;
     const size_t pool_bytes = (size_t)num_blocks * num_kv_heads * block_size * head_dim *
                               (fp8 ? 1 : (size_t)esz);
     if (overlaps(k_cache, pool_bytes, v_cache, pool_bytes))

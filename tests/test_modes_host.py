@@ -145,3 +145,21 @@ def test_the_binding_refuses_host_tensors():
         P.pa_decode_prefix(q, q, pool, pool, table, lens, lens, lens, 0.1, 2, 16, max_group_size=1, max_prefix_len=0)
     with pytest.raises(ValueError):
         P.pa_rotary_and_cache(q, q, q, q, pool, pool, lens.long(), lens, [0.1] * 32)
+
+
+@pytest.mark.parametrize("name", ["table", "lens", "slopes", "glob"])
+def test_decode_mod_rejects_unaligned_arrays(lib, name):
+    a = decode_args(slopes=FAKE * 11, glob=FAKE * 12, max_glob=4)
+    a[name] += 2
+    assert lib.pa_decode_mod(*a.values()) == INV
+
+
+@pytest.mark.parametrize("name", ["table", "lens", "plens", "start"])
+def test_prefix_rejects_unaligned_arrays(lib, name):
+    a = prefix_args()
+    a[name] += 2
+    assert lib.pa_decode_prefix(*a.values()) == INV
+
+
+def test_chunk_mod_rejects_an_unaligned_query_start(lib):
+    assert lib.pa_chunk_attention_mod(*chunk_args(start=FAKE * 7 + 2).values()) == INV

@@ -112,3 +112,8 @@ def test_rotary_fp8_rejects(lib):
     assert call(FAKE * 9, FAKE * 10, D=24, rot=24, q_out_stride=96, q_stride=96, k_stride=48,
                 v_stride=48) == N.PA_ERR_UNSUPPORTED
     assert call(FAKE * 9, FAKE * 10, tokens=0) == N.PA_OK    # nothing to do, no launch
+
+
+@pytest.mark.parametrize("kw", [dict(slots=FAKE * 7 + 4), dict(positions=FAKE * 8 + 2)])
+def test_rotary_rejects_unaligned_arrays(lib, kw):
+    assert lib.pa_rotary_and_cache(*rotary_args(**kw).values()) == N.PA_ERR_INVALID
