@@ -98,7 +98,9 @@ int rows_tile(const Shape& s, int per)
 // than a 16-row matrix fragment that is mostly empty (the rule of pa_decode); E4M3 codes at
 // head_dim 128 go to the tensor core as they are for up to four rows.  Other groups take
 // the next of 4, 8, 16, 32 or 64 rows, padded, so that a K/V byte is read once whatever the
-// group.
+// group.  Capped decode of contexts up to 2048, this rule's kernel against mma.sync: f16, one head
+// (64 sequences, 40 kv heads) 195 against 237 us, bf16, two heads (128, 20) 205 against 238; E4M3,
+// one head 105 against 170, four heads (256, 8) 97 against 139.
 Plan plan_heads(const Shape& s)
 {
     Plan pl{};
@@ -296,6 +298,9 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
     if (!global_lens)
         max_global_len = 0;
     const int qlen = decode ? 1 : max_query_len;
+    // (32 rows of a chunk on a decode kernel's row mode against the chunk kernel, 32 sequences,
+    // capped: 35.1 against 49.3 us over a window of 1024, 198 against 278 over 8192 tokens; 64 rows
+    // 60.2 against 51.4 and 377 against 280)
     Plan pl = decode ? plan_heads(s) : plan_rows(s, qlen, kChunkRowsMax);
     AttnMode mode = kMod;
     const bool cap = softcap > 0.f, slope = alibi_slopes != nullptr;
