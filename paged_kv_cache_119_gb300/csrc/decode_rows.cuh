@@ -275,11 +275,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     const int c = lane & 3;           // fragment column pair
     const int W0 = R0 + (warp % RW) * kRowsGroup;     // the warp's first row
     const bool idle = W0 / p.group >= n;              // no row of the group exists
-    // per row (g, g + 8): live, last visible position, and for kMod the first one past the
-    // global tokens, the global tokens and the base-2 distance slope
+    // per row (g, g + 8): live, and for kMod its position and the base-2 distance slope; a row
+    // sees token t when t < seen.glob or position - t is in [0, reach)
     bool live[2];
-    int lim[2], low[2], glob[2];
+    int lim[2];
     float slope[2];
+    const unsigned reach = kIsMod && p.mods.window > 0 ? (unsigned)p.mods.window : 0x80000000u;
     uint32_t qa[KS][4];               // A fragments of Q
     float q_unscale = 1.f;            // E4M3 caches: q was scaled by 2^-e to fit f16
 #pragma unroll
@@ -287,18 +288,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         const int R = W0 + g + 8 * j;
         const int tok = R / p.group;
         live[j] = tok < n;
-        lim[j] = kIsMod ? L - n + tok : L - 1;
-        low[j] = 0;
-        glob[j] = 0;
+        // (a padding row, all zeros and never stored, may see anything)
+        lim[j] = kIsMod ? L - n + tok : 0;
         slope[j] = 0.f;
-        if (kIsMod && live[j]) {
-            low[j] = p.mods.window > 0 ? max(0, lim[j] - p.mods.window + 1) : 0;
-            glob[j] = seen.glob;
-            if (has_slope(MODE) && p.mods.slopes)
-                slope[j] = p.mods.slopes[kvh * p.group + (R - tok * p.group)] * 1.4426950408889634f;
-        }
-        if (!live[j])
-            lim[j] = -1;
+        if (has_slope(MODE) && live[j] && p.mods.slopes)
+            slope[j] = p.mods.slopes[kvh * p.group + (R - tok * p.group)] * 1.4426950408889634f;
         const uint32_t* qrow = reinterpret_cast<const uint32_t*>(reinterpret_cast<const T*>(p.q) +
                                                                  (live[j] ? out_row(R) : 0) * D);
 #pragma unroll
@@ -451,7 +445,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int tt = 8 * h + 2 * c + (k & 1), t = tb + tt, j = k >> 1;
-                    const bool sees = kIsMod ? t < glob[j] || (t >= low[j] && t <= lim[j]) : tt < nvalid;
+                    const bool sees = kIsMod ? t < seen.glob || (unsigned)(lim[j] - t) < reach : tt < nvalid;
                     s[h][k] = sees ? s[h][k] : -INFINITY;
                 }
         }
