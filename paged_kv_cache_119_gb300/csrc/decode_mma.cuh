@@ -542,8 +542,9 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[kvh] * q_unscale : p.scale_log2;
     // chunk rows: the last visible position of rows 2c and 2c+1 (-1: padding row)
     int lim[2] = {0, 0};
-    // kMod: first visible position past the global tokens, the global tokens, base-2 slope
-    int low[2] = {0, 0}, glob[2] = {0, 0};
+    // kMod: a row at position lim sees token t when t < seen.glob or lim - t is in [0, reach);
+    // its base-2 slope
+    const unsigned reach = kIsMod && p.mods.window > 0 ? (unsigned)p.mods.window : 0x80000000u;
     float slope[2] = {0.f, 0.f};
     // kMod: the first row's last visible position, and where the last row's window starts
     int first_pos = 0, low_max = 0;
@@ -561,12 +562,9 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             const bool live = 2 * c + j < NH && tk < n;
             lim[j] = !live ? -1 : (MODE == kPrefix || MODE == kSuffix) ? L - 1 : L - n + tk;
             if constexpr (kIsMod) {
-                if (live) {
-                    low[j] = p.mods.window > 0 ? max(0, lim[j] - p.mods.window + 1) : 0;
-                    glob[j] = seen.glob;
-                    if (has_slope(MODE) && p.mods.slopes)
-                        slope[j] = p.mods.slopes[kvh * p.group + (R - tk * p.group)] * 1.4426950408889634f;
-                }
+                lim[j] = L - n + tk;               // (a padding row, all zeros, may see anything)
+                if (has_slope(MODE) && live && p.mods.slopes)
+                    slope[j] = p.mods.slopes[kvh * p.group + (R - tk * p.group)] * 1.4426950408889634f;
             }
         }
     }
@@ -674,7 +672,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int r = j & 1, t = tb + (j < 2 ? tok_a : tok_b);
-                        const bool sees = t < glob[r] || (t >= low[r] && t <= lim[r]);
+                        const bool sees = t < seen.glob || (unsigned)(lim[r] - t) < reach;
                         x[j] = sees ? x[j] : -INFINITY;
                     }
                 }

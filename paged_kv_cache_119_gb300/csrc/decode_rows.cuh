@@ -19,7 +19,7 @@
 // w % RW of the tiles w / RW, w / RW + 4 / RW, .., so RW warps share a tile, and up to 64 rows
 // share one read of K and V.  The warps of a row group merge through shared memory at the end.
 // Bound: HBM where 16 rows or fewer share a byte, issue slots of mma.sync and softmax beyond.
-// 32 sequences of 5 new tokens, 4 heads a kv head, f16, a window of 1024: 35 us (3.9 TB/s);
+// 32 sequences of 5 new tokens, 4 heads a kv head, f16, a window of 1024: 33.7 us (4.1 TB/s);
 // the pass over 16 prefixes of 1024 tokens for 8 x 4 rows each, bf16: 18 us.  On decode_mma_kernel
 // (8 rows a CTA) the first took 89 us, on a transposed tcgen05 form of 16 and 32 rows 65.
 // Modes: kMod (chunk rows, or with query_start null the heads of each sequence's last token;
