@@ -1,8 +1,9 @@
 // attn_merge.cuh -- merges the partial rows of the modified-score and the shared-prefix
 // calls.  With per-part maxima m_k (base 2), sums l_k and normalised rows o_k:
 //   M = max m_k,  w_k = 2^(m_k - M) l_k,  o = sum w_k o_k / sum w_k.
-// A part that saw no visible token has m = -inf and weighs nothing; a poisoned part is NaN
-// and makes the row NaN; no visible token at all gives 0.
+// A part that saw no visible token has m = -inf, weight 0 and a row of zeros; a poisoned part's
+// row is NaN and makes the sum NaN whatever its weight (it has none when the part held no valid
+// block); no visible token at all gives the sum of the zeros.
 //
 // The merge is launched behind its pass and starts beside the pass's last CTAs: it finds out
 // whose row it has from the call's inputs, and waits for the pass before it reads a part.
@@ -96,7 +97,7 @@ __device__ __forceinline__ RowPiece<D> merge_parts(const float* ml, const float*
         den += __shfl_xor_sync(kFullMask, den, msk);
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        num.f[e] = den > 0.f ? num.f[e] / den : (den == 0.f ? 0.f : __int_as_float(0x7fc00000));
+        num.f[e] = den > 0.f ? num.f[e] / den : (den == 0.f ? num.f[e] : __int_as_float(0x7fc00000));
     return num;
 }
 
