@@ -21,6 +21,7 @@
 // (4.65 TB/s), 16391 tokens of 32 + 2 x 32 heads, f16 into E4M3, 671 MB, 143 us (4.7 TB/s; the
 // quotients and conversions fill the issue slots).  One CTA per token, or several that share a
 // token's items when the step has few tokens: a step of 4 tokens takes 6.2 us, a launch.
+#include <algorithm>
 #include <type_traits>
 
 #include "pa_device.cuh"
@@ -98,6 +99,20 @@ __device__ __forceinline__ void rot_store(T* p, const float (&f)[VEC])
             }
         }
         *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+}
+
+// Stores the pairs of a vector of 16-bit elements from `pairs` on as they were loaded (a NaN
+// would lose its payload on the way through fp32).
+template <typename T, int VEC>
+__device__ __forceinline__ void rot_store_passed(T* p, const RotRaw<T, VEC>& r, int pairs)
+{
+    if constexpr (VEC == 8) {
+        const uint32_t u[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i >= pairs)
+                reinterpret_cast<uint32_t*>(p)[i] = u[i];
     }
 }
 
@@ -225,9 +240,10 @@ struct RotWalk {
 
 // grid = (tokens, slices); slice blockIdx.y takes every gridDim.y-th group of kRotThreads
 // items of the token.  VEC: elements per item vector (16 bytes), or 1 when a half-layout pair
-// does not line up with 16-byte vectors (R/2 not a multiple of VEC).  The items of a token are, in this order, the turned ones of q and k (half
-// layout: two vectors; interleaved: one), the vectors of q and k past R, and the vectors of v;
-// a thread loads its next item before it works on the present one.  FIX: the turned items of a
+// does not line up with 16-byte vectors (R/2 not a multiple of VEC).  The items of a token are,
+// in this order, the turned ones of q and k (half layout: two vectors; interleaved: one), the
+// vector of each q and k row that interleaved pairs end in, if any, the vectors of q and k past
+// R, and the vectors of v; a thread loads its next item before it works on the present one.  FIX: the turned items of a
 // head divide kRotThreads, so a thread meets the same pairs in every head and keeps their
 // cosines and sines in registers.
 template <typename T, bool FP8, bool INTER, int VEC, bool FIX>
@@ -235,15 +251,14 @@ __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
     rotary_cache_kernel(const __grid_constant__ RotaryParams p)
 {
     constexpr int NP = INTER ? VEC / 2 : VEC;    // pairs of a turned item
-    // (m cos, m sin) of the token's pairs; past the last (a vector that R ends in) (1, 0)
-    __shared__ float2 cs[kRotMaxPairs + NP];
+    __shared__ float2 cs[kRotMaxPairs];          // (m cos, m sin) of the token's pairs
     __shared__ int64_t slot_base;                // element of head 0 of the slot, or -1
     // E4M3: (scale, reciprocal) of the K and V heads, as far as they fit
     __shared__ float2 scales[FP8 ? 2 * kRotScales : 1];
     const int half = p.half;
     const int nv = p.head_dim / VEC;
-    const int nturn = INTER ? (2 * half + VEC - 1) / VEC : half / VEC;   // turned items of a head
-    const int past = INTER ? nturn : 2 * nturn;                          // first vector past R
+    const int nturn = INTER ? 2 * half / VEC : half / VEC;               // turned items of a head
+    const int past = INTER ? (2 * half + VEC - 1) / VEC : 2 * nturn;     // first vector past R
     const int heads = p.num_q_heads + p.num_kv_heads;
     const int step = gridDim.y * kRotThreads;
     const int first = blockIdx.y * kRotThreads + threadIdx.x;
@@ -253,7 +268,7 @@ __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
     constexpr int W = FP8 && VEC == 8 ? 2 : 1;
     const bool pass_wide = past % W == 0;
     const int pw = pass_wide ? W : 1;
-    const RotWalk turn0 = RotWalk::from(first, step, nturn);
+    const RotWalk turn0 = !INTER || nturn > 0 ? RotWalk::from(first, step, nturn) : RotWalk{heads, 0, 0, 0, 1};
     const RotWalk pass0 = past < nv ? RotWalk::from(first, step, (nv - past) / pw) : RotWalk{heads, 0, 0, 0, 1};
     const RotWalk v0 = RotWalk::from(first, step, nv / W);
     if constexpr (FP8) {
@@ -286,16 +301,14 @@ __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
         }
     };
     load_turned(at, xa, xb);
-    for (int i = threadIdx.x; i < half + NP; i += kRotThreads) {
+    for (int i = threadIdx.x; i < half; i += kRotThreads) {
+        // turns as a signed 0.64 fraction in [-1/2, 1/2); half turns = that * 2
+        const int64_t n = p.positions[tok];
+        const long long phase = (long long)((unsigned long long)n * p.phase[i]);
         float s = 0.f, c = 1.f;
-        if (i < half) {
-            // turns as a signed 0.64 fraction in [-1/2, 1/2); half turns = that * 2
-            const int64_t n = p.positions[tok];
-            const long long phase = (long long)((unsigned long long)n * p.phase[i]);
-            sincospif(__ll2float_rn(phase) * 0x1p-63f, &s, &c);
-            c *= p.magnitude;
-            s *= p.magnitude;
-        }
+        sincospif(__ll2float_rn(phase) * 0x1p-63f, &s, &c);
+        c *= p.magnitude;
+        s *= p.magnitude;
         cs[i] = make_float2(c, s);
     }
     if (threadIdx.x == kRotThreads - 1) {
@@ -313,11 +326,12 @@ __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
     __syncthreads();
     const int64_t base = slot_base;
 
+    // (the clamps below hold nothing back: without them the half layouts spill up to 56 bytes more)
     float2 t[NP];
     if constexpr (FIX)
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-            t[i] = cs[min(at.vec * NP + i, half)];
+            t[i] = cs[min(at.vec * NP + i, half - 1)];
     while (at.row < heads) {
         RotWalk nx = at;
         nx.next();
@@ -330,7 +344,7 @@ __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
             if constexpr (!FIX)
 #pragma unroll
                 for (int i = 0; i < NP; ++i)
-                    t[i] = cs[min(at.vec * NP + i, half)];
+                    t[i] = cs[min(at.vec * NP + i, half - 1)];
             float a[VEC], b[VEC];
             rot_float<T, VEC>(xa, a);
             if constexpr (INTER) {
@@ -366,6 +380,38 @@ __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
         at = nx;
         xa = na;
         xb = nb;
+    }
+
+    if constexpr (INTER) {
+        // the vector that R ends in: its first `pairs` pairs turn, the others pass as they are
+        const int pairs = half - nturn * NP;
+        if (pairs > 0)
+            for (int row = first; row < heads; row += step) {
+                const bool is_k = row >= p.num_q_heads;
+                if (is_k && base < 0)
+                    continue;
+                const int h = is_k ? row - p.num_q_heads : row;
+                const int d = nturn * VEC;
+                const RotRaw<T, VEC> x = rot_load<T, VEC>(row_of(row) + d);
+                float a[VEC];
+                rot_float<T, VEC>(x, a);
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    if (i < pairs) {
+                        const float2 r = cs[nturn * NP + i];
+                        const float x0 = a[2 * i], x1 = a[2 * i + 1];
+                        a[2 * i] = fmaf(x0, r.x, -(x1 * r.y));
+                        a[2 * i + 1] = fmaf(x1, r.x, x0 * r.y);
+                    }
+                const int64_t cell = base + h * head_stride + d;
+                if (FP8 && is_k) {
+                    rot_store_e4m3<VEC>(static_cast<unsigned char*>(p.k_cache) + cell, a, scale_of(h, false));
+                } else {
+                    T* dst = is_k ? static_cast<T*>(p.k_cache) + cell : qo + h * p.head_dim + d;
+                    rot_store<T, VEC>(dst, a);
+                    rot_store_passed<T, VEC>(dst, x, pairs);
+                }
+            }
     }
 
     // Vectors that do not turn, bit for bit (or quantised): those of q and k past R, then
@@ -427,8 +473,8 @@ __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
 template <typename T, bool FP8, bool INTER, int VEC>
 cudaError_t launch_variant(const RotaryParams& p, cudaStream_t stream)
 {
-    const int per = INTER ? (2 * p.half + VEC - 1) / VEC : p.half / VEC;
-    const int64_t turned = (int64_t)(p.num_q_heads + p.num_kv_heads) * per;
+    const int per = INTER ? 2 * p.half / VEC : p.half / VEC;
+    const int64_t turned = (int64_t)(p.num_q_heads + p.num_kv_heads) * std::max(per, 1);
     // few tokens: a token's items are shared over CTAs until the grid holds four per SM.  (A CTA
     // that took several tokens in turn, to set up its walks once, measured slower: 155 against
     // 142 us for 16391 tokens into E4M3.)
@@ -437,7 +483,7 @@ cudaError_t launch_variant(const RotaryParams& p, cudaStream_t stream)
     int64_t slices = (4 * (int64_t)sms + p.num_tokens - 1) / p.num_tokens;
     slices = slices < most ? slices : most;
     const dim3 grid((unsigned)p.num_tokens, (unsigned)slices);
-    if (kRotThreads % per == 0)
+    if (per > 0 && kRotThreads % per == 0)
         rotary_cache_kernel<T, FP8, INTER, VEC, true><<<grid, kRotThreads, 0, stream>>>(p);
     else
         rotary_cache_kernel<T, FP8, INTER, VEC, false><<<grid, kRotThreads, 0, stream>>>(p);
