@@ -216,14 +216,19 @@ __device__ __forceinline__ float2 row_range(const float (&s)[kChunkTileTok])
     return make_float2(min3f(fminf(lo[0], lo[1]), lo[2], lo[3]), max3f(fmaxf(hi[0], hi[1]), hi[2], hi[3]));
 }
 
-// Caps a row's 64 scores (s * mul in base-2 units, in place).  Rows of a warp that stay within
-// the cap itself (|y| <= 1, y = x / cap) take the six-term odd polynomial of tanh (least relative
-// error there, 5.9e-7, fitted numerically); others cap_score.
-__device__ __forceinline__ void cap_row(float (&s)[kChunkTileTok], float mul, const ScoreMods& m)
+// Caps a row's 64 scores (s * mul in base-2 units, in place).  Rows of a warp that see the whole
+// tile and stay within the cap itself (|y| <= 1, y = x / cap) take the six-term odd polynomial of
+// tanh (least relative error there, 5.9e-7, fitted numerically); others cap_score (where a score
+// is of a hidden token, what its slot holds chooses nothing).
+__device__ __forceinline__ void cap_row(float (&s)[kChunkTileTok], float mul, const ScoreMods& m, bool whole)
 {
     const float k = mul * m.inv_cap;
-    const float2 mm = row_range(s);
-    if (__all_sync(kFullMask, fmaxf(fabsf(mm.x), fabsf(mm.y)) * fabsf(k) <= 1.f)) {
+    bool within = whole;
+    if (within) {
+        const float2 mm = row_range(s);
+        within = __all_sync(kFullMask, fmaxf(fabsf(mm.x), fabsf(mm.y)) * fabsf(k) <= 1.f);
+    }
+    if (within) {
         constexpr float q[6] = {0.99999941f, -0.33329042f, 0.13281434f, -0.05160568f, 0.01674312f, -0.00306706f};
 #pragma unroll
         for (int c = 0; c < kChunkTileTok; c += 2) {
@@ -826,7 +831,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     if (!poly) {
                         if constexpr (kCap) {
                             mul = 1.f;
-                            cap_row(s, sl2, p.mods);
+                            cap_row(s, sl2, p.mods, whole);
                         }
                         if constexpr (kSlope) {
                             // |pos - t| = pos - t while no column lies behind pos

@@ -644,9 +644,13 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             const int tok_a = 16 * mb + g, tok_b = tok_a + 8;
             float x[4];
             if constexpr (kIsMod) {
-                // scores well within the cap (the usual case): the short form of tanh
+                // all rows see all 16 tokens, but at a window's ends and the last tokens
+                const int b0 = tb + 16 * mb;
+                const bool whole = b0 + 16 <= seen.glob || (b0 + 15 <= first_pos && b0 >= low_max);
+                // scores well within the cap (the usual case): the short form of tanh (only where
+                // no score is of a hidden token: what such a slot holds chooses nothing)
                 bool near_cap = false;
-                if (has_cap(MODE) && p.mods.cap > 0.f) {
+                if (has_cap(MODE) && p.mods.cap > 0.f && whole) {
                     const float far0 = fmaxf(fmaxf(fabsf(s[0]), fabsf(s[1])), fmaxf(fabsf(s[2]), fabsf(s[3])));
                     near_cap = __all_sync(kFullMask, far0 * fabsf(sl2) * p.mods.inv_cap <= kCapNear);
                     if (near_cap) {
@@ -666,9 +670,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                     for (int j = 0; j < 4; ++j)
                         x[j] = fmaf(-slope[j & 1], (float)abs(lim[j & 1] - (tb + (j < 2 ? tok_a : tok_b))), x[j]);
                 }
-                // all rows see all 16 tokens, but at a window's ends and the last tokens
-                const int b0 = tb + 16 * mb;
-                if (!(b0 + 16 <= seen.glob || (b0 + 15 <= first_pos && b0 >= low_max))) {
+                if (!whole) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int r = j & 1, t = tb + (j < 2 ? tok_a : tok_b);

@@ -409,14 +409,19 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             ragged = ragged || (tb < seen.lo && tb + TB > seen.glob);
             mask = !(tb + TB <= seen.glob || (tb + TB - 1 <= first_pos && tb >= low_max));
             if (has_cap(MODE) && p.mods.cap > 0.f) {
-                float far0 = 0.f;
+                // scores well within the cap (the usual case): the short form of tanh (only where
+                // no score is of a hidden token: what such a slot holds chooses nothing)
+                bool near_cap = !mask;
+                if (near_cap) {
+                    float far0 = 0.f;
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
+                    for (int h = 0; h < 4; ++h)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        far0 = fmaxf(far0, fabsf(s[h][k]));
-                // scores well within the cap (the usual case): the short form of tanh
-                if (__all_sync(kFullMask, far0 * p.mods.inv_cap <= kCapNear)) {
+                        for (int k = 0; k < 4; ++k)
+                            far0 = fmaxf(far0, fabsf(s[h][k]));
+                    near_cap = __all_sync(kFullMask, far0 * p.mods.inv_cap <= kCapNear);
+                }
+                if (near_cap) {
 #pragma unroll
                     for (int h = 0; h < 4; ++h)
 #pragma unroll
