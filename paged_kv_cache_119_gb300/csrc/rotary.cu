@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
     rotary_cache_kernel(const __grid_constant__ RotaryParams p)
 {
     constexpr int NP = INTER ? VEC / 2 : VEC;    // pairs of a turned item
-    __shared__ float2 cs[kRotMaxPairs];          // (m cos, m sin) of the token's pairs
+    // (m cos, m sin) of the token's pairs, and (1, 0) past the last
+    __shared__ float2 cs[kRotMaxPairs + NP];
     __shared__ int64_t slot_base;                // element of head 0 of the slot, or -1
     // E4M3: (scale, reciprocal) of the K and V heads, as far as they fit
     __shared__ float2 scales[FP8 ? 2 * kRotScales : 1];
@@ -301,14 +302,16 @@ __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
         }
     };
     load_turned(at, xa, xb);
-    for (int i = threadIdx.x; i < half; i += kRotThreads) {
-        // turns as a signed 0.64 fraction in [-1/2, 1/2); half turns = that * 2
-        const int64_t n = p.positions[tok];
-        const long long phase = (long long)((unsigned long long)n * p.phase[i]);
+    for (int i = threadIdx.x; i < half + NP; i += kRotThreads) {
         float s = 0.f, c = 1.f;
-        sincospif(__ll2float_rn(phase) * 0x1p-63f, &s, &c);
-        c *= p.magnitude;
-        s *= p.magnitude;
+        if (i < half) {
+            // turns as a signed 0.64 fraction in [-1/2, 1/2); half turns = that * 2
+            const int64_t n = p.positions[tok];
+            const long long phase = (long long)((unsigned long long)n * p.phase[i]);
+            sincospif(__ll2float_rn(phase) * 0x1p-63f, &s, &c);
+            c *= p.magnitude;
+            s *= p.magnitude;
+        }
         cs[i] = make_float2(c, s);
     }
     if (threadIdx.x == kRotThreads - 1) {
@@ -331,7 +334,7 @@ __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
     if constexpr (FIX)
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-            t[i] = cs[min(at.vec * NP + i, half - 1)];
+            t[i] = cs[min(at.vec * NP + i, half)];
     while (at.row < heads) {
         RotWalk nx = at;
         nx.next();
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
             if constexpr (!FIX)
 #pragma unroll
                 for (int i = 0; i < NP; ++i)
-                    t[i] = cs[min(at.vec * NP + i, half - 1)];
+                    t[i] = cs[min(at.vec * NP + i, half)];
             float a[VEC], b[VEC];
             rot_float<T, VEC>(xa, a);
             if constexpr (INTER) {
