@@ -112,6 +112,15 @@ struct Mma<__half> {
     }
 };
 
+// bf16 queries become f16 operands over E4M3 caches: the exponent of the power of two that puts a
+// row's largest |q| in [2^14, 2^15) (at most 2^126), so that the 8-bit mantissas convert exactly
+// down to 2^-28 of it.  0 for rows of zeros, of bf16 subnormals, and with an infinity or NaN.
+__device__ __forceinline__ int f16_row_shift(float amax)
+{
+    const int ex = (__float_as_int(amax) >> 23) & 0xff;    // amax in [2^(ex - 127), 2^(ex - 126))
+    return ex == 0 || ex == 255 ? 0 : min(126, 141 - ex);
+}
+
 // Converts one raw E4M3 tile [B][D] (row-major bytes) into the 128-byte-swizzled
 // 16-bit layout the tensor-map TMA produces: D/64 regions of B rows x 128 bytes,
 // the 16-byte chunk j of row r stored at chunk position j ^ (r & 7).  One lane per
@@ -479,6 +488,9 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     // Q^T fragments: b0 = q[head g][16ks + 2c, +1], b1 = q[head g][16ks + 2c + 8, +9]
     uint32_t qb[KS][2];
     float q_unscale = 1.f;            // for E4M3 caches: q was scaled by 2^-e to fit f16
+    // the other modes scale each bf16 row by a power of its own (f16_row_shift), up or down
+    constexpr bool kRowScale = kFp8 && !std::is_same_v<T, __half> && MODE != kPlain;
+    float row_unscale[2] = {1.f, 1.f};               // of rows 2c and 2c+1
     {
         bool live = g < NH;
         int64_t qr = (int64_t)seq * p.num_q_heads + h0 + (live ? g : 0);
@@ -499,7 +511,30 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             qb[ks][0] = live ? __ldg(qrow + d0 / 2) : 0u;
             qb[ks][1] = live ? __ldg(qrow + d1 / 2) : 0u;
         }
-        if constexpr (kFp8 && !std::is_same_v<T, __half>) {
+        if constexpr (kRowScale) {
+            float amax = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 f = Mma<T>::unpack(qb[ks][j]);
+                    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));     // of row g
+            amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
+            const int sh = f16_row_shift(amax);
+            const float up = __int_as_float((127 + sh) << 23);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 f = Mma<T>::unpack(qb[ks][j]);
+                    qb[ks][j] = Mma<__half>::pack(f.x * up, f.y * up);
+                }
+            const float un = __int_as_float((127 - sh) << 23);
+            row_unscale[0] = __shfl_sync(kFullMask, un, 8 * c);          // lane of row 2c
+            row_unscale[1] = __shfl_sync(kFullMask, un, 8 * c + 4);
+        } else if constexpr (kFp8 && !std::is_same_v<T, __half>) {
             // bf16 queries become f16 operands: scale by a power of two 2^-e so that the
             // largest |q| of the CTA's heads stays below 2^15 (no overflow; the scaling
             // is exact), and fold 2^e back into the scores
@@ -540,6 +575,8 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     bool poisoned = false;
     // scores carry the softmax scale (base 2) and, for a quantised cache, the K scale
     const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[kvh] * q_unscale : p.scale_log2;
+    const float row_sl2[2] = {sl2 * row_unscale[0], sl2 * row_unscale[1]};
+    auto sl2_of = [&](int j) -> float { return kRowScale ? row_sl2[j & 1] : sl2; };   // of s[j]
     // chunk rows: the last visible position of rows 2c and 2c+1 (-1: padding row)
     int lim[2] = {0, 0};
     // kMod: a row at position lim sees token t when t < seen.glob or lim - t is in [0, reach);
@@ -651,17 +688,22 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                 // no score is of a hidden token: what such a slot holds chooses nothing)
                 bool near_cap = false;
                 if (has_cap(MODE) && p.mods.cap > 0.f && whole) {
-                    const float far0 = fmaxf(fmaxf(fabsf(s[0]), fabsf(s[1])), fmaxf(fabsf(s[2]), fabsf(s[3])));
-                    near_cap = __all_sync(kFullMask, far0 * fabsf(sl2) * p.mods.inv_cap <= kCapNear);
+                    float far0;
+                    if constexpr (kRowScale)
+                        far0 = fmaxf(fmaxf(fabsf(s[0]), fabsf(s[2])) * fabsf(row_sl2[0]),
+                                     fmaxf(fabsf(s[1]), fabsf(s[3])) * fabsf(row_sl2[1]));
+                    else
+                        far0 = fmaxf(fmaxf(fabsf(s[0]), fabsf(s[1])), fmaxf(fabsf(s[2]), fabsf(s[3]))) * fabsf(sl2);
+                    near_cap = __all_sync(kFullMask, far0 * p.mods.inv_cap <= kCapNear);
                     if (near_cap) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            s[j] = cap_score_near(s[j] * sl2, p.mods);
+                            s[j] = cap_score_near(s[j] * sl2_of(j), p.mods);
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[j] = near_cap ? s[j] : s[j] * sl2;
+                    x[j] = near_cap ? s[j] : s[j] * sl2_of(j);
                     if (has_cap(MODE) && p.mods.cap > 0.f && !near_cap)
                         x[j] = cap_score(x[j], p.mods);
                 }
@@ -679,10 +721,10 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                     }
                 }
             } else {
-                x[0] = tok_a < nvalid ? s[0] * sl2 : -INFINITY;
-                x[1] = tok_a < nvalid ? s[1] * sl2 : -INFINITY;
-                x[2] = tok_b < nvalid ? s[2] * sl2 : -INFINITY;
-                x[3] = tok_b < nvalid ? s[3] * sl2 : -INFINITY;
+                x[0] = tok_a < nvalid ? s[0] * sl2_of(0) : -INFINITY;
+                x[1] = tok_a < nvalid ? s[1] * sl2_of(1) : -INFINITY;
+                x[2] = tok_b < nvalid ? s[2] * sl2_of(2) : -INFINITY;
+                x[3] = tok_b < nvalid ? s[3] * sl2_of(3) : -INFINITY;
             }
             if constexpr (CH && MODE == kPlain) {
                 // causal within the chunk: token t is visible to a row at position >= t

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     float slope[2];
     const unsigned reach = kIsMod && p.mods.window > 0 ? (unsigned)p.mods.window : 0x80000000u;
     uint32_t qa[KS][4];               // A fragments of Q
-    float q_unscale = 1.f;            // E4M3 caches: q was scaled by 2^-e to fit f16
+    float row_unscale[2] = {1.f, 1.f};   // bf16 rows over E4M3 caches were scaled to fit f16
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int R = W0 + g + 8 * j;
@@ -306,31 +306,31 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         }
     }
     if constexpr (kFp8 && !std::is_same_v<T, __half>) {
-        // bf16 queries become f16 operands: a power of two 2^-e keeps the largest |q| of the
-        // warp below 2^15 (exact), and 2^e goes back into the scores
-        float amax = 0.f;
+        // bf16 queries become f16 operands, each row scaled by a power of two (f16_row_shift)
+        // that goes back into its scores
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+        for (int j = 0; j < 2; ++j) {
+            float amax = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = Mma<T>::unpack(qa[ks][j]);
-                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int msk = 16; msk >= 1; msk >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, msk));
-        int e = 0;
-        if (amax >= 32768.f)
-            e = ((__float_as_int(amax) >> 23) & 0xff) - 127 - 14;
-        const float down = __int_as_float((127 - e) << 23);
-        q_unscale = __int_as_float((127 + e) << 23);
+                for (int k = j; k < 4; k += 2) {
+                    const float2 f = Mma<T>::unpack(qa[ks][k]);
+                    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, 2));
+            const int sh = f16_row_shift(amax);
+            const float up = __int_as_float((127 + sh) << 23);
+            row_unscale[j] = __int_as_float((127 - sh) << 23);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = Mma<T>::unpack(qa[ks][j]);
-                qa[ks][j] = Mma<__half>::pack(f.x * down, f.y * down);
-            }
+                for (int k = j; k < 4; k += 2) {
+                    const float2 f = Mma<T>::unpack(qa[ks][k]);
+                    qa[ks][k] = Mma<__half>::pack(f.x * up, f.y * up);
+                }
+        }
     }
     float m[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
     // O fragments of column block i: (row g, dims x, y), (row g + 8, dims x, y); x, y =
@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         for (int j = 0; j < 4; ++j)
             o[i][j] = 0.f;
     bool poisoned = false;
-    const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[kvh] * q_unscale : p.scale_log2;
+    const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[kvh] : p.scale_log2;
+    const float row_sl2[2] = {sl2 * row_unscale[0], sl2 * row_unscale[1]};
 
     for (int it = warp / RW; it < ntiles; it += TW) {
         const int stage = it % NSTAGE;
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         for (int h = 0; h < 4; ++h)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                s[h][k] *= sl2;
+                s[h][k] *= row_sl2[k >> 1];
         bool ragged = nvalid < TB;                // some tokens are outside, or seen by no row
         bool mask = ragged;                       // some row does not see some token
         if constexpr (kIsMod) {
