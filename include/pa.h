@@ -525,11 +525,8 @@ int pa_chunk_attention_mod_fp8(void* out, pa_dtype out_dtype, const void* q, pa_
  * prefix length 0, is fine).  The first prefix_lens[s] tokens of a sequence are the ones its
  * group shares: whole blocks (a multiple of block_size, equal within a group), whose table
  * entries are read from the group's first sequence; the others of the group name the same
- * blocks.  out is what pa_decode returns for the same tables and lengths (up to rounding:
- * with max_group_size * num_q_heads / num_kv_heads > 32 the prefix runs on the tcgen05 chunk
- * kernel, whose probabilities are one f16 term; see pa_chunk_attention, also for V elements
- * without an f16 value over a bf16 cache, PA_DEVERR_RANGE.  E4M3 caches at head_dim 64 stay
- * on the decode kernels).
+ * blocks.  out is what pa_decode returns for the same tables and lengths, up to fp32 rounding
+ * and that of the probabilities to two 16-bit terms (2^-16), whatever the size of the groups.
  *
  *   prefix_lens      DEVICE int32 [num_seqs], 0 <= prefix_lens[s] <= context_lens[s]
  *   group_start      DEVICE int32 [num_groups + 1], non-decreasing

@@ -49,6 +49,10 @@
 // range.  A value without an f16 value (|v| >= 65536, infinite or NaN) becomes
 // infinite or NaN; the epilogue sets PA_DEVERR_RANGE for a row whose probabilities are
 // finite but whose O is not.  K stays bf16 (the score product is bf16 x bf16).
+// Over a shared prefix (kPrefix), whose result has to be the plain decode's, P enters as hi + lo
+// terms of V's own type instead (2^-16 relative in bf16, 2^-22 in f16), which fill the 64 columns
+// of the S buffer, and V is not converted: two products where there was one, and no converter
+// warps over bf16 caches.
 // Long contexts with few CTAs are split into partitions merged by
 // chunk_reduce_kernel, as in the decode path.
 // The epilogue reads O once its issuer's one-phase completion barrier has fired (P.V of
@@ -194,6 +198,27 @@ __device__ __forceinline__ float min3f(float a, float b, float c)
     return r;
 }
 
+// Two values as one word of two 16-bit ones (a in the low half), rounded to nearest, and back.
+template <typename TM>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b)
+{
+    if constexpr (DType<TM>::id == PA_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+template <typename TM>
+__device__ __forceinline__ float2 unpack_pair(uint32_t w)
+{
+    if constexpr (DType<TM>::id == PA_BF16)
+        return make_float2(bf16_lo(w), bf16_hi(w));
+    else
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
 // Smallest (x) and largest (y) of a row's 64 scores.
 __device__ __forceinline__ float2 row_range(const float (&s)[kChunkTileTok])
 {
@@ -262,8 +287,9 @@ __device__ __forceinline__ void cap_row(float (&s)[kChunkTileTok], float mul, co
 template <typename T, int NRAW, int MODE>
 constexpr int chunk_threads()
 {
-    return (NRAW > 0 || std::is_same_v<T, __nv_bfloat16> || is_mod(MODE)) ? kChunkThreadsConv
-                                                                          : kChunkThreads;
+    return (NRAW > 0 || (std::is_same_v<T, __nv_bfloat16> && MODE != kPrefix) || is_mod(MODE))
+               ? kChunkThreadsConv
+               : kChunkThreads;
 }
 
 template <typename T, int D, int BS, int NST, int NRAW = 0, int MODE = kPlain>
@@ -274,7 +300,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     using Sm = ChunkSmem<D, NST, NRAW>;
     constexpr bool kF8 = NRAW > 0;
     constexpr bool kIsMod = is_mod(MODE), kCap = has_cap(MODE), kSlope = has_slope(MODE);
-    constexpr bool kVConv = !kF8 && std::is_same_v<T, __nv_bfloat16>;   // bf16 V -> f16 in place
+    constexpr bool kTwoTerms = MODE == kPrefix;  // P as hi + lo of V's type, else one f16 term
+    constexpr bool kVConv = !kF8 && std::is_same_v<T, __nv_bfloat16> && !kTwoTerms;   // bf16 V -> f16 in place
     constexpr bool kVHand = kVConv || (!kF8 && kIsMod);           // V handed over (vconv)
     constexpr bool kVZero = !kVConv && !kIsMod;    // softmax warps zero the last tile's V rows
     using TM = std::conditional_t<kF8, __half, T>;   // operand type of the score product
@@ -633,7 +660,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         if (lane == 0) {
             const uint32_t sq = smem_addr(smem + Sm::kQOff + q * Sm::kQTile);
             const uint32_t idesc_s = mma_idesc_f16(kBf16, kChunkRows, NT, false);
-            const uint32_t idesc_o = mma_idesc_f16(false, kChunkRows, D, true);   // f16 P, V
+            const uint32_t idesc_o = mma_idesc_f16(kTwoTerms && kBf16, kChunkRows, D, true);   // f16 P, V
             bool ok = mbar_wait(q_full, 0);
             // S of tile it into this query tile's S buffer it & 1
             auto issue_scores = [&](int it) {
@@ -684,6 +711,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     const uint64_t b = sw128_desc(vb + kk * 16 * 128, Sm::kKVHalf, 1024);
                     tc_mma_f16_ts(tbase + q * 128, pcol + kk * 8, b, idesc_o,
                                   (it > 0 || kk > 0) ? 1u : 0u);
+                    if constexpr (kTwoTerms)
+                        tc_mma_f16_ts(tbase + q * 128, pcol + NT / 2 + kk * 8, b, idesc_o, 1u);
                 }
                 tc_commit(&pv_done[q]);
                 tc_commit(&empty[it % NST]);
@@ -952,7 +981,17 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 lsum += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) +
                         ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y));
             }
-            if (warp_live) {
+            if (kTwoTerms && warp_live) {
+                // P over the S buffer: hi pairs in the first 32 columns, lo pairs in the others
+                uint32_t w[NT];
+#pragma unroll
+                for (int k = 0; k < NT / 2; ++k) {
+                    w[k] = pack_pair<TM>(s[2 * k], s[2 * k + 1]);
+                    const float2 f = unpack_pair<TM>(w[k]);
+                    w[NT / 2 + k] = pack_pair<TM>(s[2 * k] - f.x, s[2 * k + 1] - f.y);
+                }
+                tmem_st64_raw(sp_col, w);
+            } else if (warp_live) {
                 // P over the first 32 columns of the S buffer, as f16 pairs
                 uint32_t ph[NT / 2];
 #pragma unroll

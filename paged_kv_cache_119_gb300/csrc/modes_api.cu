@@ -459,11 +459,12 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
 }
 
 // (sequence, head) rows per kv head up to which the pass over a shared prefix runs on a decode
-// kernel's row mode; the whole call, row mode against chunk kernel, bf16 / E4M3 caches:
-//   24 rows x 16 groups over 1024 tokens   36.2 against 38.8, 36.9 against 39.1 us
-//   32 rows x 16 groups over 4096          69.5 against 80.7, 72.7 against 76.1
-//   48 rows x 16 groups over 1024          52.1 against 49.0, 58.1 against 51.7
-//   64 rows x 8 groups over 4096           65.0 against 55.9, 74.4 against 58.2
+// kernel's row mode; the whole call, row mode against chunk kernel, bf16 / E4M3 caches, 32/8
+// heads, up to 128 own tokens a sequence:
+//   24 rows x 16 groups over 1024 tokens   27.6 against 31.6, 30.8 against 34.6 us
+//   32 rows x 16 groups over 4096          60.5 against 72.2, 67.3 against 76.7
+//   48 rows x 16 groups over 1024          41.9 against 39.7, 51.1 against 47.8
+//   64 rows x 8 groups over 4096           57.0 against 50.2, 67.2 against 55.5
 constexpr int kPrefixRowsMax = 32;
 
 // The two passes of a shared-prefix decode.
