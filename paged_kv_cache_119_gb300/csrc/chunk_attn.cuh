@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         const int pos = MODE == kPrefix ? L - 1 : pos_first + tok;
         // kMod: first visible position past the global tokens, base-2 distance slope
         const int low = kIsMod && p.mods.window > 0 ? max(0, pos - p.mods.window + 1) : 0;
-        const float slope = kSlope ? p.mods.slopes[kvh * G + g] * 1.4426950408889634f : 0.f;
+        const float slope = kSlope ? base2_slope(p.mods.slopes[kvh * G + g]) : 0.f;
         const int64_t qrow = (int64_t)(qs0 + j0 + tok) * p.num_q_heads + (int64_t)kvh * G + g;
         // scores are used as s * sl2 with sl2 > 0: a negative scale flips the sign of q
         // (exact), a zero scale makes q zero (every score 0); over E4M3 caches the K scale

@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
     if constexpr (MODE == kMod) {
 #pragma unroll
         for (int g = 0; g < GC; ++g)
-            slope[g] = p.mods.slopes ? p.mods.slopes[h0 + g] * 1.4426950408889634f : 0.f;
+            slope[g] = p.mods.slopes ? base2_slope(p.mods.slopes[h0 + g]) : 0.f;
     }
     bool poisoned = false;
     float* my_p = pbuf + warp * GC * BS;

@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             if constexpr (kIsMod) {
                 lim[j] = L - n + tk;               // (a padding row, all zeros, may see anything)
                 if (has_slope(MODE) && live && p.mods.slopes)
-                    slope[j] = p.mods.slopes[kvh * p.group + (R - tk * p.group)] * 1.4426950408889634f;
+                    slope[j] = base2_slope(p.mods.slopes[kvh * p.group + (R - tk * p.group)]);
             }
         }
     }

@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         lim[j] = kIsMod ? L - n + tok : 0;
         slope[j] = 0.f;
         if (has_slope(MODE) && live[j] && p.mods.slopes)
-            slope[j] = p.mods.slopes[kvh * p.group + (R - tok * p.group)] * 1.4426950408889634f;
+            slope[j] = base2_slope(p.mods.slopes[kvh * p.group + (R - tok * p.group)]);
         const uint32_t* qrow = reinterpret_cast<const uint32_t*>(reinterpret_cast<const T*>(p.q) +
                                                                  (live[j] ? out_row(R) : 0) * D);
 #pragma unroll

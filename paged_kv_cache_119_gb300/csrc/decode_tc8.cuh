@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
             if constexpr (MODE == kMod) {
                 low[r] = p.mods.window > 0 ? max(0, lim[r] - p.mods.window + 1) : 0;
                 if (p.mods.slopes && orow[r] >= 0)
-                    slope[r] = p.mods.slopes[orow[r] % p.num_q_heads] * 1.4426950408889634f;
+                    slope[r] = base2_slope(p.mods.slopes[orow[r] % p.num_q_heads]);
             }
         }
         // ---- query terms into Qt: this thread is head dim tl of every row

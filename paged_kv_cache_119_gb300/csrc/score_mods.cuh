@@ -70,6 +70,13 @@ __device__ __forceinline__ float cap_score_near(float x, const ScoreMods& m)
     return x * fmaf(fmaf(fmaf(kCapP3, z, kCapP2), z, kCapP1), z, kCapP0);
 }
 
+// A distance slope in base-2 units, held within +-10^28 so that slope * distance (below 2^30) stays
+// finite for every finite slope: from there on one token of distance already outweighs any score.
+__device__ __forceinline__ float base2_slope(float s)
+{
+    return fminf(fmaxf(s * 1.4426950408889634f, -1e28f), 1e28f);
+}
+
 // Tokens some row of a set sees: [0, glob) and [lo, end), 0 <= glob <= end, lo <= end.
 struct Seen {
     int glob, lo, end;
