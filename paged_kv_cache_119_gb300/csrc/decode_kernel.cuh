@@ -607,16 +607,17 @@ struct CoreVariant {
     {
         return configure_once(reinterpret_cast<const void*>(kernel()), Smem::kBytes);
     }
+    // (the plain mode: the others are launched and merged by modes_api.cu)
     static cudaError_t launch(const DecodeParams& p, cudaStream_t stream)
     {
         cudaError_t err = configure();
         if (err != cudaSuccess)
             return err;
         const bool split = p.partition_tokens > 0;
-        dim3 grid(split ? p.max_parts - p.part_base : 1, p.num_kv_heads * p.chunks, p.num_seqs);
+        dim3 grid(split ? p.max_parts : 1, p.num_kv_heads * p.chunks, p.num_seqs);
         kernel()<<<grid, kDecodeThreads, Smem::kBytes, stream>>>(p);
         err = cudaGetLastError();
-        if (err != cudaSuccess || !split || MODE != kPlain)   // the others merge on their own
+        if (err != cudaSuccess || !split)
             return err;
         reduce_kernel<T, D><<<dim3(p.num_q_heads, p.num_seqs), D, 0, stream>>>(p);
         return cudaGetLastError();

@@ -956,7 +956,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             row = (int64_t)(qs0 + j) * p.num_q_heads + kvh * p.group + (R - j * p.group);
         }
         if (split) {
-            const int64_t prow = row * p.max_parts + (MODE == kSuffix ? p.part_base : 0) + part;
+            const int64_t prow = row * p.max_parts + part;
             p.part_o[prow * D + d] = out;
             if (d == 0) {
                 p.part_ml[prow * 2 + 0] = M;

@@ -698,18 +698,19 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                     poisoned = aborted = true;
                     break;
                 }
-                // rows nv .. 127 are one contiguous span: the 128 threads zero it together,
-                // consecutive 16-byte stores (no bank conflicts)
                 if constexpr (MODE == kMod) {            // rows of unseen tokens, anywhere
                     uint4* vt = reinterpret_cast<uint4*>(smem + st * Sm::kStage + Sm::kTile);
                     for (int j = tl; j < kTc8Tok * 8; j += kTc8Tok)
                         if (!is_seen(seen, tb + j / 8))
                             vt[j] = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    // rows nv .. 127 are one contiguous span: the 128 threads zero it together,
+                    // consecutive 16-byte stores (no bank conflicts)
+                    const int nv = t1 - tb;              // 1 .. 127 rows of the range
+                    uint4* vz = reinterpret_cast<uint4*>(smem + st * Sm::kStage + Sm::kTile + nv * 128);
+                    for (int j = tl; j < (kTc8Tok - nv) * 8; j += kTc8Tok)
+                        vz[j] = make_uint4(0u, 0u, 0u, 0u);
                 }
-                const int nv = MODE == kMod ? min(kTc8Tok, t1 - tb) : t1 - tb;   // rows of the range
-                uint4* vz = reinterpret_cast<uint4*>(smem + st * Sm::kStage + Sm::kTile + nv * 128);
-                for (int j = tl; j < (kTc8Tok - nv) * 8; j += kTc8Tok)
-                    vz[j] = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
             tc_fence_before();
