@@ -991,7 +991,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 for (int k = 0; k < NT / 2; ++k) {
                     w[k] = pack_pair<TM>(s[2 * k], s[2 * k + 1]);
                     const float2 f = unpack_pair<TM>(w[k]);
-                    w[NT / 2 + k] = pack_pair<TM>(s[2 * k] - f.x, s[2 * k + 1] - f.y);
+                    const float2 d = ffma2(f, make_float2(-1.f, -1.f), make_float2(s[2 * k], s[2 * k + 1]));
+                    w[NT / 2 + k] = pack_pair<TM>(d.x, d.y);
                 }
                 tmem_st64_raw(sp_col, w);
             } else if (warp_live) {
