@@ -467,7 +467,8 @@ int pa_chunk_attention_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtyp
  * (NaN included).  Tokens that some row of the call sees must be finite.
  * All other arguments, kinds of cache, output types, checks and errors are those of
  * pa_decode, pa_decode_fp8, pa_chunk_attention and pa_chunk_attention_fp8;
- * max_context_len is at most 2^30.  Workspace: pa_decode_workspace_bytes /
+ * max_context_len is at most 2^30.  Rounding is that of the plain calls: fp32-level, but for long
+ * chunks, whose probabilities are one f16 term (see pa_chunk_attention).  Workspace: pa_decode_workspace_bytes /
  * pa_chunk_workspace_bytes of the same sizes; with a window, in place of max_context_len, of
  * the tokens that a sequence's rows can have to read, in tiles of 128:
  *   128 * (ceil(max_global_len / 128) + (window + max_query_len + 125) / 128 + 1),
@@ -525,8 +526,8 @@ int pa_chunk_attention_mod_fp8(void* out, pa_dtype out_dtype, const void* q, pa_
  * prefix length 0, is fine).  The first prefix_lens[s] tokens of a sequence are the ones its
  * group shares: whole blocks (a multiple of block_size, equal within a group), whose table
  * entries are read from the group's first sequence; the others of the group name the same
- * blocks.  out is what pa_decode returns for the same tables and lengths, up to fp32 rounding
- * and that of the probabilities to two 16-bit terms (2^-16), whatever the size of the groups.
+ * blocks.  out is what pa_decode returns for the same tables and lengths, up to rounding at the
+ * same level (fp32 sums, probabilities to 2^-16), whatever the size of the groups.
  *
  *   prefix_lens      DEVICE int32 [num_seqs], 0 <= prefix_lens[s] <= context_lens[s]
  *   group_start      DEVICE int32 [num_groups + 1], non-decreasing

@@ -10,9 +10,9 @@
 // Bound: reading the parts (a few MB that the passes have just left in L2), so latency.  One
 // warp per (row, head): its lanes read the (m, l) of 32 parts at once and a 16-byte piece of
 // the row each, four parts in flight; the sequence or group that owns the row is found by a
-// 33-way search of all lanes.  6144 rows of 8 parts take 9.8 us from a cold start and 4096 rows
-// of 2 or 3 parts 7.1; one CTA per row with a serial search and serial (m, l) reads took 15.6
-// and 8.7.
+// 33-way search of all lanes.  Alone and from a cold start, 6144 rows of 10 parts take 11.6 us and
+// 4096 rows of 2 or 3 parts 8.4 to 9.9.  (When this form was chosen, one CTA per row with a serial
+// search and serial (m, l) reads took 1.6 and 1.2 times as long.)
 #pragma once
 
 #include "decode_kernel.cuh"

@@ -52,7 +52,9 @@
 // Over a shared prefix (kPrefix), whose result has to be the plain decode's, P enters as hi + lo
 // terms of V's own type instead (2^-16 relative in bf16, 2^-22 in f16), which fill the 64 columns
 // of the S buffer, and V is not converted: two products where there was one, and no converter
-// warps over bf16 caches.
+// warps over bf16 caches.  (1.0 -> 1.2 us a tile of 256 rows.  Modified scores keep the one term
+// of the plain chunk call that they extend: with two, 4 x 512 tokens of 8192, 64/8 heads, capped,
+// took 701 against 588 us.)
 // Long contexts with few CTAs are split into partitions merged by
 // chunk_reduce_kernel, as in the decode path.
 // The epilogue reads O once its issuer's one-phase completion barrier has fired (P.V of

@@ -17,8 +17,8 @@
 //     i + R/2 .., so that every element is read once; the arithmetic is fp32 and each
 //     result is rounded once, to the row type or, divided by the head's scale, to E4M3.
 // Bound: HBM (read q, k, v; write q, and the k and v rows), near which the work per element
-// still shows: 4096 tokens of 64 + 2 x 8 heads of 128, bf16, interleaved, 168 MB, take 36 us
-// (4.65 TB/s), 16391 tokens of 32 + 2 x 32 heads, f16 into E4M3, 671 MB, 143 us (4.7 TB/s; the
+// still shows: 4096 tokens of 64 + 2 x 8 heads of 128, bf16, interleaved, 168 MB, take 34.7 us
+// (4.8 TB/s), 16391 tokens of 32 + 2 x 32 heads, f16 into E4M3, 671 MB, 143 us (4.7 TB/s; the
 // quotients and conversions fill the issue slots).  One CTA per token, or several that share a
 // token's items when the step has few tokens: a step of 4 tokens takes 6.2 us, a launch.
 #include <algorithm>
