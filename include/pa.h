@@ -468,9 +468,10 @@ int pa_chunk_attention_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtyp
  * All other arguments, kinds of cache, output types, checks and errors are those of
  * pa_decode, pa_decode_fp8, pa_chunk_attention and pa_chunk_attention_fp8;
  * max_context_len is at most 2^30.  Rounding is that of the plain calls: fp32-level, but for long
- * chunks, whose probabilities are one f16 term (see pa_chunk_attention).  Workspace: pa_decode_workspace_bytes /
- * pa_chunk_workspace_bytes of the same sizes; with a window, in place of max_context_len, of
- * the tokens that a sequence's rows can have to read, in tiles of 128:
+ * chunks, whose probabilities are one f16 term (see pa_chunk_attention).  Workspace:
+ * pa_decode_workspace_bytes / pa_chunk_workspace_bytes of the same sizes; with a window, in
+ * place of max_context_len, of the tokens that a sequence's rows can have to read, in tiles of
+ * 128:
  *   128 * (ceil(max_global_len / 128) + (window + max_query_len + 125) / 128 + 1),
  * where that is less (max_query_len 1 in a decode call; integer division).  A chunk call's
  * rounding may depend on whether it has a workspace: with one, a last wave that would leave

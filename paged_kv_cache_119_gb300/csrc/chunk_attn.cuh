@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         // multiply-adds more than an uncapped score, and no MUFU work beyond its one exp2.
         // Taken by a warp's tile that all its rows see whole and whose scores lie in that
         // range; other tiles take cap_row.  With kk in [10^-6, 8] the powers of kk and, as
-        // |s| <= 1/2 kk, of s are normal numbers.  kp3 may be subnormal or 0 where sl2 is tiny as
+        // |s| <= 0.5 / kk, of s are normal numbers.  kp3 may be subnormal or 0 where sl2 is tiny as
         // well; its term then errs by at most 2^-150 |s|^7 <= 6 10^-48 / kk^7, 6 10^-6 of a score
         // in base-2 units.
         // Over E4M3 caches, where bf16 rows came in as 2^e q and kk is as small, the polynomial is

@@ -243,9 +243,9 @@ struct RotWalk {
 // does not line up with 16-byte vectors (R/2 not a multiple of VEC).  The items of a token are,
 // in this order, the turned ones of q and k (half layout: two vectors; interleaved: one), the
 // vector of each q and k row that interleaved pairs end in, if any, the vectors of q and k past
-// R, and the vectors of v; a thread loads its next item before it works on the present one.  FIX: the turned items of a
-// head divide kRotThreads, so a thread meets the same pairs in every head and keeps their
-// cosines and sines in registers.
+// R, and the vectors of v; a thread loads its next item before it works on the present one.
+// FIX: the turned items of a head divide kRotThreads, so a thread meets the same pairs in every
+// head and keeps their cosines and sines in registers.
 template <typename T, bool FP8, bool INTER, int VEC, bool FIX>
 __global__ void __launch_bounds__(kRotThreads, FP8 ? 5 : INTER ? 8 : 6)
     rotary_cache_kernel(const __grid_constant__ RotaryParams p)
