@@ -24,13 +24,13 @@ def clear_error_word(built):
     yield
 
 
-@pytest.mark.parametrize("softcap", [0.0, 20.0])
-@pytest.mark.parametrize("slope", [1e20, 3e36, 3e38, -1e20, -3e38])
 SHAPES = [(2, 1, 128, torch.float16, False), (8, 1, 64, torch.bfloat16, False),
           (16, 1, 128, torch.float16, False), (40, 1, 128, torch.bfloat16, False), (4, 1, 128, torch.float16, True),
           (8, 1, 128, torch.bfloat16, True), (16, 1, 128, torch.float16, True), (2, 1, 64, torch.bfloat16, True)]
 
 
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("slope", [1e20, 3e36, 3e38, -1e20, -3e38])
 @pytest.mark.parametrize("Hq,Hkv,D,dtype,fp8,new", [
     (2, 2, 128, torch.float32, False, None),        # (fp32 caches have no chunk call)
     *[(*shape, new) for shape in SHAPES for new in (None, [3, 5, 2], [40, 70, 33])]])
