@@ -25,7 +25,13 @@
  *                         window and tokens that every row sees.
  *   pa_decode_prefix      pa_decode for sequences that share long prefixes, each prefix read
  *                         once for its group.
- * The cache writes and the attention calls have _fp8 forms over E4M3 caches.
+ *   pa_cross_attention    rows of a sequence see all cached tokens of their own sequence,
+ *                         whose number has nothing to do with theirs (an encoder's states).
+ * The cache writes and the attention calls have _fp8 forms over E4M3 caches with a scale for each
+ * kv head, and the following _fp8_block forms over E4M3 caches with a scale for each block and
+ * kv head, which the write finds by itself:
+ *   pa_append_fp8_block, pa_rotary_and_append_fp8_block, pa_decode_fp8_block,
+ *   pa_chunk_attention_fp8_block, pa_cross_attention_fp8_block.
  *
  * Layout (the pages leave the in-block layout to the backend; iaim.asia page,
  * section KV Cache 如何按块分配).  All tensors are dense, row-major, in device
@@ -567,6 +573,129 @@ int pa_decode_prefix_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtype 
                          int32_t num_kv_heads, int32_t head_dim, int32_t block_size, float scale,
                          int32_t partition_size, void* workspace, size_t workspace_bytes,
                          void* stream);
+
+/*
+ * Cross attention: the rows query_start[s] .. query_start[s+1]-1 of q and out (as in
+ * pa_chunk_attention) see all context_lens[s] tokens that block_tables[s] reaches:
+ *   out[row][h] = sum_{t < L_s} a_t v_t,  a_t = exp(scale q[row][h] . k_t) / sum_u exp(..),
+ * for the rows of a decoder over an encoder's states, several beams or a whole prompt of them.
+ * n_s and L_s are unrelated: more rows than tokens is fine, L_s = 0 gives rows of zeros.
+ * All other arguments, types, kernels, roundings and errors are those of
+ * pa_chunk_attention_mod and pa_chunk_attention_mod_fp8 without modifications, but that n_s > L_s
+ * is no error and max_query_len may exceed max_context_len.  Workspace: pa_chunk_workspace_bytes of
+ * the same sizes.  out overlaps no input.
+ */
+int pa_cross_attention(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
+                       const void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                       const int32_t* block_tables, int64_t block_table_stride,
+                       const int32_t* context_lens, const int32_t* query_start,
+                       int64_t num_query_tokens, int32_t max_query_len, int32_t max_context_len,
+                       int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                       int32_t block_size, float scale, int32_t partition_size, void* workspace,
+                       size_t workspace_bytes, void* stream);
+int pa_cross_attention_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
+                           const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, int64_t num_blocks, const int32_t* block_tables,
+                           int64_t block_table_stride, const int32_t* context_lens,
+                           const int32_t* query_start, int64_t num_query_tokens,
+                           int32_t max_query_len, int32_t max_context_len, int32_t num_seqs,
+                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t block_size, float scale, int32_t partition_size, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Block-scaled E4M3 caches: the element of block b, kv head h is code * k_scales[b][h] (K) or
+ * code * v_scales[b][h] (V).  The scales are DEVICE fp32 arrays [num_blocks][scale_stride],
+ * scale_stride >= num_kv_heads, 4-byte aligned, caller-owned; the attention calls take any positive
+ * scales, held within 2^-48 .. 2^48 (a scale beyond counts as that end); the appends write powers
+ * of two.  No calibration is needed, and a block with small values keeps its precision beside one
+ * with large ones.  A block's scales move with it: with scale_stride a multiple of 4 (rows of whole
+ * 16 bytes, 16-byte aligned) pa_copy_blocks and pa_swap_blocks take the two arrays as pools of
+ * block_bytes = 4 * scale_stride.
+ *
+ * pa_append_fp8_block: writes new tokens at the end of their sequences.  Sequence s owns rows
+ * query_start[s] .. query_start[s+1]-1 of k and v (n_s rows): the last n_s of its
+ * context_lens[s] = L_s tokens, as in pa_chunk_attention, so row j goes to position
+ * L_s - n_s + j, found through block_tables[s].  For each block that new tokens touch and each
+ * head, K and V apart:
+ *   s_new = the smallest power of two within 2^-48 .. 2^48 with |x| <= 448 s_new for every finite
+ *           new x; if the block holds earlier tokens (positions before L_s - n_s), no less than the
+ *           block's present scale s_old (held within those bounds)
+ *   codes of those earlier tokens, where s_new > s_old: e4m3(code * (s_old / s_new))
+ *   codes of the new tokens: e4m3(fp32(x) / s_new), rounded to nearest even; magnitudes beyond 448
+ *           saturate, NaN stays NaN
+ * A block whose first slot the call writes is a fresh one, whatever it held.  Slots behind the last
+ * token, and blocks that the call does not touch, stay as they were.  Restating a code by a power
+ * of two is exact but for codes that fall below 2^-6.
+ *   k, v         device, num_tokens rows of [Hkv][D] of `dtype` (PA_F16 or PA_BF16; PA_F32 is
+ *                PA_ERR_UNSUPPORTED); *_stride: elements from one token's row to the next (a
+ *                multiple of 8, at least one row); 16-byte aligned
+ *   k_cache, v_cache, k_scales, v_scales   overlap neither each other nor any input
+ *   max_query_len    host bound on every n_s (sizes the grid)
+ *   head_dim 64 or 128, block_size 16 or 32
+ * Two sequences of a call must not append to the same block (copy it first), and sequences must
+ * not share the block a call appends to.  On the device: n_s > L_s, n_s > max_query_len, L_s beyond the
+ * table row and rows that no sequence owns set PA_DEVERR_CONTEXT_LEN (such a sequence is
+ * skipped, such rows are left alone); a block id outside the pool sets PA_DEVERR_BLOCK_ID and its
+ * tokens are skipped.
+ *
+ * pa_rotary_and_append_fp8_block: the same with K turned by its positions first (in fp32, not rounded
+ * to `dtype` on the way) and q_out[i] = rot(q[i]) as in pa_rotary_and_cache: q, q_out, inv_freq,
+ * rotary_dim, interleaved and magnitude as there.  positions: DEVICE int32 [num_tokens], or NULL for
+ * each token's place in its sequence (L_s - n_s + j).  Rows of skipped sequences get no q_out; the
+ * tokens of an invalid block do.
+ *
+ * pa_decode_fp8_block, pa_chunk_attention_fp8_block, pa_cross_attention_fp8_block: pa_decode_fp8,
+ * pa_chunk_attention_fp8 and pa_cross_attention_fp8 over such caches.  Other arguments, checks,
+ * accuracy and workspace as there (max_context_len at most 2^30; partition_size a multiple of 128;
+ * block_table entries are read, and V rows of slots past the context may hold anything, as
+ * in the modified-score calls).
+ */
+int pa_append_fp8_block(const void* k, int64_t k_stride, const void* v, int64_t v_stride, pa_dtype dtype,
+                        void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                        int64_t scale_stride, int64_t num_blocks, const int32_t* block_tables,
+                        int64_t block_table_stride, const int32_t* context_lens,
+                        const int32_t* query_start, int64_t num_tokens, int32_t max_query_len,
+                        int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        void* stream);
+int pa_rotary_and_append_fp8_block(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                                   const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                   pa_dtype dtype, void* k_cache, void* v_cache, float* k_scales,
+                                   float* v_scales, int64_t scale_stride, int64_t num_blocks,
+                                   const int32_t* block_tables, int64_t block_table_stride,
+                                   const int32_t* context_lens, const int32_t* query_start,
+                                   const int32_t* positions, int64_t num_tokens, int32_t max_query_len,
+                                   int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, const double* inv_freq,
+                                   int32_t rotary_dim, int32_t interleaved, float magnitude, void* stream);
+int pa_decode_fp8_block(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
+                        const void* k_cache, const void* v_cache, const float* k_scales,
+                        const float* v_scales, int64_t scale_stride, int64_t num_blocks,
+                        const int32_t* block_tables, int64_t block_table_stride,
+                        const int32_t* context_lens, int32_t max_context_len, int32_t num_seqs,
+                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                        int32_t block_size, float scale, int32_t partition_size, void* workspace,
+                        size_t workspace_bytes, void* stream);
+int pa_chunk_attention_fp8_block(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
+                                 const void* k_cache, const void* v_cache, const float* k_scales,
+                                 const float* v_scales, int64_t scale_stride, int64_t num_blocks,
+                                 const int32_t* block_tables, int64_t block_table_stride,
+                                 const int32_t* context_lens, const int32_t* query_start,
+                                 int64_t num_query_tokens, int32_t max_query_len,
+                                 int32_t max_context_len, int32_t num_seqs, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                 float scale, int32_t partition_size, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+int pa_cross_attention_fp8_block(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
+                                 const void* k_cache, const void* v_cache, const float* k_scales,
+                                 const float* v_scales, int64_t scale_stride, int64_t num_blocks,
+                                 const int32_t* block_tables, int64_t block_table_stride,
+                                 const int32_t* context_lens, const int32_t* query_start,
+                                 int64_t num_query_tokens, int32_t max_query_len,
+                                 int32_t max_context_len, int32_t num_seqs, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                 float scale, int32_t partition_size, void* workspace,
+                                 size_t workspace_bytes, void* stream);
 
 /*
  * The partition length (tokens) a pa_decode / pa_decode_fp8 call, or a

@@ -82,6 +82,32 @@ SIGNATURES = {
                                             _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32,
                                             _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp,
                                             _sz, _vp]),
+    "pa_cross_attention": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _vp, ctypes.c_int, _i64, _vp,
+                                          _i64, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
+                                          _i32, _f32, _i32, _vp, _sz, _vp]),
+    "pa_cross_attention_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, _vp,
+                                              _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _i32,
+                                              _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp, _sz,
+                                              _vp]),
+    "pa_append_fp8_block": (ctypes.c_int, [_vp, _i64, _vp, _i64, ctypes.c_int, _vp, _vp, _vp, _vp,
+                                           _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32,
+                                           _i32, _i32, _vp]),
+    "pa_rotary_and_append_fp8_block": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                                      ctypes.c_int, _vp, _vp, _vp, _vp, _i64, _i64,
+                                                      _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32,
+                                                      _i32, _i32, _i32, _i32, _vp, _i32, _i32,
+                                                      _f32, _vp]),
+    "pa_decode_fp8_block": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, _vp,
+                                           _vp, _i64, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _i32,
+                                           _i32, _i32, _f32, _i32, _vp, _sz, _vp]),
+    "pa_chunk_attention_fp8_block": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp,
+                                                    _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp,
+                                                    _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                                    _f32, _i32, _vp, _sz, _vp]),
+    "pa_cross_attention_fp8_block": (ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp,
+                                                    _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp,
+                                                    _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                                    _f32, _i32, _vp, _sz, _vp]),
     "pa_copy_blocks": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.POINTER(_vp), _i32,
                                       ctypes.POINTER(_i64), _i64, _i64, _i64, _vp]),
     "pa_swap_blocks": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.POINTER(_vp), _i32,

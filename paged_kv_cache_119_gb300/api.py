@@ -547,8 +547,10 @@ def pa_chunk_attention_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
     return out
 
 
-def _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_size):
-    """Checks shared by the calls below; returns the device."""
+def _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_size,
+                    block_scaled=False):
+    """Checks shared by the calls below; returns the device.  block_scaled: E4M3 caches whose
+    scales (and whose types) the caller checks."""
     _cuda("q", q)
     dev = torch.cuda.current_device()
     quick = q.get_device() == dev and _dense_on(dev, (out, k_cache, v_cache, *scales, *[t for _, t in ints]))
@@ -568,6 +570,8 @@ def _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_
         _scales(*scales, num_kv_heads)
         if q.dtype not in (torch.float16, torch.bfloat16):
             raise TypeError("q must be float16 or bfloat16 for an E4M3 cache")
+    elif block_scaled:
+        pass
     elif k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
         raise TypeError("q, k_cache and v_cache must share a dtype")
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or \
@@ -809,6 +813,236 @@ def pa_decode_prefix_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tens
                    block_tables, context_lens, prefix_lens, group_start, scale, num_kv_heads,
                    block_size, max_group_size, max_prefix_len, max_suffix_len, partition_size,
                    workspace, stream)
+
+
+def _block_scales(k_scales, v_scales, k_cache, quick):
+    """Checks the scales of a block-scaled cache, float32 [N, stride >= Hkv] of dense rows;
+    returns the stride."""
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if not quick:
+            _cuda(name, t)
+        if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != k_cache.shape[0] or \
+                t.shape[1] < k_cache.shape[1]:
+            raise ValueError(f"{name} must be float32 [num_blocks, at least num_kv_heads]")
+    if k_scales.shape != v_scales.shape:
+        raise ValueError("k_scales and v_scales must have one shape")
+    return k_scales.shape[1]
+
+
+def _paged(fn, out, q, k_cache, v_cache, head_scales, block_scales, block_tables, context_lens,
+           query_start, scale, num_kv_heads, block_size, max_query_len, max_context_len,
+           partition_size, workspace, stream):
+    """Body of the cross attention and of the attention over block-scaled caches."""
+    ints = [("block_tables", block_tables), ("context_lens", context_lens)]
+    if query_start is not None:
+        ints.append(("query_start", query_start))
+    if block_scales:
+        _fp8_cache("k_cache", k_cache)
+        _fp8_cache("v_cache", v_cache)
+        if q.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError("q must be float16 or bfloat16 for an E4M3 cache")
+    dev = _attention_args(out, q, k_cache, v_cache, head_scales, ints, num_kv_heads, block_size,
+                          bool(block_scales))
+    stride = ()
+    if block_scales:
+        quick = _dense_on(q.get_device(), block_scales)
+        stride = (_block_scales(*block_scales, k_cache, quick),)
+        if not quick:
+            _one_device(q, *block_scales)
+    R, Hq, D = q.shape
+    S = context_lens.shape[0]
+    if context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [S, W] and context_lens [S]")
+    if query_start is None and S != R:
+        raise ValueError("q must hold one row per sequence")
+    if query_start is not None and query_start.shape != (S + 1,):
+        raise ValueError("query_start must be [S + 1]")
+    W = block_tables.shape[1]
+    if max_context_len is None:
+        max_context_len = W * block_size
+    if partition_size < 0 or workspace is not None:
+        need = 0
+    elif query_start is None:
+        need = _decode_need(S, Hq, D, max_context_len, block_size, partition_size)
+    else:
+        need = _chunk_need(R, Hq, D, max_context_len, partition_size)
+    workspace, ws_ptr, ws_bytes = _scratch(need, workspace, q, stream)
+    scales = block_scales or head_scales
+    args = [out.data_ptr(), _dtype(out), q.data_ptr()]
+    if scales:
+        args.append(_dtype(q))
+    args += [k_cache.data_ptr(), v_cache.data_ptr()]
+    args += [t.data_ptr() for t in scales] if scales else [_dtype(q)]
+    args += [*stride, k_cache.shape[0], block_tables.data_ptr(), W, context_lens.data_ptr()]
+    if query_start is not None:
+        args += [query_start.data_ptr(), R, int(max_query_len)]
+    args += [int(max_context_len), S, Hq, num_kv_heads, D, block_size, float(scale),
+             int(partition_size), ws_ptr, ws_bytes, _stream(stream, dev)]
+    N.check(fn, getattr(N.load(), fn)(*args))
+    return out
+
+
+def pa_cross_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                       v_cache: torch.Tensor, block_tables: torch.Tensor,
+                       context_lens: torch.Tensor, query_start: torch.Tensor, scale: float,
+                       num_kv_heads: int, block_size: int, max_query_len: int,
+                       max_context_len: int | None = None, partition_size: int = 0,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Cross attention: rows query_start[s] .. query_start[s+1]-1 of q and out [rows, Hq, D] see
+    all context_lens[s] tokens of sequence s (an encoder's states, say), however many rows
+    there are; a sequence without tokens gives rows of zeros.  max_query_len bounds the rows of
+    a sequence; a workspace of pa_chunk_workspace_bytes(...) is allocated when none is given."""
+    return _paged("pa_cross_attention", out, q, k_cache, v_cache, (), (), block_tables, context_lens,
+                  query_start, scale, num_kv_heads, block_size, max_query_len, max_context_len,
+                  partition_size, workspace, stream)
+
+
+def pa_cross_attention_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                           block_tables: torch.Tensor, context_lens: torch.Tensor,
+                           query_start: torch.Tensor, scale: float, num_kv_heads: int,
+                           block_size: int, max_query_len: int, max_context_len: int | None = None,
+                           partition_size: int = 0, workspace: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
+    """pa_cross_attention over E4M3 caches with a scale for each kv head (float32 [Hkv])."""
+    return _paged("pa_cross_attention_fp8", out, q, k_cache, v_cache, (k_scale, v_scale), (),
+                  block_tables, context_lens, query_start, scale, num_kv_heads, block_size,
+                  max_query_len, max_context_len, partition_size, workspace, stream)
+
+
+def pa_cross_attention_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                                 v_cache: torch.Tensor, k_scales: torch.Tensor,
+                                 v_scales: torch.Tensor, block_tables: torch.Tensor,
+                                 context_lens: torch.Tensor, query_start: torch.Tensor, scale: float,
+                                 num_kv_heads: int, block_size: int, max_query_len: int,
+                                 max_context_len: int | None = None, partition_size: int = 0,
+                                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_cross_attention over E4M3 caches with a scale for each block and kv head (float32
+    [num_blocks, stride >= Hkv])."""
+    return _paged("pa_cross_attention_fp8_block", out, q, k_cache, v_cache, (), (k_scales, v_scales),
+                  block_tables, context_lens, query_start, scale, num_kv_heads, block_size,
+                  max_query_len, max_context_len, partition_size, workspace, stream)
+
+
+def pa_decode_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                        block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                        num_kv_heads: int, block_size: int, max_context_len: int | None = None,
+                        partition_size: int = 0, workspace: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """pa_decode_fp8 over E4M3 caches with a scale for each block and kv head (float32
+    [num_blocks, stride >= Hkv]), as pa_append_fp8_block writes them."""
+    return _paged("pa_decode_fp8_block", out, q, k_cache, v_cache, (), (k_scales, v_scales),
+                  block_tables, context_lens, None, scale, num_kv_heads, block_size, None,
+                  max_context_len, partition_size, workspace, stream)
+
+
+def pa_chunk_attention_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                                 v_cache: torch.Tensor, k_scales: torch.Tensor,
+                                 v_scales: torch.Tensor, block_tables: torch.Tensor,
+                                 context_lens: torch.Tensor, query_start: torch.Tensor, scale: float,
+                                 num_kv_heads: int, block_size: int, max_query_len: int,
+                                 max_context_len: int | None = None, partition_size: int = 0,
+                                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """pa_chunk_attention_fp8 over E4M3 caches with a scale for each block and kv head."""
+    return _paged("pa_chunk_attention_fp8_block", out, q, k_cache, v_cache, (), (k_scales, v_scales),
+                  block_tables, context_lens, query_start, scale, num_kv_heads, block_size,
+                  max_query_len, max_context_len, partition_size, workspace, stream)
+
+
+def _append(fn, q_out, q, k, v, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+            query_start, positions, inv_freq, interleaved, magnitude, max_query_len, stream):
+    rows = [("k", k), ("v", v)] if q is None else [("q_out", q_out), ("q", q), ("k", k), ("v", v)]
+    strides = [_rows(name, t) for name, t in rows]
+    ints = [("block_tables", block_tables), ("context_lens", context_lens),
+            ("query_start", query_start)]
+    if positions is not None:
+        ints.append(("positions", positions))
+    dev = torch.cuda.current_device()
+    quick = _dense_on(dev, (k_cache, v_cache, k_scales, v_scales, *[t for _, t in ints])) and \
+        all(t.get_device() == dev for _, t in rows)
+    if not quick:
+        for name, t in ints:
+            _cuda(name, t)
+    for name, t in ints:
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+    T, Hkv, D = k.shape
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be [T, Hkv, D] of one shape and dtype")
+    Hq = Hkv
+    if q is not None:
+        Hq = q.shape[1]
+        if q_out.shape != q.shape or (q.shape[0], q.shape[2]) != (T, D):
+            raise ValueError("q and q_out must be [T, Hq, D]")
+        if not q.dtype == q_out.dtype == k.dtype:
+            raise TypeError("q, q_out, k and v must share a dtype")
+    _fp8_cache("k_cache", k_cache)
+    _fp8_cache("v_cache", v_cache)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or \
+            (k_cache.shape[1], k_cache.shape[3]) != (Hkv, D):
+        raise ValueError(f"caches must be [N, {Hkv}, B, {D}]")
+    stride = _block_scales(k_scales, v_scales, k_cache, quick)
+    S = context_lens.shape[0]
+    if context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != S or \
+            query_start.shape != (S + 1,):
+        raise ValueError("block_tables must be [S, W], context_lens [S] and query_start [S + 1]")
+    if positions is not None and positions.shape != (T,):
+        raise ValueError("positions must be [T]")
+    if not quick:
+        _one_device(k, v, k_cache, v_cache, k_scales, v_scales, *[t for _, t in rows],
+                    *[t for _, t in ints])
+    if max_query_len is None:
+        max_query_len = T
+    args = []
+    for (_, t), st in zip(rows, strides):
+        args += [t.data_ptr(), st]
+    args += [_dtype(k), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+             v_scales.data_ptr(), stride, k_cache.shape[0], block_tables.data_ptr(),
+             block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr()]
+    if q is not None:
+        args.append(0 if positions is None else positions.data_ptr())
+    args += [T, int(max_query_len), S] + ([Hq] if q is not None else []) + [Hkv, D, k_cache.shape[2]]
+    if q is not None:
+        freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        if freq.ndim != 1:
+            raise ValueError("inv_freq must be a host sequence of rotary_dim / 2 numbers")
+        args += [freq.tobytes(), 2 * freq.size, int(bool(interleaved)), float(magnitude)]
+    N.check(fn, getattr(N.load(), fn)(*args, _stream(stream, dev)))
+
+
+def pa_append_fp8_block(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                        block_tables: torch.Tensor, context_lens: torch.Tensor,
+                        query_start: torch.Tensor, max_query_len: int | None = None,
+                        stream=None) -> None:
+    """Appends new tokens to E4M3 caches with a scale for each block and kv head.
+
+    Rows query_start[s] .. query_start[s+1]-1 of k and v [T, Hkv, D] (float16 or bfloat16; the
+    token stride is free) are the last of sequence s's context_lens[s] tokens.  Each touched
+    block's scales (k_scales, v_scales float32 [num_blocks, stride >= Hkv]) become the smallest
+    powers of two that hold its tokens; where a scale grows, the block's earlier tokens are
+    restated.  max_query_len bounds the tokens of a sequence (default T; a tight bound saves
+    empty CTAs)."""
+    _append("pa_append_fp8_block", None, None, k, v, k_cache, v_cache, k_scales, v_scales,
+            block_tables, context_lens, query_start, None, None, False, 1.0, max_query_len, stream)
+
+
+def pa_rotary_and_append_fp8_block(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                                   v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                   k_scales: torch.Tensor, v_scales: torch.Tensor,
+                                   block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                   query_start: torch.Tensor, inv_freq,
+                                   positions: torch.Tensor | None = None,
+                                   interleaved: bool = False, magnitude: float = 1.0,
+                                   max_query_len: int | None = None, stream=None) -> torch.Tensor:
+    """pa_append_fp8_block with the rotary positions of q and k in the same launch: q_out =
+    rot(q), and the turned k is appended.  positions int32 [T], or None for each token's place
+    in its sequence; inv_freq, interleaved and magnitude as in pa_rotary_and_cache."""
+    _append("pa_rotary_and_append_fp8_block", q_out, q, k, v, k_cache, v_cache, k_scales, v_scales,
+            block_tables, context_lens, query_start, positions, inv_freq, interleaved, magnitude,
+            max_query_len, stream)
+    return q_out
 
 
 def pa_decode_partition_tokens(q_dtype: torch.dtype, kv_dtype: torch.dtype, num_seqs: int,

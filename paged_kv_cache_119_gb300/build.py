@@ -20,10 +20,11 @@ LIB_PATH = os.path.join(BUILD_DIR, "libpa.so")
 
 SOURCES = ["pa_api.cu", "cache_ops.cu", "decode_f32.cu", "decode_f16.cu", "decode_bf16.cu",
            "decode_fp8.cu", "decode_tc8.cu", "decode_noalloc.cu", "chunk_attn.cu", "seq_order.cu",
-           "probe.cu", "rotary.cu", "modes_core.cu", "modes_rows_f16.cu", "modes_rows_bf16.cu",
+           "probe.cu", "rotary.cu", "append.cu", "modes_core.cu", "modes_rows_f16.cu", "modes_rows_bf16.cu",
            "modes_rows_f16_fp8.cu", "modes_rows_bf16_fp8.cu", "modes_tc8.cu", "modes_chunk_f16.cu",
            "modes_chunk_bf16.cu", "modes_chunk_f16_fp8.cu", "modes_chunk_bf16_fp8.cu",
-           "modes_merge.cu", "modes_api.cu", "block_manager.cpp"]
+           "modes_block_f16.cu", "modes_block_bf16.cu", "modes_merge.cu", "modes_api.cu",
+           "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "-Xptxas", "-v", "-I", INCLUDE, "-I", CSRC]

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mod_reduce_kernel(const Deco
     }
     const int L = p.context_lens[s];
     const bool owned = row >= qs0 && row < (int64_t)qs0 + n;       // else no sequence's row: left alone
-    const bool bad = L < 0 || L > p.max_context_len || (p.query_start && (n > L || n > p.max_query_len));
+    const bool bad = L < 0 || L > p.max_context_len || (p.query_start && ((n > L && !p.mods.all_seen) || n > p.max_query_len));
     int parts = 0;
     if (owned && !bad) {
         const int R = (int)(row - qs0) * p.group + h % p.group;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mod_reduce_cut_kernel(const 
     const int qs0 = p.query_start[s], n = p.query_start[s + 1] - qs0;
     const int L = p.context_lens[s];
     const bool sane = qs0 >= 0 && n >= 0 && (int64_t)qs0 + n <= p.num_rows;
-    const bool bad = L < 0 || L > p.max_context_len || n > L || n > p.max_query_len;
+    const bool bad = L < 0 || L > p.max_context_len || (n > L && !p.mods.all_seen) || n > p.max_query_len;
     const bool here = sane && !bad && R / p.group < n;
     const int parts = here ? mod_parts(p, s, L, n, R0, tile_tokens) : 0;
     auto out_row = [&](int r) -> int64_t {

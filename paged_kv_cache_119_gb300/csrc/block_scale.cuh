@@ -1,0 +1,40 @@
+// block_scale.cuh -- E4M3 caches with a scale for each block and kv head (mode kBlock of the
+// attention kernels): value = code * scale[block][head], one array of scales for K, one for V.
+//
+// With s_t, u_t the K and V scale of token t's block and x_t its score (base 2), the output is
+//     sum_t p_t u_t c_t / sum_t p_t,   p_t = 2^(x_t - m),  x_t = (q . k codes) s_t.
+// The V scale rides on the exponent: with w_t = 2^(x_t + log2 u_t - M), M the largest exponent,
+//     O = sum w_t c_t,   l = sum w_t / u_t,   out = O / l,
+// so the kernels' online softmax runs on x_t + log2 u_t (one multiply-add where there was a
+// multiply), P . V takes w_t <= 1 and the codes as they are, and only the row sums meet 1 / u_t,
+// once a block.  Weights that P . V rounds in 16 or 8 bits are rounded relative to the largest
+// p_t u_t, that is, to what a token can add to the output.  Scales count as held within
+// 2^-48 .. 2^48: then x_t + log2 u_t - M stays above -126 for every token whose p_t is within
+// 2^-30 of the largest, and the sum l loses none of them.
+#pragma once
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+constexpr float kScaleLow = 0x1p-48f, kScaleHigh = 0x1p48f;
+
+// (K scale, log2 of the V scale, its reciprocal) of a block and head; exact for powers of two.
+__device__ __forceinline__ float4 block_scale(const float* k_scale, const float* v_scale, int64_t i)
+{
+    const float k = fminf(fmaxf(__ldg(k_scale + i), kScaleLow), kScaleHigh);
+    const float v = fminf(fmaxf(__ldg(v_scale + i), kScaleLow), kScaleHigh);
+    const int bits = __float_as_int(v);
+    const float frac = __int_as_float((bits & 0x7fffff) | 0x3f800000);      // [1, 2)
+    const float lg = frac == 1.f ? 0.f : log2f(frac);
+    return make_float4(k, (float)((bits >> 23) - 127) + lg, __frcp_rn(v), 0.f);
+}
+
+// Scales of a CTA's blocks on their way from the producer to the consumers: block i of the CTA
+// at i % kScaleRing.  The producer fills 32 entries at a time, before the copies of those
+// blocks; the entries that it overwrites are of blocks more than 32 back, whose tiles are
+// consumed while the ring of tiles holds at most 32 blocks.
+constexpr int kScaleRing = 64;
+constexpr int kScaleRingBytes = kScaleRing * 16;
+
+}  // namespace pa

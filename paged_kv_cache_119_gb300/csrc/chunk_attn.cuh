@@ -73,6 +73,7 @@
 
 #include <type_traits>
 
+#include "block_scale.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "score_mods.cuh"
@@ -117,6 +118,9 @@ struct ChunkSmem {
     static constexpr int kSlotOff = kOkOff + 4 * (NST + NRAW);   // TMEM address
     static constexpr int kBytes = kSlotOff + 16;
     static constexpr int kAlloc = kBytes + 1024;                 // 1 KB alignment slack
+    // kBlock: the scales of a tile's blocks (up to 4), of the stages, then of the raw slots
+    static constexpr int kScaleOff = (kBytes + 15) / 16 * 16;
+    static constexpr int kAllocBlock = kScaleOff + (NST + NRAW) * 64 + 1024;
     // tensor memory: O of query tile q at column 128 q, its two S/P buffers at
     // 256 + 128 q and 256 + 128 q + 64 (P: f16 pairs in the first 32 columns)
     static constexpr int kTmemCols = 512;
@@ -124,7 +128,7 @@ struct ChunkSmem {
     static_assert(D <= 128, "O must fit in 128 columns");
     static_assert(NRAW == 0 || D == 128, "E4M3 tiles need 128-byte rows");
     static_assert(kRawTile % 1024 == 0, "swizzle atoms need 1 KB alignment");
-    static_assert(kAlloc <= 227 * 1024, "shared memory");
+    static_assert(kAllocBlock <= 227 * 1024, "shared memory");
 };
 
 // Stages of the K/V ring: as many as fit next to the query tiles.
@@ -285,7 +289,8 @@ __device__ __forceinline__ void cap_row(float (&s)[kChunkTileTok], float mul, co
 // MODE: kPlain; kMod, modified scores: only the tiles that hold a token some row of the CTA
 // sees are read, and the converter warps (over every cache type) zero the V rows of tokens no
 // row sees; kPrefix, the rows of a group of sequences (query_start = the group's first one)
-// over the tokens they share, partial rows only.
+// over the tokens they share, partial rows only; kBlock, kMod over an E4M3 cache with a scale for
+// each block (four or two in a tile).
 template <typename T, int NRAW, int MODE>
 constexpr int chunk_threads()
 {
@@ -302,6 +307,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     using Sm = ChunkSmem<D, NST, NRAW>;
     constexpr bool kF8 = NRAW > 0;
     constexpr bool kIsMod = is_mod(MODE), kCap = has_cap(MODE), kSlope = has_slope(MODE);
+    constexpr bool kBlk = is_block(MODE);
+    static_assert(!kBlk || kF8, "block scales belong to E4M3 caches");
     constexpr bool kTwoTerms = MODE == kPrefix;  // P as hi + lo of V's type, else one f16 term
     constexpr bool kVConv = !kF8 && std::is_same_v<T, __nv_bfloat16> && !kTwoTerms;   // bf16 V -> f16 in place
     constexpr bool kVHand = kVConv || (!kF8 && kIsMod);           // V handed over (vconv)
@@ -330,6 +337,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     uint64_t* vconv = raw_empty + NRAW;          // [stage] (bf16 caches: V tile is f16)
     int* stage_ok = reinterpret_cast<int*>(smem + Sm::kOkOff);
     int* raw_ok = stage_ok + NST;
+    float4* stage_scale = reinterpret_cast<float4*>(smem + Sm::kScaleOff);   // [stage][4] (kBlock)
+    float4* raw_scale = stage_scale + NST * 4;                               // [raw slot][4]
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + Sm::kSlotOff);
 
     const int warp = threadIdx.x >> 5;
@@ -362,7 +371,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     const int tseq = MODE == kPrefix ? (rows_sane && n > 0 ? qs0 : 0) : seq;
     const int L = MODE == kPrefix ? p.prefix_lens[tseq] : p.context_lens[seq];
     if (!rows_sane || L < 0 || L > p.max_context_len || n > p.max_query_len ||
-        (MODE == kPrefix ? L % BS != 0 : n > L)) {
+        (MODE == kPrefix ? L % BS != 0 : n > L && !(takes_cross(MODE) && p.mods.all_seen))) {
         if (part == 0 && unit_y == 0 && threadIdx.x == 0)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
         if (!split && rows_sane && part == 0 && mt == 0) {
@@ -398,8 +407,20 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         order = seen_tiles(seen, NT);
         t_end = seen.end;
         c0 = split ? part * (p.partition_tokens / NT) : 0;
-        if (c0 >= order.count)
+        if (c0 >= order.count) {
+            // an empty context (cross attention only: a chunk's rows see themselves) gives zeros
+            if (takes_cross(MODE) && order.count == 0 && !split)
+                for (int i = threadIdx.x; i < ntok * G * D; i += blockDim.x) {
+                    const int tok = i / (G * D);
+                    const int64_t idx = ((int64_t)(qs0 + j0 + tok) * p.num_q_heads + (int64_t)kvh * G) * D +
+                                        (i - tok * G * D);
+                    if (p.out_f32)
+                        store_as(static_cast<float*>(p.out) + idx, 0.f);
+                    else
+                        store_as(static_cast<T*>(p.out) + idx, 0.f);
+                }
             return;
+        }
         ntiles = split ? min(order.count - c0, p.partition_tokens / NT) : order.count;
     }
     int t1 = t_end;
@@ -474,18 +495,47 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         uint64_t* pempty = kF8 ? raw_empty : empty;
         int* pok = kF8 ? raw_ok : stage_ok;
         int issued = 0;
+        // kBlock: this lane's table entry of a tile (-2: none to read), two tiles ahead, and the
+        // scales of its block, one tile ahead
+        auto entry = [&](int it) -> int {
+            if (it >= ntiles || lane >= BPT)
+                return -2;
+            const int b = tile_token(it) / BS + lane;
+            return b < blk_end && any_seen(seen, b * BS, min(b * BS + BS, t1)) ? max(__ldg(bt_row + b), -1) : -2;
+        };
+        auto scale_of = [&](int e) -> float4 {
+            return e >= 0 && (int64_t)e < p.num_blocks
+                       ? block_scale(p.k_scale, p.v_scale, (int64_t)e * p.scale_stride + kvh)
+                       : make_float4(1.f, 0.f, 1.f, 0.f);
+        };
+        int cur = -2, next = -2;
+        float4 sc{}, next_sc{};
+        if constexpr (kBlk) {
+            cur = entry(0);
+            next = entry(1);
+            next_sc = scale_of(cur);
+        }
         for (int it = 0; it < ntiles; ++it) {
             const int st = it % NP;
             const int b0 = tile_token(it) / BS;
             int nb = min(BPT, blk_end - b0);
             bool want = lane < nb;
-            if constexpr (kIsMod) {        // only blocks that hold a seen token
+            int pbn = -1;
+            bool valid = false;
+            if constexpr (kBlk) {
+                want = cur != -2;
+                pbn = cur;
+                valid = pbn >= 0 && (int64_t)pbn < p.num_blocks;
+                nb = __popc(__ballot_sync(kFullMask, want));
+                cur = next;
+                next = entry(it + 2);
+                sc = next_sc;
+                next_sc = scale_of(cur);
+            } else if constexpr (kIsMod) {        // only blocks that hold a seen token
                 want = want && any_seen(seen, (b0 + lane) * BS, min((b0 + lane) * BS + BS, t1));
                 nb = __popc(__ballot_sync(kFullMask, want));
             }
-            int pbn = -1;
-            bool valid = false;
-            if (want) {
+            if (!kBlk && want) {
                 pbn = __ldg(bt_row + b0 + lane);
                 valid = pbn >= 0 && (int64_t)pbn < p.num_blocks;
             }
@@ -495,7 +545,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 if (it >= NP && !mbar_wait(&pempty[st], ((it / NP) - 1) & 1)) {
                     atomicOr(p.err, PA_DEVERR_TIMEOUT);
                     ok = 0;
-                } else {
+                } else if (!kBlk) {
                     const int nvalid = __popc(vmask);
                     pok[st] = nvalid == nb ? 1 : 0;
                     if (nvalid != nb)
@@ -507,6 +557,20 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
             }
             if (!__shfl_sync(kFullMask, ok, 0))
                 break;
+            if constexpr (kBlk) {
+                // the slot is free: its scales, then the announcement that carries them
+                if (lane < BPT)
+                    raw_scale[st * 4 + lane] = sc;
+                __syncwarp();
+                if (lane == 0) {
+                    const int nvalid = __popc(vmask);
+                    pok[st] = nvalid == nb ? 1 : 0;
+                    if (nvalid != nb)
+                        atomicOr(p.err, PA_DEVERR_BLOCK_ID);
+                    mbar_arrive_expect_tx(&pfull[st], (uint32_t)nvalid * 2u * BS * 128u);
+                }
+                __syncwarp();
+            }
             if (kF8 && valid) {
                 unsigned char* kdst = smem + Sm::kRawOff + st * Sm::kRawStage + lane * (BS * 128);
                 const int z = pbn * p.num_kv_heads + kvh;     // < 2^31 (checked on the host)
@@ -574,6 +638,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     }
                 }
                 fence_proxy_async_smem();                    // f16 tiles -> tensor core
+                if (kBlk && warp == 3 + kChunkSoftmaxWarps && lane < BPT)
+                    stage_scale[st * 4 + lane] = raw_scale[r * 4 + lane];
                 __syncwarp();
                 if (lane == 0) {
                     if (warp == 3 + kChunkSoftmaxWarps)
@@ -741,8 +807,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         const int64_t qrow = (int64_t)(qs0 + j0 + tok) * p.num_q_heads + (int64_t)kvh * G + g;
         // scores are used as s * sl2 with sl2 > 0: a negative scale flips the sign of q
         // (exact), a zero scale makes q zero (every score 0); over E4M3 caches the K scale
-        // of the kv head joins the softmax scale
-        const float sl2_raw = kF8 ? p.scale_log2 * p.k_scale[kvh] : p.scale_log2;
+        // of the kv head joins the softmax scale (kBlock: the one of a block, tile by tile)
+        const float sl2_raw = kF8 && !kBlk ? p.scale_log2 * p.k_scale[kvh] : p.scale_log2;
         const uint32_t qflip = sl2_raw < 0.f ? 0x80008000u : 0u;
         const bool qzero = sl2_raw == 0.f;
         float sl2 = qzero ? 1.f : fabsf(sl2_raw);
@@ -906,7 +972,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                             for (int c = 0; c < NT; ++c)
                                 s[c] = (vis >> c) & 1ull ? s[c] : -INFINITY;
                         }
-                        smax = row_max(s);
+                        if constexpr (!kBlk)
+                            smax = row_max(s);
                     }
                 } else {
                     if (lim < NT - 1) {
@@ -916,7 +983,28 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     }
                     smax = row_max(s);
                 }
-                float tmax = smax == -INFINITY ? -INFINITY : smax * mul;
+                float tmax;
+                if constexpr (kBlk) {
+                    tmax = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < BPT; ++k) {
+                        float mx[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mx[i] = max3f(s[k * BS + i], s[k * BS + 4 + i], s[k * BS + 8 + i]);
+#pragma unroll
+                        for (int c = 12; c + 8 <= BS; c += 8)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mx[i] = max3f(mx[i], s[k * BS + c + i], s[k * BS + c + 4 + i]);
+                        const float top = max3f(s[k * BS + BS - 4], s[k * BS + BS - 3],
+                                                fmaxf(s[k * BS + BS - 2], s[k * BS + BS - 1]));
+                        const float4 sc = stage_scale[st * 4 + k];
+                        tmax = fmaxf(tmax, fmaf(max3f(max3f(mx[0], mx[1], mx[2]), mx[3], top), sl2 * sc.x, sc.y));
+                    }
+                } else {
+                    tmax = smax == -INFINITY ? -INFINITY : smax * mul;
+                }
                 if (kCap && poly) {
                     const float y = kF8 ? smax * kk : smax;
                     tmax = y * poly_at(y * y);
@@ -954,6 +1042,24 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 const float nm = (m_ref == -INFINITY ? 0.f : -m_ref) + kChunkPExp;
                 float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                  make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                if constexpr (kBlk) {
+                    // w = 2^7 2^(s sl2 s_k + log2 u_k - m_ref), the sum of w / u_k (block_scale.cuh)
+#pragma unroll
+                    for (int k = 0; k < BPT; ++k) {
+                        const float4 sc = stage_scale[st * 4 + k];
+                        const float2 f = make_float2(sl2 * sc.x, sl2 * sc.x), add = make_float2(nm + sc.y, nm + sc.y);
+                        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                        for (int c = k * BS; c < (k + 1) * BS; c += 2) {
+                            const float2 x = ffma2(make_float2(s[c], s[c + 1]), f, add);
+                            s[c] = ex2_approx(x.x);
+                            s[c + 1] = ex2_approx(x.y);
+                            part[(c >> 1) & 1] = ffma2(make_float2(s[c], s[c + 1]), make_float2(1.f, 1.f),
+                                                       part[(c >> 1) & 1]);
+                        }
+                        lsum = fmaf((part[0].x + part[0].y) + (part[1].x + part[1].y), sc.z, lsum);
+                    }
+                }
                 // (one loop for either form of the scores: a test in one loop for both cost 13 %
                 // where the cap bites)
                 auto weights = [&](auto capped) {
@@ -980,10 +1086,11 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                         weights(std::true_type{});
                     else
                         weights(std::false_type{});
-                } else {
+                } else if constexpr (!kBlk) {
                     weights(std::false_type{});
                 }
-                lsum += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) +
+                if constexpr (!kBlk)
+                    lsum += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) +
                         ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y));
             }
             if (kTwoTerms && warp_live) {
@@ -1044,7 +1151,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         tc_fence_after();
         if (warp_live) {
             // over E4M3 caches the V scale of the kv head multiplies the output
-            const float inv = lsum > 0.f ? (kF8 ? p.v_scale[kvh] : 1.f) / lsum : 0.f;
+            const float inv = lsum > 0.f ? (kF8 && !kBlk ? p.v_scale[kvh] : 1.f) / lsum : 0.f;
             const int which = (split || p.out_f32) ? 0 : (DType<T>::id == PA_F16 ? 1 : 2);
             // over a bf16 cache, O that is not finite while the probabilities and their
             // sum are means the row weighed a V element without an f16 value (O itself

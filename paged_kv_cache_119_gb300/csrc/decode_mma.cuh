@@ -32,6 +32,7 @@
 
 #include <type_traits>
 
+#include "block_scale.cuh"
 #include "decode_kernel.cuh"
 
 namespace pa {
@@ -187,6 +188,9 @@ struct MmaSmem {
     static constexpr int kFlagOffset = kOkOffset + NSTAGE * 4;
     static constexpr int kBytes = kFlagOffset + 16;
     static constexpr int kAlloc = kBytes + 1024;                 // room to align the ring to 1 KB
+    // kBlock: the scales of the CTA's blocks behind all that
+    static constexpr int kScaleOffset = (kBytes + 15) / 16 * 16;
+    static constexpr int kAllocBlock = kScaleOffset + kScaleRingBytes + 1024;
     // merge area at offset 0 (the ring, or the staging tiles), reused once every tile
     // is consumed
     static constexpr int kMergeAcc = kDecodeConsumerWarps * 8 * D * 4;
@@ -213,7 +217,8 @@ constexpr int mma_min_blocks() { return (sizeof(TK) == 1 && BS == 32) ? 3 : 4; }
 // MODE (with CH): kMod, chunk rows with modified scores (query_start null: one row per query
 // head of each sequence's last token), kModBoth when they have a cap or slopes; kPrefix, the rows of a group of sequences over the
 // tokens they share (blockIdx.z = group); kSuffix, each sequence's query heads over its
-// tokens after the shared prefix.  kPrefix and kSuffix write partial rows only.
+// tokens after the shared prefix.  kPrefix and kSuffix write partial rows only.  kBlock: kMod
+// over an E4M3 cache with a scale for each block.
 template <typename T, typename TK, int D, int BS, int NH, int NSTAGE, bool CH = false, int BPT = 1,
           int MODE = kPlain>
 __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>())
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     constexpr int TB = BS * BPT;      // tokens per tile
     using Sm = MmaSmem<TK, D, TB, NSTAGE>;
     constexpr bool kFp8 = Sm::kFp8;
-    constexpr bool kIsMod = is_mod(MODE);
+    constexpr bool kIsMod = is_mod(MODE), kBlk = is_block(MODE);
     // tensor-core operand type: the query type for 16-bit caches; f16 for E4M3 caches
     // (an E4M3 code converts to f16 exactly in one instruction per pair)
     using TM = std::conditional_t<kFp8, __half, T>;
@@ -235,6 +240,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     static_assert(NH == 1 || NH == 2 || NH == 4 || NH == 8, "1, 2, 4 or 8 query heads per CTA");
     static_assert(NSTAGE % NCW == 0, "each ring stage must belong to one consumer warp");
     static_assert(BS % 16 == 0 && D % 64 == 0, "block_size 16/32, head_dim 64/128");
+    static_assert(!kBlk || (kFp8 && NSTAGE * BPT <= 32), "the ring of scales outlasts the ring of tiles");
 
     if (overlap_passes<MODE>(p.num_seqs))
         return;
@@ -245,6 +251,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
     uint64_t* empty = full + NSTAGE;
     int* stage_ok = reinterpret_cast<int*>(smem + Sm::kOkOffset);
     int* poison = reinterpret_cast<int*>(smem + Sm::kFlagOffset);
+    float4* scales = reinterpret_cast<float4*>(smem + Sm::kScaleOffset);    // kBlock
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -285,6 +292,8 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
         }
         if (kIsMod && !p.query_start)
             bad_len = L < 0 || L > p.max_context_len;      // an empty context is a zero row
+        if (takes_cross(MODE) && p.query_start && p.mods.all_seen)
+            bad_len = L < 0 || L > p.max_context_len || n > p.max_query_len;
     }
     if (bad_len || !rows_sane) {
         if (part == 0 && blockIdx.y == 0 && threadIdx.x == 0)
@@ -393,12 +402,31 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             next = entry(lane);
         else
             next = (lane < nblk) ? __ldg(bt_row + lane) : 0;
+        // kBlock: the scales of this lane's block of the batch (entries are then fetched two
+        // batches ahead, their scales one)
+        auto scale_of = [&](int e) -> float4 {
+            return e >= 0 && (int64_t)e < p.num_blocks
+                       ? block_scale(p.k_scale, p.v_scale, (int64_t)e * p.scale_stride + kvh)
+                       : make_float4(1.f, 0.f, 1.f, 0.f);
+        };
+        int after = 0;
+        float4 sc{};
+        if constexpr (kBlk) {
+            after = entry(32 + lane);
+            sc = scale_of(next);
+        }
         bool aborted = false;
         // block-table entries 32 at a time (BPT divides 32, so no tile straddles two
         // batches), the next 32 in flight while the current ones are used
         for (int base = 0; base < nblk && !aborted; base += 32) {
             const int cur = next;
-            if constexpr (kIsMod) {
+            if constexpr (kBlk) {
+                scales[(base + lane) & (kScaleRing - 1)] = sc;
+                __syncwarp();
+                next = after;
+                sc = scale_of(next);
+                after = entry(base + 64 + lane);
+            } else if constexpr (kIsMod) {
                 next = entry(base + 32 + lane);
             } else if (base + 32 + lane < nblk) {
                 next = __ldg(bt_row + base + 32 + lane);
@@ -574,7 +602,8 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             o[i][j] = 0.f;
     bool poisoned = false;
     // scores carry the softmax scale (base 2) and, for a quantised cache, the K scale
-    const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[kvh] * q_unscale : p.scale_log2;
+    // (kBlock: the K scale of each block comes with its tile)
+    const float sl2 = kBlk ? p.scale_log2 : kFp8 ? p.scale_log2 * p.k_scale[kvh] * q_unscale : p.scale_log2;
     const float row_sl2[2] = {sl2 * row_unscale[0], sl2 * row_unscale[1]};
     auto sl2_of = [&](int j) -> float { return kRowScale ? row_sl2[j & 1] : sl2; };   // of s[j]
     // chunk rows: the last visible position of rows 2c and 2c+1 (-1: padding row)
@@ -680,6 +709,9 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             // ---- online softmax: s[0], s[1] = token 16mb+g; s[2], s[3] = token 16mb+g+8
             const int tok_a = 16 * mb + g, tok_b = tok_a + 8;
             float x[4];
+            float4 sc{};                       // kBlock: the scales of these 16 tokens' block
+            if constexpr (kBlk)
+                sc = scales[(it * BPT + 16 * mb / BS) & (kScaleRing - 1)];
             if constexpr (kIsMod) {
                 // all rows see all 16 tokens, but at a window's ends and the last tokens
                 const int b0 = tb + 16 * mb;
@@ -703,7 +735,10 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[j] = near_cap ? s[j] : s[j] * sl2_of(j);
+                    if constexpr (kBlk)
+                        x[j] = fmaf(s[j], sl2_of(j) * sc.x, sc.y);
+                    else
+                        x[j] = near_cap ? s[j] : s[j] * sl2_of(j);
                     if (has_cap(MODE) && p.mods.cap > 0.f && !near_cap)
                         x[j] = cap_score(x[j], p.mods);
                 }
@@ -748,7 +783,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                 const float pb = (mnew == -INFINITY) ? 0.f : ex2_approx(x[j + 2] - mnew);
                 x[j] = pa;
                 x[j + 2] = pb;
-                lsum[j] = fmaf(lsum[j], alpha[j], pa + pb);
+                lsum[j] = fmaf(lsum[j], alpha[j], kBlk ? (pa + pb) * sc.z : pa + pb);
             }
             // once the running maxima settle (most tiles of a long context) no row of the
             // warp rescales, and the 4 x KS multiplies by 1 are skipped
@@ -898,7 +933,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             den = fmaf(cw[w], ml.y, den);
         }
         // no visible token gives 0; a poisoned CTA, or NaN scores, NaN
-        const float vs = kFp8 ? p.v_scale[kvh] : 1.f;
+        const float vs = kFp8 && !kBlk ? p.v_scale[kvh] : 1.f;
         const float mul = bad || den != den ? __int_as_float(0x7fc00000) : den > 0.f ? vs / den : 0.f;
         const int64_t row = (int64_t)(qs0 + j) * p.num_q_heads + kvh * p.group + (R0 + h - j * p.group);
         const int64_t prow = row * p.max_parts + (MODE == kSuffix ? p.part_base : 0) + part;

@@ -53,6 +53,9 @@ struct RowsSmem {
     static constexpr int kFlagOffset = kOkOffset + NSTAGE * 4;
     static constexpr int kBytes = kFlagOffset + 16;
     static constexpr int kAlloc = kBytes + 1024;                         // room to align to 1 KB
+    // kBlock: the scales of the CTA's blocks behind all that
+    static constexpr int kScaleOffset = (kBytes + 15) / 16 * 16;
+    static constexpr int kAllocBlock = kScaleOffset + kScaleRingBytes + 1024;
     static_assert(!kFp8 || D == 128, "E4M3 tiles are read in place: 128-byte rows");
     static_assert(kHalfBytes % 1024 == 0, "swizzle atoms need 1 KB alignment");
 };
@@ -74,7 +77,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     constexpr int NR = kRowsGroup * RW;
     constexpr int KS = D / 16;        // k-steps of the score product
     constexpr int NB = D / 8;         // 8-dim column blocks of O
-    constexpr bool kIsMod = is_mod(MODE);
+    constexpr bool kIsMod = is_mod(MODE), kBlk = is_block(MODE);
+    static_assert(!kBlk || (kFp8 && NSTAGE * BPT <= 32), "the ring of scales outlasts the ring of tiles");
     static_assert(kIsMod || MODE == kPrefix || MODE == kSuffix, "the plain mode has its own kernels");
     static_assert(NCW % RW == 0 && NSTAGE % NCW == 0, "each ring stage belongs to one warp of a row group");
     static_assert((BS == 16 || BS == 32) && D % 64 == 0, "block_size 16/32, head_dim 64/128");
@@ -88,6 +92,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     uint64_t* empty = full + NSTAGE;
     int* stage_ok = reinterpret_cast<int*>(smem + Sm::kOkOffset);
     int* poison = reinterpret_cast<int*>(smem + Sm::kFlagOffset);
+    float4* scales = reinterpret_cast<float4*>(smem + Sm::kScaleOffset);    // kBlock
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -119,7 +124,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             bad_len = bad_len || start < 0 || start > p.max_prefix_len || start % BS != 0 || start > L ||
                       L - start > p.max_suffix_len;
         } else if (p.query_start) {
-            bad_len = bad_len || n > L || n > p.max_query_len;
+            bad_len = bad_len || (n > L && !(takes_cross(MODE) && p.mods.all_seen)) || n > p.max_query_len;
         }
     }
     // the q / out row of row R of the kv head (R / group < n)
@@ -207,12 +212,32 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                     return kUnseen;
             return max(__ldg(bt_row + b), -1);
         };
-        // entries 32 at a time (BPT divides 32), the next 32 in flight
+        // entries 32 at a time (BPT divides 32), the next 32 in flight; kBlock: entries two
+        // batches ahead, their scales one
         int next = entry(lane);
+        auto scale_of = [&](int e) -> float4 {
+            return e >= 0 && (int64_t)e < p.num_blocks
+                       ? block_scale(p.k_scale, p.v_scale, (int64_t)e * p.scale_stride + kvh)
+                       : make_float4(1.f, 0.f, 1.f, 0.f);
+        };
+        int after = 0;
+        float4 sc{};
+        if constexpr (kBlk) {
+            after = entry(32 + lane);
+            sc = scale_of(next);
+        }
         bool aborted = false;
         for (int base = 0; base < nblk && !aborted; base += 32) {
             const int cur = next;
-            next = entry(base + 32 + lane);
+            if constexpr (kBlk) {
+                scales[(base + lane) & (kScaleRing - 1)] = sc;
+                __syncwarp();
+                next = after;
+                sc = scale_of(next);
+                after = entry(base + 64 + lane);
+            } else {
+                next = entry(base + 32 + lane);
+            }
             const int cnt = min(32, nblk - base);
             for (int i = 0; i < cnt; i += BPT) {
                 int pbn[BPT];
@@ -342,7 +367,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         for (int j = 0; j < 4; ++j)
             o[i][j] = 0.f;
     bool poisoned = false;
-    const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[kvh] : p.scale_log2;
+    // (kBlock: the K scale of each block comes with its tile)
+    const float sl2 = kFp8 && !kBlk ? p.scale_log2 * p.k_scale[kvh] : p.scale_log2;
     const float row_sl2[2] = {sl2 * row_unscale[0], sl2 * row_unscale[1]};
 
     for (int it = warp / RW; it < ntiles; it += TW) {
@@ -399,11 +425,26 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                 }
         }
         // ---- online softmax: s[h][2j + e] = row g + 8j, token 8h + 2c + e of the tile
+        float inv_v[2] = {1.f, 1.f};              // kBlock: 1 / V scale of each 16 tokens' block
+        if constexpr (kBlk) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+            for (int mb = 0; mb < 2; ++mb) {
+                const float4 sc = scales[(it * BPT + 16 * mb / BS) & (kScaleRing - 1)];
+                inv_v[mb] = sc.z;
+                const float mul[2] = {row_sl2[0] * sc.x, row_sl2[1] * sc.x};
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                s[h][k] *= row_sl2[k >> 1];
+                for (int h = 2 * mb; h < 2 * mb + 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        s[h][k] = fmaf(s[h][k], mul[k >> 1], sc.y);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[h][k] *= row_sl2[k >> 1];
+        }
         bool ragged = nvalid < TB;                // some tokens are outside, or seen by no row
         bool mask = ragged;                       // some row does not see some token
         if constexpr (kIsMod) {
@@ -492,7 +533,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             for (int h = 0; h < 4; ++h) {
                 s[h][2 * j] = ex2_approx(s[h][2 * j] - ref);
                 s[h][2 * j + 1] = ex2_approx(s[h][2 * j + 1] - ref);
-                sum += s[h][2 * j] + s[h][2 * j + 1];
+                if constexpr (kBlk)
+                    sum = fmaf(s[h][2 * j] + s[h][2 * j + 1], inv_v[h >> 1], sum);
+                else
+                    sum += s[h][2 * j] + s[h][2 * j + 1];
             }
             lsum[j] += sum;
         }
@@ -615,7 +659,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         den = fmaf(cw[w], ml.y, den);
     }
     // no visible token gives 0; a poisoned CTA, or NaN scores, NaN
-    const float vs = kFp8 ? p.v_scale[kvh] : 1.f;
+    const float vs = kFp8 && !kBlk ? p.v_scale[kvh] : 1.f;
     const float mul = bad || den != den ? __int_as_float(0x7fc00000) : den > 0.f ? vs / den : 0.f;
     const int64_t row = out_row(R0 + h);
     const int64_t prow = row * p.max_parts + (MODE == kSuffix ? p.part_base : 0) + part;

@@ -46,6 +46,7 @@
 
 #include <cuda.h>
 
+#include "block_scale.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "score_mods.cuh"
@@ -181,7 +182,7 @@ __device__ __forceinline__ int sw128_byte(int row, int col)
 // (decode: R query heads of one kv head; CH: R (chunk token, head) rows of one kv head,
 // row R0 + r = token (R0 + r) / group, head (R0 + r) % group).
 // grid = (partitions, num_kv_heads * chunks, num_seqs); kTc8Threads threads.
-// MODE (with CH): as in decode_mma_kernel.
+// MODE (with CH): as in decode_mma_kernel (cap and slopes in kMod itself).
 template <typename T, int BS, int R, int NST, bool CH, int MODE = kPlain>
 __global__ void __launch_bounds__(kTc8Threads, 3)
     decode_tc8_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tk,
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
     constexpr int D = 128;
     constexpr int N = Sm::N;
     constexpr int BPT = kTc8Tok / BS;           // cache blocks per tile
+    constexpr bool kIsMod = is_mod(MODE), kBlk = is_block(MODE);
     static_assert(BS == 16 || BS == 32, "block_size 16 or 32");
 
     if (overlap_passes<MODE>(p.num_seqs))
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
 
     int qs0 = 0, n = 1;
     if constexpr (CH) {
-        if (MODE == kSuffix || (MODE == kMod && !p.query_start)) {
+        if (MODE == kSuffix || (kIsMod && !p.query_start)) {
             qs0 = seq;
         } else {
             qs0 = p.query_start[seq];
@@ -258,8 +260,10 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                       L > p.max_context_len ||
                       L - start > p.max_suffix_len;
         }
-        if (MODE == kMod && !p.query_start)
+        if (kIsMod && !p.query_start)
             bad_len = L < 0 || L > p.max_context_len;      // an empty context is a zero row
+        if (takes_cross(MODE) && p.query_start && p.mods.all_seen)
+            bad_len = L < 0 || L > p.max_context_len || n > p.max_query_len;
     }
     if (bad_len || !rows_sane) {
         if (part == 0 && blockIdx.y == 0 && threadIdx.x == 0)
@@ -285,7 +289,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         const int last = L - n + min(n - 1, (R0 + R - 1) / p.group);   // last row's position
         if constexpr (MODE == kPlain)
             t_end = last + 1;
-        if constexpr (MODE == kMod) {
+        if constexpr (kIsMod) {
             seen = seen_by(p.mods, seq, L, L - n + R0 / p.group, last);
             order = seen_tiles(seen, kTc8Tok);
             t_end = seen.end;
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
     }
     int t0 = start, t1 = t_end;
     int c0 = 0, ntiles = 0;                       // kMod: first tile of the list to read
-    if constexpr (MODE == kMod) {
+    if constexpr (kIsMod) {
         c0 = split ? part * (p.partition_tokens / kTc8Tok) : 0;
         if (split && c0 >= order.count)
             return;
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
     }
     // first token of tile it
     auto tile_token = [&](int it) -> int {
-        if constexpr (MODE == kMod)
+        if constexpr (kIsMod)
             return order(c0 + it) * kTc8Tok;
         else
             return t0 + it * kTc8Tok;
@@ -357,7 +361,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         const int32_t* bt_row = p.block_tables + (int64_t)tseq * p.bt_stride;
         const uint64_t policy = l2_evict_first_policy();
         const int blk_first = t0 / BS;             // partitions start on block boundaries
-        const int nblk = MODE == kMod ? ntiles * BPT : (t1 + BS - 1) / BS - blk_first;
+        const int nblk = kIsMod ? ntiles * BPT : (t1 + BS - 1) / BS - blk_first;
         // kMod: the table entry of the CTA's i-th block (negative ids are one -1), or kUnseen:
         // only blocks that hold a seen token are read (and checked)
         constexpr int kUnseen = -2;
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         // block-table entries 32 at a time (4 or 8 tiles), the next 32 in flight while the
         // current ones are used
         int cur, nxt;
-        if constexpr (MODE == kMod) {
+        if constexpr (kIsMod) {
             cur = entry(lane);
             nxt = entry(32 + lane);
         } else {
@@ -382,7 +386,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
             const int lb = it * BPT;               // first block of the tile, CTA-relative
             if (it > 0 && (lb & 31) == 0) {
                 cur = nxt;
-                if constexpr (MODE == kMod)
+                if constexpr (kIsMod)
                     nxt = entry(lb + 32 + lane);
                 else
                     nxt = lb + 32 + lane < nblk ? __ldg(bt_row + blk_first + lb + 32 + lane) : -1;
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
             int pbn = -1;
             bool valid = false;
             bool want = lane < nb;
-            if constexpr (MODE == kMod) {
+            if constexpr (kIsMod) {
                 want = lane < BPT && e != kUnseen;
                 nb = __popc(__ballot_sync(kFullMask, want));
             }
@@ -523,9 +527,9 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                 lim[r] = orow[r] >= 0 ? L - n + (R0 + r) / p.group : -1;
             else
                 lim[r] = L - 1;
-            if constexpr (MODE == kMod) {
+            if constexpr (kIsMod) {
                 low[r] = p.mods.window > 0 ? max(0, lim[r] - p.mods.window + 1) : 0;
-                if (p.mods.slopes && orow[r] >= 0)
+                if (!kBlk && p.mods.slopes && orow[r] >= 0)
                     slope[r] = base2_slope(p.mods.slopes[orow[r] % p.num_q_heads]);
             }
         }
@@ -545,7 +549,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                     red_l[sw * R + r] = am[r];
             }
             named_barrier(2, 128);
-            const float ks = p.k_scale[kvh] * p.scale_log2;
+            const float ks = kBlk ? p.scale_log2 : p.k_scale[kvh] * p.scale_log2;
             float sg[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -609,10 +613,33 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                 acc[r] = fmaf(acc[r], al[r],
                               combine_terms(ov[4 * r], ov[4 * r + 1], ov[4 * r + 2], ov[4 * r + 3]));
         };
+        // kBlock: the scales of this token's block, one tile ahead, its table entry two tiles
+        // ahead (a producer's table entries are not ordered before these warps' reads)
+        const int32_t* bt_row = p.block_tables + (int64_t)tseq * p.bt_stride;
+        auto block_of = [&](int it) -> int {
+            const int t = tile_token(it) + tl;
+            return it < ntiles && t < t1 ? __ldg(bt_row + t / BS) : -1;
+        };
+        auto scale_of = [&](int e) -> float4 {
+            return e >= 0 && (int64_t)e < p.num_blocks
+                       ? block_scale(p.k_scale, p.v_scale, (int64_t)e * p.scale_stride + kvh)
+                       : make_float4(1.f, 0.f, 1.f, 0.f);
+        };
+        int next_block = -1;
+        float4 sc{}, next_sc{};
+        if constexpr (kBlk) {
+            next_sc = scale_of(block_of(0));
+            next_block = block_of(1);
+        }
         for (int it = 0; it < ntiles; ++it) {
             const int b = it & 1;
             const int st = it % NST;
             const int tb = tile_token(it);
+            if constexpr (kBlk) {
+                sc = next_sc;
+                next_sc = scale_of(next_block);
+                next_block = block_of(it + 2);
+            }
             // the scores imply the tile's K (the K slot may already hold a later tile:
             // neither kfull nor any per-stage word is read here)
             if (!mbar_wait(&s_full[b], (it >> 1) & 1)) {
@@ -629,11 +656,15 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const float s = combine_terms(sv[4 * r], sv[4 * r + 1], sv[4 * r + 2], sv[4 * r + 3]);
-                if constexpr (MODE == kMod) {
-                    x[r] = s * mult[r];
-                    if (p.mods.cap > 0.f)
-                        x[r] = cap_score(x[r], p.mods);
-                    x[r] = fmaf(-slope[r], (float)abs(lim[r] - pos), x[r]);
+                if constexpr (kIsMod) {
+                    if constexpr (kBlk) {
+                        x[r] = fmaf(s, mult[r] * sc.x, sc.y);
+                    } else {
+                        x[r] = s * mult[r];
+                        if (p.mods.cap > 0.f)
+                            x[r] = cap_score(x[r], p.mods);
+                        x[r] = fmaf(-slope[r], (float)abs(lim[r] - pos), x[r]);
+                    }
                     const bool sees = orow[r] >= 0 && (pos < seen.glob || (pos >= low[r] && pos <= lim[r]));
                     x[r] = sees ? x[r] : -INFINITY;
                 } else {
@@ -666,7 +697,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                 m[r] = mnew;
                 // p in [0, 1]; 0 while the row has seen no visible token, NaN for a NaN score
                 x[r] = (mnew == -INFINITY && x[r] == -INFINITY) ? 0.f : ex2_approx(x[r] - mnew);
-                lsum[r] = fmaf(lsum[r], al[r], x[r]);
+                lsum[r] = fmaf(lsum[r], al[r], kBlk ? x[r] * sc.z : x[r]);
             }
 #pragma unroll
             for (int r = 0; r < R; r += 2) {
@@ -687,7 +718,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                     const int n = kTc8Terms * r + k;
                     pbuf[n * 128 + (tl ^ ((n & 7) << 4))] = (unsigned char)pt[r][k];
                 }
-            if (MODE == kMod ? (tb + kTc8Tok > t1 || (tb < seen.lo && tb + kTc8Tok > seen.glob))
+            if (kIsMod ? (tb + kTc8Tok > t1 || (tb < seen.lo && tb + kTc8Tok > seen.glob))
                              : tb + kTc8Tok > t1) {
                 // last tile: V rows of tokens past the range (unused slot, missing block,
                 // stale tile) become 0, once the tile's V is in (its slot is not reused
@@ -698,7 +729,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
                     poisoned = aborted = true;
                     break;
                 }
-                if constexpr (MODE == kMod) {            // rows of unseen tokens, anywhere
+                if constexpr (kIsMod) {            // rows of unseen tokens, anywhere
                     uint4* vt = reinterpret_cast<uint4*>(smem + st * Sm::kStage + Sm::kTile);
                     for (int j = tl; j < kTc8Tok * 8; j += kTc8Tok)
                         if (!is_seen(seen, tb + j / 8))
@@ -745,7 +776,7 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
         if (poisoned)
             *poison = 1;
         named_barrier(2, 128);
-        const float vs = p.v_scale[kvh] * (1.f / 256.f);   // P carried 256 p
+        const float vs = (kBlk ? 1.f : p.v_scale[kvh]) * (1.f / 256.f);   // P carried 256 p
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float l = (red_l[r] + red_l[R + r]) + (red_l[2 * R + r] + red_l[3 * R + r]);

@@ -1,5 +1,5 @@
-// modes_api.cu -- entry points of the attention with modified scores and of the
-// shared-prefix decode (include/pa.h): argument checks, the choice of kernel and split, and
+// modes_api.cu -- entry points of the attention with modified scores, over block-scaled E4M3
+// caches and across to other states, and of the shared-prefix decode (include/pa.h): argument checks, the choice of kernel and split, and
 // the launches.  Host code only.
 #include <algorithm>
 #include <cmath>
@@ -31,6 +31,8 @@ struct Plan {
 struct Shape {
     pa_dtype q_dtype, kv_dtype;
     int num_q_heads, num_kv_heads, head_dim, block_size;
+    int64_t scale_stride = 0;    // > 0: E4M3 scales for each block, this many floats apart
+    bool block_scales() const { return scale_stride > 0; }
     int group() const { return num_q_heads / num_kv_heads; }
     bool fp8() const { return kv_dtype == PA_FP8_E4M3; }
 };
@@ -38,6 +40,10 @@ struct Shape {
 int occupancy(const Shape& s, AttnMode mode, Family f, int per)
 {
     const bool bf16 = s.q_dtype == PA_BF16;
+    if (mode == kBlock && f == Family::kRows)
+        return (bf16 ? occupancy_rows_block_bf16 : occupancy_rows_block_f16)(s.head_dim, s.block_size, per);
+    if (mode == kBlock && f == Family::kChunk)
+        return (bf16 ? occupancy_chunk_block_bf16 : occupancy_chunk_block_f16)(s.head_dim, s.block_size);
     switch (f) {
     case Family::kCore:
         return occupancy_core_mode(mode, s.q_dtype, s.kv_dtype, s.head_dim, s.block_size, per);
@@ -119,7 +125,7 @@ Plan plan_heads(const Shape& s)
         pl.tile = 128;
         return pl;
     }
-    if (G <= 2) {
+    if (G <= 2 && !s.block_scales()) {
         pl.family = Family::kCore;
         pl.per = G;
         pl.chunks = 1;
@@ -160,6 +166,12 @@ cudaError_t launch(const Shape& s, AttnMode mode, const Plan& pl, const DecodePa
                    cudaStream_t st)
 {
     const bool bf16 = s.q_dtype == PA_BF16;
+    if (mode == kBlock && pl.family == Family::kRows)
+        return (bf16 ? launch_rows_block_bf16 : launch_rows_block_f16)(d, s.head_dim, s.block_size, pl.per, tk,
+                                                                       tv, grid, st);
+    if (mode == kBlock && pl.family == Family::kChunk)
+        return (bf16 ? launch_chunk_block_bf16 : launch_chunk_block_f16)(c, s.head_dim, s.block_size, tk, tv,
+                                                                         grid, st);
     switch (pl.family) {
     case Family::kCore:
         return launch_core_mode(d, mode, s.q_dtype, s.kv_dtype, s.head_dim, s.block_size, pl.per, grid,
@@ -219,12 +231,19 @@ int check_shape(const Shape& s, pa_dtype out_dtype, const float* k_scale, const 
     return 1;
 }
 
+// The scales of consecutive blocks are rows of scale_stride floats.
+int check_scale_stride(int64_t scale_stride, int num_kv_heads)
+{
+    return num_kv_heads <= 0 || scale_stride < num_kv_heads || scale_stride > (int64_t(1) << 40) ? PA_ERR_INVALID
+                                                                                               : 1;
+}
+
 constexpr int kMaxContext = 1 << 30;             // positions and their sums stay in int32
 
 struct Buffers {
     void* out;
     size_t out_bytes;
-    Span spans[9];
+    Span spans[11];
     int n = 0;
     void add(const void* p, size_t bytes)
     {
@@ -263,9 +282,12 @@ int64_t seen_bound(int max_context_len, int window, int max_global, int query_le
     return std::min(all, tiles * tile);
 }
 
-// Shared body of the four modified-score calls; query_start null: decode (one row per
-// sequence, num_query_tokens = num_seqs).
-int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Shape& s,
+// What a call of mod_impl is: decode (one row per sequence, query_start null, num_query_tokens =
+// num_seqs), a causal chunk, or cross attention (every row sees all tokens).
+enum class Call { kDecode, kChunk, kCross };
+
+// Shared body of the calls with modified scores, over block-scaled caches and across.
+int mod_impl(Call call, void* out, pa_dtype out_dtype, const void* q, const Shape& s,
              const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
              int64_t num_blocks, const int32_t* block_tables, int64_t block_table_stride,
              const int32_t* context_lens, const int32_t* query_start, int64_t num_query_tokens,
@@ -274,6 +296,7 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
              int32_t max_global_len, int32_t partition_size, void* workspace, size_t workspace_bytes,
              void* stream)
 {
+    const bool decode = call == Call::kDecode, cross = call == Call::kCross;
     const int ok = check_shape(s, out_dtype, k_scale, v_scale, num_blocks, block_table_stride, num_seqs,
                                scale, partition_size);
     if (ok <= 0)
@@ -282,7 +305,7 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
         return s.q_dtype == PA_F32 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID;
     if (max_context_len < 0 || max_context_len > kMaxContext ||
         (int64_t)max_context_len > block_table_stride * s.block_size || max_query_len < 0 ||
-        max_query_len > max_context_len || num_query_tokens < 0 || num_query_tokens > INT32_MAX)
+        (!cross && max_query_len > max_context_len) || num_query_tokens < 0 || num_query_tokens > INT32_MAX)
         return PA_ERR_INVALID;
     // the cap's reciprocal and its base-2 form stay normal numbers
     if (!(softcap == 0.f || (softcap >= 1e-30f && softcap <= 1e30f)) || window < 0 || max_global_len < 0)
@@ -295,6 +318,10 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
         !aligned4(alibi_slopes) || !aligned4(global_lens) || !aligned4(block_tables) ||
         !aligned4(context_lens) || !aligned4(query_start) || !aligned4(k_scale) || !aligned4(v_scale))
         return PA_ERR_INVALID;
+    if (cross) {                                 // every row sees its sequence's whole context
+        global_lens = context_lens;
+        max_global_len = max_context_len;
+    }
     if (!global_lens)
         max_global_len = 0;
     const int qlen = decode ? 1 : max_query_len;
@@ -302,9 +329,11 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
     // capped: 35.1 against 49.3 us over a window of 1024, 198 against 278 over 8192 tokens; 64 rows
     // 60.2 against 51.4 and 377 against 280)
     Plan pl = decode ? plan_heads(s) : plan_rows(s, qlen, kChunkRowsMax);
-    AttnMode mode = kMod;
+    AttnMode mode = s.block_scales() ? kBlock : kMod;
     const bool cap = softcap > 0.f, slope = alibi_slopes != nullptr;
-    if (pl.family == Family::kChunk)
+    if (s.block_scales())
+        ;                                        // (no cap, no slopes)
+    else if (pl.family == Family::kChunk)
         mode = cap ? (slope ? kModBoth : kModCap) : (slope ? kModSlope : kMod);
     else if (pl.family == Family::kRows)
         mode = cap || slope ? kModBoth : kMod;
@@ -327,6 +356,11 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
     b.add(query_start, (size_t)(num_seqs + 1) * 4);
     b.add(alibi_slopes, (size_t)s.num_q_heads * 4);
     b.add(global_lens, (size_t)num_seqs * 4);
+    if (s.block_scales()) {
+        const size_t scales = ((size_t)(num_blocks - 1) * s.scale_stride + s.num_kv_heads) * 4;
+        b.add(k_scale, scales);
+        b.add(v_scale, scales);
+    }
     if (!b.out_clear())
         return PA_ERR_INVALID;
 
@@ -358,6 +392,8 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
     d.mods.global_lens = global_lens;
     d.mods.window = window;
     d.mods.max_global = max_global_len;
+    d.mods.all_seen = cross ? 1 : 0;
+    d.scale_stride = s.scale_stride;
     if (softcap > 0.f) {
         d.mods.cap = (float)((double)softcap * 1.4426950408889634);
         d.mods.inv_cap = 1.f / d.mods.cap;
@@ -436,6 +472,7 @@ int mod_impl(bool decode, void* out, pa_dtype out_dtype, const void* q, const Sh
     c.scale_log2 = d.scale_log2;
     c.mods = d.mods;
     c.whole_units = d.whole_units;
+    c.scale_stride = s.scale_stride;
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // a one-pass CUDA-core grid of several waves starts the longest sequences first, as
@@ -645,7 +682,7 @@ int pa_decode_mod(void* out, pa_dtype out_dtype, const void* q, const void* k_ca
 {
     if (!valid_dtype(kv_dtype))
         return PA_ERR_INVALID;
-    return mod_impl(true, out, out_dtype, q,
+    return mod_impl(Call::kDecode, out, out_dtype, q,
                     Shape{kv_dtype, kv_dtype, num_q_heads, num_kv_heads, head_dim, block_size}, k_cache,
                     v_cache, nullptr, nullptr, num_blocks, block_tables, block_table_stride, context_lens,
                     nullptr, num_seqs, 0, max_context_len, num_seqs, scale, softcap, alibi_slopes,
@@ -663,7 +700,7 @@ int pa_decode_mod_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_d
                       const int32_t* global_lens, int32_t max_global_len, int32_t partition_size,
                       void* workspace, size_t workspace_bytes, void* stream)
 {
-    return mod_impl(true, out, out_dtype, q,
+    return mod_impl(Call::kDecode, out, out_dtype, q,
                     Shape{q_dtype, PA_FP8_E4M3, num_q_heads, num_kv_heads, head_dim, block_size}, k_cache,
                     v_cache, k_scale, v_scale, num_blocks, block_tables, block_table_stride, context_lens,
                     nullptr, num_seqs, 0, max_context_len, num_seqs, scale, softcap, alibi_slopes,
@@ -684,7 +721,7 @@ int pa_chunk_attention_mod(void* out, pa_dtype out_dtype, const void* q, const v
 {
     if (kv_dtype == PA_FP8_E4M3)
         return PA_ERR_UNSUPPORTED;               // E4M3 caches: pa_chunk_attention_mod_fp8
-    return mod_impl(false, out, out_dtype, q,
+    return mod_impl(Call::kChunk, out, out_dtype, q,
                     Shape{kv_dtype, kv_dtype, num_q_heads, num_kv_heads, head_dim, block_size}, k_cache,
                     v_cache, nullptr, nullptr, num_blocks, block_tables, block_table_stride, context_lens,
                     query_start, num_query_tokens, max_query_len, max_context_len, num_seqs, scale,
@@ -704,12 +741,108 @@ int pa_chunk_attention_mod_fp8(void* out, pa_dtype out_dtype, const void* q, pa_
                                int32_t max_global_len, int32_t partition_size, void* workspace,
                                size_t workspace_bytes, void* stream)
 {
-    return mod_impl(false, out, out_dtype, q,
+    return mod_impl(Call::kChunk, out, out_dtype, q,
                     Shape{q_dtype, PA_FP8_E4M3, num_q_heads, num_kv_heads, head_dim, block_size}, k_cache,
                     v_cache, k_scale, v_scale, num_blocks, block_tables, block_table_stride, context_lens,
                     query_start, num_query_tokens, max_query_len, max_context_len, num_seqs, scale,
                     softcap, alibi_slopes, window, global_lens, max_global_len, partition_size, workspace,
                     workspace_bytes, stream);
+}
+
+int pa_decode_fp8_block(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
+                        const void* k_cache, const void* v_cache, const float* k_scales,
+                        const float* v_scales, int64_t scale_stride, int64_t num_blocks,
+                        const int32_t* block_tables, int64_t block_table_stride,
+                        const int32_t* context_lens, int32_t max_context_len, int32_t num_seqs,
+                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                        int32_t block_size, float scale, int32_t partition_size, void* workspace,
+                        size_t workspace_bytes, void* stream)
+{
+    const int ok = check_scale_stride(scale_stride, num_kv_heads);
+    if (ok <= 0)
+        return ok;
+    return mod_impl(Call::kDecode, out, out_dtype, q,
+                    Shape{q_dtype, PA_FP8_E4M3, num_q_heads, num_kv_heads, head_dim, block_size, scale_stride},
+                    k_cache, v_cache, k_scales, v_scales, num_blocks, block_tables, block_table_stride,
+                    context_lens, nullptr, num_seqs, 0, max_context_len, num_seqs, scale, 0.f, nullptr, 0,
+                    nullptr, 0, partition_size, workspace, workspace_bytes, stream);
+}
+
+int pa_chunk_attention_fp8_block(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
+                                 const void* k_cache, const void* v_cache, const float* k_scales,
+                                 const float* v_scales, int64_t scale_stride, int64_t num_blocks,
+                                 const int32_t* block_tables, int64_t block_table_stride,
+                                 const int32_t* context_lens, const int32_t* query_start,
+                                 int64_t num_query_tokens, int32_t max_query_len,
+                                 int32_t max_context_len, int32_t num_seqs, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                 float scale, int32_t partition_size, void* workspace,
+                                 size_t workspace_bytes, void* stream)
+{
+    const int ok = check_scale_stride(scale_stride, num_kv_heads);
+    if (ok <= 0)
+        return ok;
+    return mod_impl(Call::kChunk, out, out_dtype, q,
+                    Shape{q_dtype, PA_FP8_E4M3, num_q_heads, num_kv_heads, head_dim, block_size, scale_stride},
+                    k_cache, v_cache, k_scales, v_scales, num_blocks, block_tables, block_table_stride,
+                    context_lens, query_start, num_query_tokens, max_query_len, max_context_len, num_seqs,
+                    scale, 0.f, nullptr, 0, nullptr, 0, partition_size, workspace, workspace_bytes, stream);
+}
+
+int pa_cross_attention(void* out, pa_dtype out_dtype, const void* q, const void* k_cache,
+                       const void* v_cache, pa_dtype kv_dtype, int64_t num_blocks,
+                       const int32_t* block_tables, int64_t block_table_stride,
+                       const int32_t* context_lens, const int32_t* query_start,
+                       int64_t num_query_tokens, int32_t max_query_len, int32_t max_context_len,
+                       int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                       int32_t block_size, float scale, int32_t partition_size, void* workspace,
+                       size_t workspace_bytes, void* stream)
+{
+    if (kv_dtype == PA_FP8_E4M3)
+        return PA_ERR_UNSUPPORTED;               // E4M3 caches: the _fp8 forms
+    return mod_impl(Call::kCross, out, out_dtype, q,
+                    Shape{kv_dtype, kv_dtype, num_q_heads, num_kv_heads, head_dim, block_size}, k_cache,
+                    v_cache, nullptr, nullptr, num_blocks, block_tables, block_table_stride, context_lens,
+                    query_start, num_query_tokens, max_query_len, max_context_len, num_seqs, scale, 0.f,
+                    nullptr, 0, nullptr, 0, partition_size, workspace, workspace_bytes, stream);
+}
+
+int pa_cross_attention_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
+                           const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, int64_t num_blocks, const int32_t* block_tables,
+                           int64_t block_table_stride, const int32_t* context_lens,
+                           const int32_t* query_start, int64_t num_query_tokens,
+                           int32_t max_query_len, int32_t max_context_len, int32_t num_seqs,
+                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t block_size, float scale, int32_t partition_size, void* workspace,
+                           size_t workspace_bytes, void* stream)
+{
+    return mod_impl(Call::kCross, out, out_dtype, q,
+                    Shape{q_dtype, PA_FP8_E4M3, num_q_heads, num_kv_heads, head_dim, block_size}, k_cache,
+                    v_cache, k_scale, v_scale, num_blocks, block_tables, block_table_stride, context_lens,
+                    query_start, num_query_tokens, max_query_len, max_context_len, num_seqs, scale, 0.f,
+                    nullptr, 0, nullptr, 0, partition_size, workspace, workspace_bytes, stream);
+}
+
+int pa_cross_attention_fp8_block(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype,
+                                 const void* k_cache, const void* v_cache, const float* k_scales,
+                                 const float* v_scales, int64_t scale_stride, int64_t num_blocks,
+                                 const int32_t* block_tables, int64_t block_table_stride,
+                                 const int32_t* context_lens, const int32_t* query_start,
+                                 int64_t num_query_tokens, int32_t max_query_len,
+                                 int32_t max_context_len, int32_t num_seqs, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                 float scale, int32_t partition_size, void* workspace,
+                                 size_t workspace_bytes, void* stream)
+{
+    const int ok = check_scale_stride(scale_stride, num_kv_heads);
+    if (ok <= 0)
+        return ok;
+    return mod_impl(Call::kCross, out, out_dtype, q,
+                    Shape{q_dtype, PA_FP8_E4M3, num_q_heads, num_kv_heads, head_dim, block_size, scale_stride},
+                    k_cache, v_cache, k_scales, v_scales, num_blocks, block_tables, block_table_stride,
+                    context_lens, query_start, num_query_tokens, max_query_len, max_context_len, num_seqs,
+                    scale, 0.f, nullptr, 0, nullptr, 0, partition_size, workspace, workspace_bytes, stream);
 }
 
 size_t pa_decode_prefix_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t head_dim,

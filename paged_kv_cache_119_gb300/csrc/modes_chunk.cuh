@@ -13,7 +13,7 @@ struct ChunkMode {
     static constexpr int kRaw = F8 ? 4 : 0;
     using Sm = ChunkSmem<D, kStages, kRaw>;
     static constexpr int kThreads = chunk_threads<T, kRaw, MODE>();
-    static constexpr int kSmem = Sm::kAlloc;
+    static constexpr int kSmem = is_block(MODE) ? Sm::kAllocBlock : Sm::kAlloc;
     static constexpr auto kernel() { return chunk_attn_kernel<T, D, BS, kStages, kRaw, MODE>; }
     static cudaError_t configure()
     {

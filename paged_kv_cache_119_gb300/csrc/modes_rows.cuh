@@ -18,10 +18,13 @@ struct RowsMode {
     static constexpr int kThreads = kDecodeThreads;
     static constexpr int smem_bytes()
     {
-        if constexpr (NH <= 8)
-            return MmaSmem<TK, D, BS * kBPT, kStages>::kAlloc;
-        else
-            return RowsSmem<TK, D, kStages, NH / kRowsGroup>::kAlloc;
+        if constexpr (NH <= 8) {
+            using Sm = MmaSmem<TK, D, BS * kBPT, kStages>;
+            return is_block(MODE) ? Sm::kAllocBlock : Sm::kAlloc;
+        } else {
+            using Sm = RowsSmem<TK, D, kStages, NH / kRowsGroup>;
+            return is_block(MODE) ? Sm::kAllocBlock : Sm::kAlloc;
+        }
     }
     static constexpr int kSmem = smem_bytes();
     static constexpr auto kernel()

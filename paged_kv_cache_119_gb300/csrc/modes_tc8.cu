@@ -42,6 +42,8 @@ bool tc8_any_mode(AttnMode mode, int block_size, int rows, F&& f)
 {
     if (mode == kMod)
         return tc8_variant<T, kMod>(block_size, rows, f);
+    if (mode == kBlock)
+        return tc8_variant<T, kBlock>(block_size, rows, f);
     if (mode == kPrefix)
         return tc8_variant<T, kPrefix>(block_size, rows, f);
     return mode == kSuffix && tc8_variant<T, kSuffix>(block_size, rows, f);

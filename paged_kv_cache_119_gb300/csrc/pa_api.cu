@@ -950,6 +950,160 @@ static int rotary_impl(void* q_out, int64_t q_out_stride, const void* q, int64_t
                : PA_ERR_CUDA;
 }
 
+// Shared body of the two appends; rotary_dim 0: nothing turns, no q.
+static int append_impl(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                       const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                       pa_dtype dtype, void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                       int64_t scale_stride, int64_t num_blocks, const int32_t* block_tables,
+                       int64_t block_table_stride, const int32_t* context_lens,
+                       const int32_t* query_start, const int32_t* positions, int64_t num_tokens,
+                       int32_t max_query_len, int32_t num_seqs, int32_t num_q_heads,
+                       int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                       const double* inv_freq, int32_t rotary_dim, int32_t interleaved, float magnitude,
+                       void* stream)
+{
+    const bool turn = rotary_dim != 0;
+    if (!(dtype == PA_F16 || dtype == PA_BF16))
+        return dtype == PA_F32 ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID;
+    if (num_tokens < 0 || num_tokens > INT32_MAX || max_query_len < 0 || num_seqs < 0 ||
+        num_seqs > 65535 || num_q_heads <= 0 || num_q_heads > 65535 || num_kv_heads <= 0 ||
+        num_kv_heads > 65535 || num_blocks <= 0 || num_blocks > INT32_MAX || block_table_stride <= 0 ||
+        scale_stride < num_kv_heads || scale_stride > (int64_t(1) << 40) || !std::isfinite(magnitude))
+        return PA_ERR_INVALID;
+    if (!(head_dim == 64 || head_dim == 128) || !(block_size == 16 || block_size == 32))
+        return PA_ERR_UNSUPPORTED;
+    // token positions, and the cells of a pool, are counted in 32 bits
+    if (block_table_stride > (int64_t(1) << 30) / block_size ||
+        num_blocks * num_kv_heads >= (int64_t(1) << 31))
+        return PA_ERR_INVALID;
+    if (turn) {
+        if (rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > head_dim || !inv_freq)
+            return PA_ERR_INVALID;
+        for (int i = 0; i < rotary_dim / 2; ++i)
+            if (!(std::fabs(inv_freq[i]) < 1048576.0))
+                return PA_ERR_INVALID;
+    }
+    if (num_tokens == 0 || num_seqs == 0 || max_query_len == 0)
+        return PA_OK;
+    if ((turn && (!q_out || !q)) || !k || !v || !k_cache || !v_cache || !k_scales || !v_scales ||
+        !block_tables || !context_lens || !query_start)
+        return PA_ERR_INVALID;
+    const int64_t q_row = (int64_t)num_q_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+    const int64_t strides[4] = {q_out_stride, q_stride, k_stride, v_stride};
+    const int64_t widths[4] = {q_row, q_row, kv_row, kv_row};
+    const void* rows[4] = {q_out, q, k, v};
+    const int first = turn ? 0 : 2;
+    for (int i = first; i < 4; ++i)
+        if (strides[i] < widths[i] || strides[i] > (int64_t(1) << 40) || strides[i] % 8 != 0 ||
+            !aligned16(rows[i]))
+            return PA_ERR_INVALID;
+    auto natural = [](const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !natural(k_scales, 4) || !natural(v_scales, 4) ||
+        !natural(block_tables, 4) || !natural(context_lens, 4) || !natural(query_start, 4) ||
+        !natural(positions, 4) || !natural(inv_freq, 8))
+        return PA_ERR_INVALID;
+    // what the call writes: the pools, the scales, q_out; none meets another or an input
+    const size_t pool = (size_t)num_blocks * num_kv_heads * block_size * head_dim;
+    const size_t scales = ((size_t)(num_blocks - 1) * scale_stride + num_kv_heads) * 4;
+    const Span writes[4] = {{k_cache, pool}, {v_cache, pool}, {k_scales, scales}, {v_scales, scales}};
+    const Span reads[4] = {{block_tables, (size_t)num_seqs * block_table_stride * 4},
+                           {context_lens, (size_t)num_seqs * 4},
+                           {query_start, (size_t)(num_seqs + 1) * 4},
+                           {positions, positions ? (size_t)num_tokens * 4 : 0}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if ((i < j && overlaps(writes[i].p, writes[i].n, writes[j].p, writes[j].n)) ||
+                overlaps(writes[i].p, writes[i].n, reads[j].p, reads[j].n))
+                return PA_ERR_INVALID;
+        for (int j = first; j < 4; ++j)
+            if (overlaps(writes[i].p, writes[i].n, rows[j],
+                         (size_t)((num_tokens - 1) * strides[j] + widths[j]) * 2))
+                return PA_ERR_INVALID;
+    }
+    if (turn) {
+        const size_t span = (size_t)((num_tokens - 1) * q_out_stride + q_row) * 2;
+        for (const Span& r : reads)
+            if (overlaps(q_out, span, r.p, r.n))
+                return PA_ERR_INVALID;
+        for (int i = 1; i < 4; ++i)
+            if (!(i == 1 && q_out == q && q_out_stride == q_stride) &&
+                rows_overlap(q_out, q_out_stride * 2, q_row * 2, rows[i], strides[i] * 2, widths[i] * 2,
+                             num_tokens))
+                return PA_ERR_INVALID;
+    }
+    AppendParams p{};
+    p.q_out = q_out;
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.k_cache = static_cast<unsigned char*>(k_cache);
+    p.v_cache = static_cast<unsigned char*>(v_cache);
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_start = query_start;
+    p.positions = positions;
+    p.err = device_error_word();
+    if (!p.err)
+        return PA_ERR_CUDA;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out_stride = q_out_stride;
+    p.scale_stride = scale_stride;
+    p.bt_stride = block_table_stride;
+    p.num_tokens = num_tokens;
+    p.num_blocks = num_blocks;
+    p.num_seqs = num_seqs;
+    p.max_query_len = max_query_len;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.half = rotary_dim / 2;
+    p.magnitude = magnitude;
+    for (int i = 0; i < rotary_dim / 2; ++i)
+        p.phase[i] = turn_fraction(inv_freq[i]);
+    return launch_append(p, dtype, head_dim, interleaved != 0, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+int pa_append_fp8_block(const void* k, int64_t k_stride, const void* v, int64_t v_stride, pa_dtype dtype,
+                        void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                        int64_t scale_stride, int64_t num_blocks, const int32_t* block_tables,
+                        int64_t block_table_stride, const int32_t* context_lens,
+                        const int32_t* query_start, int64_t num_tokens, int32_t max_query_len,
+                        int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        void* stream)
+{
+    return append_impl(nullptr, 0, nullptr, 0, k, k_stride, v, v_stride, dtype, k_cache, v_cache, k_scales,
+                       v_scales, scale_stride, num_blocks, block_tables, block_table_stride, context_lens,
+                       query_start, nullptr, num_tokens, max_query_len, num_seqs, num_kv_heads, num_kv_heads,
+                       head_dim, block_size, nullptr, 0, 0, 1.f, stream);
+}
+
+int pa_rotary_and_append_fp8_block(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                                   const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                   pa_dtype dtype, void* k_cache, void* v_cache, float* k_scales,
+                                   float* v_scales, int64_t scale_stride, int64_t num_blocks,
+                                   const int32_t* block_tables, int64_t block_table_stride,
+                                   const int32_t* context_lens, const int32_t* query_start,
+                                   const int32_t* positions, int64_t num_tokens, int32_t max_query_len,
+                                   int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, const double* inv_freq,
+                                   int32_t rotary_dim, int32_t interleaved, float magnitude, void* stream)
+{
+    if (rotary_dim == 0)
+        return PA_ERR_INVALID;
+    return append_impl(q_out, q_out_stride, q, q_stride, k, k_stride, v, v_stride, dtype, k_cache, v_cache,
+                       k_scales, v_scales, scale_stride, num_blocks, block_tables, block_table_stride,
+                       context_lens, query_start, positions, num_tokens, max_query_len, num_seqs, num_q_heads,
+                       num_kv_heads, head_dim, block_size, inv_freq, rotary_dim, interleaved, magnitude,
+                       stream);
+}
+
 int pa_rotary_and_cache(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
                         const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                         pa_dtype dtype, void* k_cache, void* v_cache,

@@ -38,6 +38,8 @@ constexpr int kAutoPartitionTokens = 512;
 //            648 against 508 us on 4 x 512 tokens of 8192 without a cap or slopes), kModBoth
 //            for any of them in decode_mma_kernel and decode_rows_kernel (tests for what a
 //            call does not have: 92 against 86 us on 48 windows of 4096 over an E4M3 cache)
+//   kBlock   kMod without a cap or slopes over E4M3 caches with a scale for each block and head
+//            (block_scale.cuh)
 enum AttnMode : int {
     kPlain = 0,
     kMod = 1,
@@ -45,10 +47,14 @@ enum AttnMode : int {
     kSuffix = 3,
     kModCap = 4,
     kModSlope = 5,
-    kModBoth = 6
+    kModBoth = 6,
+    kBlock = 7
 };
 __host__ __device__ constexpr bool is_mod(int mode) { return mode == kMod || mode >= kModCap; }
 __host__ __device__ constexpr bool has_cap(int mode) { return mode == kModCap || mode == kModBoth; }
+__host__ __device__ constexpr bool is_block(int mode) { return mode == kBlock; }
+// modes that cross attention runs in (ScoreMods::all_seen)
+__host__ __device__ constexpr bool takes_cross(int mode) { return mode == kMod || mode == kBlock; }
 __host__ __device__ constexpr bool has_slope(int mode) { return mode == kModSlope || mode == kModBoth; }
 
 // Modified scores (score_mods.cuh), in base-2 units.
@@ -59,6 +65,8 @@ struct ScoreMods {
     float inv_cap;               // 1 / cap
     int window;                  // 0: none
     int max_global;              // host bound: longer global_lens count as this
+    int all_seen;                // 1: cross attention, whose rows (as many as there are) see all
+                                 // tokens: global_lens are the context lengths
 };
 
 struct DecodeParams {
@@ -108,6 +116,7 @@ struct DecodeParams {
     int tile_align;              // merge of the shared prefix: block_size
     int rows_per_cta;            // kMod: (token, head) rows of a kv head one CTA serves
     int whole_units;             // kMod merge: (sequence, kv head, row tile) units without parts
+    int64_t scale_stride;        // kBlock: k_scale, v_scale are [num_blocks][scale_stride]
 };
 
 // Longest-first dispatch of a one-pass CUDA-core decode with more CTAs than one wave:
@@ -234,6 +243,40 @@ struct RotaryParams {
 cudaError_t launch_rotary(const RotaryParams& p, pa_dtype dtype, bool fp8, bool interleaved,
                           cudaStream_t stream);
 
+// New tokens appended to E4M3 caches with a scale for each block and head (append.cu); half = 0:
+// nothing turns and q is left out.
+constexpr int kAppendMaxPairs = 64;  // rotary_dim <= head_dim <= 128
+struct AppendParams {
+    void* q_out;
+    const void* q;
+    const void* k;
+    const void* v;
+    unsigned char* k_cache;
+    unsigned char* v_cache;
+    float* k_scales;                 // [num_blocks][scale_stride]
+    float* v_scales;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* query_start;
+    const int32_t* positions;        // [num_tokens], or null: a token's place in its sequence
+    unsigned* err;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+    int64_t scale_stride;
+    int64_t bt_stride;
+    int64_t num_tokens;
+    int64_t num_blocks;
+    int num_seqs;
+    int max_query_len;
+    int num_q_heads;
+    int num_kv_heads;
+    int block_size;
+    int half;                        // rotary_dim / 2
+    int per_seq;                     // units of each sequence; 0: its own number (launch_append)
+    float magnitude;
+    uint64_t phase[kAppendMaxPairs]; // turns per position as 0.64 fixed-point fractions
+};
+cudaError_t launch_append(AppendParams p, pa_dtype dtype, int head_dim, bool interleaved, cudaStream_t stream);
+
 // One copy_blocks launch covers up to kCopyMaxLayers layers and kCopyMaxPairs
 // pairs; the parameter block stays under the classic 4 KB kernel-parameter limit.
 constexpr int kCopyMaxLayers = 8;
@@ -306,6 +349,7 @@ struct ChunkParams {
     ScoreMods mods;              // kMod
     int whole_units;             // kMod: (sequence, kv head, row tile) units that are not split
     const int32_t* prefix_lens;  // kPrefix: shared tokens of each sequence
+    int64_t scale_stride;        // kBlock: k_scale, v_scale are [num_blocks][scale_stride]
 };
 cudaError_t launch_chunk_attention(const ChunkParams& p, pa_dtype dtype, int head_dim,
                                    int block_size, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -364,6 +408,19 @@ cudaError_t launch_rows_bf16_fp8(const DecodeParams& p, AttnMode mode, int head_
                        int nh, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                        cudaStream_t stream);
 int occupancy_rows_bf16_fp8(AttnMode mode, int head_dim, int block_size, int nh);
+// the same in mode kBlock (modes_block_*.cu), chunk_attn_kernel too:
+cudaError_t launch_rows_block_f16(const DecodeParams& p, int head_dim, int block_size, int nh,
+                       const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid, cudaStream_t stream);
+int occupancy_rows_block_f16(int head_dim, int block_size, int nh);
+cudaError_t launch_chunk_block_f16(const ChunkParams& p, int head_dim, int block_size,
+                       const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid, cudaStream_t stream);
+int occupancy_chunk_block_f16(int head_dim, int block_size);
+cudaError_t launch_rows_block_bf16(const DecodeParams& p, int head_dim, int block_size, int nh,
+                       const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid, cudaStream_t stream);
+int occupancy_rows_block_bf16(int head_dim, int block_size, int nh);
+cudaError_t launch_chunk_block_bf16(const ChunkParams& p, int head_dim, int block_size,
+                       const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid, cudaStream_t stream);
+int occupancy_chunk_block_bf16(int head_dim, int block_size);
 // decode_tc8_kernel (E4M3, head_dim 128), 1, 2 or 4 rows per CTA:
 cudaError_t launch_tc8_mode(const DecodeParams& p, AttnMode mode, pa_dtype q_dtype, int block_size,
                             int rows, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
