@@ -13,8 +13,8 @@
 // codes that fall below 2^-6, so that tokens appended one by one and all at once agree but for
 // those.
 //
-// Organisation.  A unit is one touched block of a sequence; a CTA takes a unit, or a slice of
-// its heads when there are few.  One warp holds the new rows of a (block, head) tile in
+// Organisation.  A unit is one touched block of a sequence; its CTAs take some of its K and V
+// tiles or some of its rows of q each.  One warp holds the new rows of a (block, head) tile in
 // registers as they were loaded (a row is D / 16 lanes x 16 elements), finds a by shuffles,
 // and converts from the registers: k and v are read once, and no atomics or second pass over
 // memory decide the scale.  When every sequence brings one token (a decode step) a row group of
@@ -90,6 +90,38 @@ __device__ __forceinline__ uint2 codes8(const float* f)
     return make_uint2(w[0], w[1]);
 }
 
+// The largest finite magnitude of the packed elements in m (a running maximum of magnitudes, two
+// 16-bit patterns a word: they order as the magnitudes do), or infinity when one was not finite.
+template <typename T>
+__device__ __forceinline__ float packed_max(uint32_t m)
+{
+    const uint32_t top = max(m & 0xffffu, m >> 16);
+    if constexpr (DType<T>::id == PA_BF16)
+        return top >= 0x7f80u ? INFINITY : __uint_as_float(top << 16);
+    else
+        return top >= 0x7c00u ? INFINITY : __half2float(__ushort_as_half((unsigned short)top));
+}
+
+__device__ __forceinline__ uint32_t fold_max(uint32_t m, const uint4& w)
+{
+    m = __vmaxu2(m, w.x & 0x7fff7fffu);
+    m = __vmaxu2(m, w.y & 0x7fff7fffu);
+    m = __vmaxu2(m, w.z & 0x7fff7fffu);
+    return __vmaxu2(m, w.w & 0x7fff7fffu);
+}
+
+// The same of finite elements alone.
+template <typename T>
+__device__ __forceinline__ uint32_t fold_finite(uint32_t m, const uint4& w)
+{
+    constexpr uint32_t kInf = DType<T>::id == PA_BF16 ? 0x7f807f80u : 0x7c007c00u;
+    const uint32_t u[4] = {w.x & 0x7fff7fffu, w.y & 0x7fff7fffu, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = __vmaxu2(m, u[i] & __vcmpltu2(u[i], kInf));
+    return m;
+}
+
 // The smallest power of two s within the scales' range with a <= 448 s (a finite, >= 0).
 __device__ __forceinline__ float scale_for(float a)
 {
@@ -108,9 +140,53 @@ __device__ __forceinline__ float2 turn(const AppendParams& p, int64_t position, 
     return make_float2(c * p.magnitude, s * p.magnitude);
 }
 
+// A thread's way through items numbered (token, head, item of the row): every `step`-th from the
+// first, without a division on the way.
+struct QWalk {
+    int row, t, h, j;                                 // row = t heads + h
+    int drow, dt, dh, dj, per, heads;
+    __device__ __forceinline__ static QWalk from(int first, int step, int per, int heads)
+    {
+        QWalk w;
+        w.per = per;
+        w.heads = heads;
+        w.row = first / per;
+        w.j = first - w.row * per;
+        w.t = w.row / heads;
+        w.h = w.row - w.t * heads;
+        w.drow = step / per;
+        w.dj = step - w.drow * per;
+        w.dt = w.drow / heads;
+        w.dh = w.drow - w.dt * heads;
+        return w;
+    }
+    __device__ __forceinline__ void advance()
+    {
+        row += drow;
+        t += dt;
+        h += dh;
+        j += dj;
+        if (j >= per) {
+            j -= per;
+            ++row;
+            ++h;
+        }
+        if (h >= heads) {
+            h -= heads;
+            ++t;
+        }
+    }
+};
+
+// CTAs per SM: the rows of q want loads in flight more than K and V want registers (4096 tokens and
+// more of 64 + 2 x 8 heads: 121 us with four, 133 with three); a tile of 32 rows of 128 is 64
+// registers a lane.
+template <int D, int B, bool ONE>
+constexpr int append_ctas() { return !ONE && D * B == 4096 ? 2 : 4; }
+
 // ONE: every sequence brings at most one token.  B: block size (ONE: of any kind).
 template <typename T, int D, int B, bool ONE, int LAYOUT>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p)
+__global__ void __launch_bounds__(kAppendThreads, append_ctas<D, B, ONE>()) append_kernel(const __grid_constant__ AppendParams p)
 {
     constexpr int LPR = D / 16;                       // lanes of a row
     constexpr int GROUP = ONE ? LPR : 32;             // lanes of a tile
@@ -221,8 +297,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 
     // ---- K and V tiles of the block: (head, K or V) numbered head fastest, K first
     const int tiles = 2 * p.num_kv_heads;
-    const int step = (int)gridDim.y * GPC;
-    if (have) {
+    const int step = p.kv_slices * GPC;
+    if (have && (int)blockIdx.y < p.kv_slices) {
         const int group = threadIdx.x / GROUP;
         const int sub = (threadIdx.x % GROUP) / LPR;  // the lane's row among RPI
         for (int base = (int)blockIdx.y * GPC; base < tiles; base += step) {
@@ -277,18 +353,41 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
                     unpack8<T>(w[i].b, f + 8);
                 }
             };
-            float amax = 0.f;                         // of the finite values
+            // the largest finite magnitude: of turned values in fp32, of others from the bits (ONE:
+            // a warp's tiles may be of both kinds, and shuffle together)
+            float amax = 0.f;
+            if (ONE || turned) {
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                float f[16];
-                load_values(i, f);
+                for (int i = 0; i < IT; ++i) {
+                    float f[16];
+                    load_values(i, f);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    amax = fabsf(f[e]) < INFINITY ? fmaxf(amax, fabsf(f[e])) : amax;
+                    for (int e = 0; e < 16; ++e)
+                        amax = fabsf(f[e]) < INFINITY ? fmaxf(amax, fabsf(f[e])) : amax;
+                }
+#pragma unroll
+                for (int m = GROUP / 2; m >= 1; m >>= 1)
+                    amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, m));
+            } else {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < IT; ++i)
+                    top = fold_max(fold_max(top, w[i].a), w[i].b);
+#pragma unroll
+                for (int m = GROUP / 2; m >= 1; m >>= 1)
+                    top = __vmaxu2(top, __shfl_xor_sync(kFullMask, top, m));
+                amax = packed_max<T>(top);
+                if (__any_sync(kFullMask, amax == INFINITY)) {       // some element is not finite
+                    top = 0;
+#pragma unroll
+                    for (int i = 0; i < IT; ++i)
+                        top = fold_finite<T>(fold_finite<T>(top, w[i].a), w[i].b);
+#pragma unroll
+                    for (int m = GROUP / 2; m >= 1; m >>= 1)
+                        top = __vmaxu2(top, __shfl_xor_sync(kFullMask, top, m));
+                    amax = packed_max<T>(top);
+                }
             }
-#pragma unroll
-            for (int m = GROUP / 2; m >= 1; m >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, m));
             float scale = scale_for(amax);
             if (r0 > 0) {
                 old = fminf(fmaxf(old, kScaleLow), kScaleHigh);
@@ -356,60 +455,78 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         }
     }
 
-    // ---- q: every row of the unit's tokens, 16 elements an item
-    if constexpr (kTurn && LAYOUT != kScalar) {
-        const int items = ntok * p.num_q_heads;       // rows; a row is LPR threads
-        const int rstep = (int)gridDim.y * (kAppendThreads / LPR);
-        const T* q = static_cast<const T*>(p.q);
-        T* qo = static_cast<T*>(p.q_out);
-        int da, db;
-        dims(j, true, da, db);
-        auto load = [&](int i, Raw16& w) {
-            if (i < items) {
-                const int t = i / p.num_q_heads;
-                const T* row = q + (row0 + t) * p.q_stride + (int64_t)(i - t * p.num_q_heads) * D;
-                w.a = *reinterpret_cast<const uint4*>(row + da);
-                w.b = *reinterpret_cast<const uint4*>(row + db);
+    // ---- q: the turned items of the unit's rows, J of a row, then the vectors past them
+    const int q_slice = (int)blockIdx.y - p.kv_slices;
+    const int q_step = ((int)gridDim.y - p.kv_slices) * kAppendThreads;
+    if (kTurn && LAYOUT != kScalar && q_slice >= 0) {
+        const int rows = ntok * p.num_q_heads;
+        const T* q = static_cast<const T*>(p.q) + row0 * p.q_stride;
+        T* qo = static_cast<T*>(p.q_out) + row0 * p.q_out_stride;
+        const int first_item = q_slice * kAppendThreads + threadIdx.x;
+        QWalk at = QWalk::from(first_item, q_step, J, p.num_q_heads), nx;
+        const int db_off = LAYOUT == kHalves ? half : 8;          // the second vector behind the first
+        const int da_mul = LAYOUT == kHalves ? 8 : 16;
+        auto load = [&](const QWalk& k, Raw16& w) {
+            if (k.row < rows) {
+                const T* row = q + k.t * p.q_stride + k.h * D + k.j * da_mul;
+                w.a = *reinterpret_cast<const uint4*>(row);
+                w.b = *reinterpret_cast<const uint4*>(row + db_off);
             }
         };
-        int i = (int)blockIdx.y * (kAppendThreads / LPR) + threadIdx.x / LPR;
         Raw16 w, next;
-        load(i, w);
-        for (; i < items; i += rstep) {
-            load(i + rstep, next);
-            const int t = i / p.num_q_heads;
-            T* row = qo + (row0 + t) * p.q_out_stride + (int64_t)(i - t * p.num_q_heads) * D;
+        load(at, w);
+        while (at.row < rows) {
+            nx = at;
+            nx.advance();
+            load(nx, next);
             float f[16];
-            Raw16 out = w;
-            if (values(w, j, t, f)) {
-                out.a = pack8<T>(f);
-                out.b = pack8<T>(f + 8);
-                if constexpr (LAYOUT == kPairs) {
-                    // pairs past the last that turns, bit for bit
-                    const int keep = half - 8 * j;    // turned pairs of the item
-                    if (keep < 8) {
-                        uint32_t* o = reinterpret_cast<uint32_t*>(&out);
-                        const uint32_t* in = reinterpret_cast<const uint32_t*>(&w);
+            values(w, at.j, at.t, f);
+            Raw16 out;
+            out.a = pack8<T>(f);
+            out.b = pack8<T>(f + 8);
+            if constexpr (LAYOUT == kPairs) {
+                // pairs past the last that turns, bit for bit
+                const int keep = half - 8 * at.j;                 // turned pairs of the item
+                if (keep < 8) {
+                    uint32_t* o = reinterpret_cast<uint32_t*>(&out);
+                    const uint32_t* in = reinterpret_cast<const uint32_t*>(&w);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            o[k] = k < keep ? o[k] : in[k];
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        o[k] = k < keep ? o[k] : in[k];
                 }
             }
-            *reinterpret_cast<uint4*>(row + da) = out.a;
-            *reinterpret_cast<uint4*>(row + db) = out.b;
+            T* row = qo + at.t * p.q_out_stride + at.h * D + at.j * da_mul;
+            *reinterpret_cast<uint4*>(row) = out.a;
+            *reinterpret_cast<uint4*>(row + db_off) = out.b;
             w = next;
+            at = nx;
+        }
+        const int still = (D - 16 * J) / 8;                       // vectors of a row that do not turn
+        if (still > 0 && (p.q_out != p.q || p.q_out_stride != p.q_stride)) {
+            at = QWalk::from(first_item, q_step, still, p.num_q_heads);
+            while (at.row < rows) {
+                // four loads in flight
+                uint4 v[4];
+                QWalk k = at;
+#pragma unroll
+                for (int i = 0; i < 4; ++i, k.advance())
+                    if (k.row < rows)
+                        v[i] = *reinterpret_cast<const uint4*>(q + k.t * p.q_stride + k.h * D + 16 * J + 8 * k.j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i, at.advance())
+                    if (at.row < rows)
+                        *reinterpret_cast<uint4*>(qo + at.t * p.q_out_stride + at.h * D + 16 * J + 8 * at.j) = v[i];
+            }
         }
     }
-    if constexpr (LAYOUT == kScalar) {
+    if (LAYOUT == kScalar && q_slice >= 0) {
         // a pair, or an element past the pairs, at a time (a pair's elements are read and
         // written by one thread: q may be turned in place)
         const int per = D - half;
         const int64_t items = (int64_t)ntok * p.num_q_heads * per;
         const T* q = static_cast<const T*>(p.q);
         T* qo = static_cast<T*>(p.q_out);
-        for (int64_t i = (int64_t)blockIdx.y * kAppendThreads + threadIdx.x; i < items;
-             i += (int64_t)gridDim.y * kAppendThreads) {
+        for (int64_t i = (int64_t)q_slice * kAppendThreads + threadIdx.x; i < items; i += q_step) {
             const int row = (int)(i / per), e = (int)(i - (int64_t)row * per);
             const int t = row / p.num_q_heads, h = row - t * p.num_q_heads;
             const T* in = q + (row0 + t) * p.q_stride + (int64_t)h * D;
@@ -427,20 +544,29 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 }
 
 template <typename T, int D, int B, bool ONE, int LAYOUT>
-cudaError_t launch_variant(const AppendParams& p, int64_t units, cudaStream_t stream)
+cudaError_t launch_variant(AppendParams p, int64_t units, cudaStream_t stream)
 {
     constexpr int LPR = D / 16;
     constexpr int GPC = kAppendThreads / (ONE ? LPR : 32);
-    // few units: their heads are shared over CTAs until the grid holds four per SM
+    // A unit's CTAs: some for its K and V tiles, others for its rows of q, each with a few rounds
+    // of work; fewer rounds while the grid would not hold four CTAs per SM.
     const int sms = device_sm_count() > 0 ? device_sm_count() : 152;
     const int64_t tiles = (2 * (int64_t)p.num_kv_heads + GPC - 1) / GPC;
     const int64_t rows = LAYOUT == kStill ? 0
                                           : ((ONE ? 1 : B) * (int64_t)p.num_q_heads + kAppendThreads / LPR - 1) /
                                                 (kAppendThreads / LPR);
-    const int64_t most = std::max<int64_t>(1, std::max(tiles, rows));
-    const int64_t slices = std::min(most, (4 * (int64_t)sms + units - 1) / units);
+    auto slices = [&](int64_t work, int64_t rounds) { return (work + rounds - 1) / rounds; };
+    int64_t kv_rounds = 2, q_rounds = 16;
+    while (kv_rounds > 1 && units * (slices(tiles, kv_rounds) + slices(rows, q_rounds)) < 4 * (int64_t)sms)
+        kv_rounds /= 2;
+    while (q_rounds > 1 && units * (slices(tiles, kv_rounds) + slices(rows, q_rounds)) < 4 * (int64_t)sms)
+        q_rounds /= 2;
+    p.kv_slices = (int)slices(tiles, kv_rounds);
+    const int64_t all = p.kv_slices + slices(rows, q_rounds);
+    if (all > 65535)
+        return cudaErrorInvalidValue;
     append_kernel<T, D, B, ONE, LAYOUT>
-        <<<dim3((unsigned)units, (unsigned)slices), kAppendThreads, 0, stream>>>(p);
+        <<<dim3((unsigned)units, (unsigned)all), kAppendThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -272,6 +272,7 @@ struct AppendParams {
     int block_size;
     int half;                        // rotary_dim / 2
     int per_seq;                     // units of each sequence; 0: its own number (launch_append)
+    int kv_slices;                   // CTAs of a unit for its K and V; the others turn q
     float magnitude;
     uint64_t phase[kAppendMaxPairs]; // turns per position as 0.64 fixed-point fractions
 };
