@@ -19,11 +19,27 @@ namespace pa {
 
 constexpr float kScaleLow = 0x1p-48f, kScaleHigh = 0x1p48f;
 
-// (K scale, log2 of the V scale, its reciprocal) of a block and head; exact for powers of two.
-__device__ __forceinline__ float4 block_scale(const float* k_scale, const float* v_scale, int64_t i)
+// The scales of block e (1 where e is no block of the pool) and a head as they lie in memory,
+// loaded well before they are used ...
+struct RawScale {
+    float k, v;
+};
+template <typename P>
+__device__ __forceinline__ RawScale load_scale(const P& p, int e, int head)
 {
-    const float k = fminf(fmaxf(__ldg(k_scale + i), kScaleLow), kScaleHigh);
-    const float v = fminf(fmaxf(__ldg(v_scale + i), kScaleLow), kScaleHigh);
+    if (e < 0 || (int64_t)e >= p.num_blocks)
+        return RawScale{1.f, 1.f};
+    const int64_t i = (int64_t)e * p.scale_stride + head;
+    return RawScale{__ldg(p.k_scale + i), __ldg(p.v_scale + i)};
+}
+
+// ... and as the kernels use them: (K scale, log2 of the V scale, its reciprocal); exact for
+// powers of two.  (Together in one step, every tile of the chunk kernel waited for the loads:
+// 1.43 us a tile against 0.96.)
+__device__ __forceinline__ float4 block_scale(const RawScale& s)
+{
+    const float k = fminf(fmaxf(s.k, kScaleLow), kScaleHigh);
+    const float v = fminf(fmaxf(s.v, kScaleLow), kScaleHigh);
     const int bits = __float_as_int(v);
     const float frac = __int_as_float((bits & 0x7fffff) | 0x3f800000);      // [1, 2)
     const float lg = frac == 1.f ? 0.f : log2f(frac);

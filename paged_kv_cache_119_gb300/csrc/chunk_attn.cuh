@@ -137,6 +137,26 @@ struct ChunkStages {
     static constexpr int value = D == 128 ? 5 : 8;
 };
 
+// Packs 8 outputs v[i] * mul (NaN when nan_out) as f16 (which = 1) or bf16 (2).
+__device__ __forceinline__ uint4 pack_out8(const float* v, float mul, bool nan_out, int which)
+{
+    const float qnan = __int_as_float(0x7fc00000);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = nan_out ? qnan : v[2 * i] * mul;
+        const float b = nan_out ? qnan : v[2 * i + 1] * mul;
+        if (which == 1) {
+            const __half2 h = __floats2half2_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Stores 32 consecutive outputs v[i] * mul (NaN when nan_out) at base + idx as
 // fp32 (which = 0), f16 (1) or bf16 (2); idx is a multiple of 32.
 __device__ __forceinline__ void store_row32(void* base, int64_t idx, const float (&v)[32], float mul,
@@ -152,23 +172,10 @@ __device__ __forceinline__ void store_row32(void* base, int64_t idx, const float
                                            v[4 * i + 3] * mul);
         return;
     }
-    uint32_t packed[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float a = nan_out ? qnan : v[2 * i] * mul;
-        const float b = nan_out ? qnan : v[2 * i + 1] * mul;
-        if (which == 1) {
-            __half2 h = __floats2half2_rn(a, b);
-            packed[i] = *reinterpret_cast<uint32_t*>(&h);
-        } else {
-            __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-            packed[i] = *reinterpret_cast<uint32_t*>(&h);
-        }
-    }
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + idx);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        dst[i] = make_uint4(packed[4 * i], packed[4 * i + 1], packed[4 * i + 2], packed[4 * i + 3]);
+        dst[i] = pack_out8(v + 8 * i, mul, nan_out, which);
 }
 
 // max(a, b, c) in one instruction (NaN operands are ignored, as by fmaxf).
@@ -308,6 +315,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     constexpr bool kF8 = NRAW > 0;
     constexpr bool kIsMod = is_mod(MODE), kCap = has_cap(MODE), kSlope = has_slope(MODE);
     constexpr bool kBlk = is_block(MODE);
+    constexpr bool kWideIO = !kCap && !kSlope;   // warps read q and write out by whole rows
     static_assert(!kBlk || kF8, "block scales belong to E4M3 caches");
     constexpr bool kTwoTerms = MODE == kPrefix;  // P as hi + lo of V's type, else one f16 term
     constexpr bool kVConv = !kF8 && std::is_same_v<T, __nv_bfloat16> && !kTwoTerms;   // bf16 V -> f16 in place
@@ -495,25 +503,23 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         uint64_t* pempty = kF8 ? raw_empty : empty;
         int* pok = kF8 ? raw_ok : stage_ok;
         int issued = 0;
-        // kBlock: this lane's table entry of a tile (-2: none to read), two tiles ahead, and the
-        // scales of its block, one tile ahead
-        auto entry = [&](int it) -> int {
-            if (it >= ntiles || lane >= BPT)
-                return -2;
+        // kBlock: this lane's table entry of a tile, two tiles ahead, and the scales of its block,
+        // one tile ahead (loaded values are not touched before their turn: a wait for each of them,
+        // tile by tile, took 1.3 us a tile)
+        auto wanted = [&](int it) -> bool {
             const int b = tile_token(it) / BS + lane;
-            return b < blk_end && any_seen(seen, b * BS, min(b * BS + BS, t1)) ? max(__ldg(bt_row + b), -1) : -2;
+            return it < ntiles && lane < BPT && b < blk_end && any_seen(seen, b * BS, min(b * BS + BS, t1));
         };
-        auto scale_of = [&](int e) -> float4 {
-            return e >= 0 && (int64_t)e < p.num_blocks
-                       ? block_scale(p.k_scale, p.v_scale, (int64_t)e * p.scale_stride + kvh)
-                       : make_float4(1.f, 0.f, 1.f, 0.f);
+        auto entry = [&](int it) -> int {
+            return wanted(it) ? __ldg(bt_row + tile_token(it) / BS + lane) : -1;
         };
-        int cur = -2, next = -2;
-        float4 sc{}, next_sc{};
+        int cur = -1, next = -1;
+        float4 sc{};
+        RawScale next_sc{};
         if constexpr (kBlk) {
             cur = entry(0);
             next = entry(1);
-            next_sc = scale_of(cur);
+            next_sc = load_scale(p, cur, kvh);
         }
         for (int it = 0; it < ntiles; ++it) {
             const int st = it % NP;
@@ -523,14 +529,14 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
             int pbn = -1;
             bool valid = false;
             if constexpr (kBlk) {
-                want = cur != -2;
+                want = wanted(it);
                 pbn = cur;
                 valid = pbn >= 0 && (int64_t)pbn < p.num_blocks;
                 nb = __popc(__ballot_sync(kFullMask, want));
                 cur = next;
                 next = entry(it + 2);
-                sc = next_sc;
-                next_sc = scale_of(cur);
+                sc = block_scale(next_sc);       // (behind the wait for the slot: 1.22 us a tile, 1.01 here)
+                next_sc = load_scale(p, cur, kvh);
             } else if constexpr (kIsMod) {        // only blocks that hold a seen token
                 want = want && any_seen(seen, (b0 + lane) * BS, min((b0 + lane) * BS + BS, t1));
                 nb = __popc(__ballot_sync(kFullMask, want));
@@ -805,6 +811,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         const int low = kIsMod && p.mods.window > 0 ? max(0, pos - p.mods.window + 1) : 0;
         const float slope = kSlope ? base2_slope(p.mods.slopes[kvh * G + g]) : 0.f;
         const int64_t qrow = (int64_t)(qs0 + j0 + tok) * p.num_q_heads + (int64_t)kvh * G + g;
+        // 16-byte pieces of a row of 16-bit elements, and the rows a warp moves at a time
+        constexpr int CPR = D / 8, RPW = 32 / CPR;
         // scores are used as s * sl2 with sl2 > 0: a negative scale flips the sign of q
         // (exact), a zero scale makes q zero (every score 0); over E4M3 caches the K scale
         // of the kv head joins the softmax scale (kBlock: the one of a block, tile by tile)
@@ -813,56 +821,113 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         const bool qzero = sl2_raw == 0.f;
         float sl2 = qzero ? 1.f : fabsf(sl2_raw);
         {
-            // Q rows into the 128-byte-swizzled operand layout; rows past the chunk are 0
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
-                                                              (row_valid ? qrow : 0) * D);
-            unsigned char* qdst = smem + Sm::kQOff + q * Sm::kQTile + rr * 128;
-            constexpr bool kToF16 = kF8 && DType<T>::id == PA_BF16;
-            float down = 1.f;
-            if constexpr (kToF16) {
-                // a bf16 row becomes f16 operands: a power of two 2^-e puts its largest
-                // |q| in [2^14, 2^15), so the 8-bit mantissas convert exactly; 2^e goes
-                // into the row's score scale
-                float amax = 0.f;
-                if (row_valid && !qzero) {
-#pragma unroll 4
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 v = __ldg(src + c);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            // Q rows into the 128-byte-swizzled operand layout; rows past the chunk are 0.  The
+            // lanes of a warp read whole rows (CPR lanes of 16 bytes each), not one row a lane:
+            // with the epilogue's stores, which go the same way, one row a lane cost a CTA 3 to 5 us
+            // at head_dim 128 (256 rows over 64 tokens 12 against 9.5 us, 4 x 512 tokens of 8192, 64/8
+            // heads, 525 against 510).  Capped and biased scores keep a row a lane: their loops
+            // lose more to the registers (568 against 608 us, capped, f16).
+            if constexpr (kWideIO) {
+                unsigned char* qdst = smem + Sm::kQOff + q * Sm::kQTile + 32 * wq * 128;
+                constexpr bool kToF16 = kF8 && DType<T>::id == PA_BF16;
+                uint4 v[CPR];
+#pragma unroll
+                for (int i = 0; i < CPR; ++i) {
+                    const int64_t row = __shfl_sync(kFullMask, row_valid && !qzero ? qrow : -1, i * RPW + lane / CPR);
+                    v[i] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + row * D) +
+                                            lane % CPR)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int i = 0; i < CPR; ++i) {
+                    const int r32 = i * RPW + lane / CPR, c = lane % CPR;
+                    if constexpr (kToF16) {
+                        // a bf16 row becomes f16 operands: a power of two 2^-e puts its largest
+                        // |q| in [2^14, 2^15), so the 8-bit mantissas convert exactly; 2^e goes
+                        // into the row's score scale
+                        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        float amax = 0.f;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)),
                                                      fabsf(__uint_as_float(w[j] & 0xffff0000u))));
-                    }
-                }
-                const int ex = (__float_as_int(amax) >> 23) & 0xff;   // biased exponent
-                // amax in [2^(ex-127), 2^(ex-126)): scale by 2^(141 - ex); rows of zeros,
-                // tiny rows and a NaN / infinite row keep the scale 1
-                const int sh = (ex == 0 || ex == 255) ? 0 : max(-100, min(100, 141 - ex));
-                down = __int_as_float((127 + sh) << 23);
-                sl2 *= __int_as_float((127 - sh) << 23);
-            }
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (row_valid && !qzero) {
-                    v = __ldg(src + c);
-                    if constexpr (kToF16) {
-                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        for (int m = CPR / 2; m >= 1; m >>= 1)
+                            amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, m));
+                        const int ex = (__float_as_int(amax) >> 23) & 0xff;   // biased exponent
+                        // amax in [2^(ex-127), 2^(ex-126)): scale by 2^(141 - ex); rows of zeros,
+                        // tiny rows and a NaN / infinite row keep the scale 1
+                        const int sh = (ex == 0 || ex == 255) ? 0 : max(-100, min(100, 141 - ex));
+                        const float down = __int_as_float((127 + sh) << 23);
+                        const int own = __shfl_sync(kFullMask, sh, lane % RPW * CPR);   // of row i RPW + lane % RPW
+                        if (lane / RPW == i)
+                            sl2 *= __int_as_float((127 - own) << 23);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const __half2 h = __floats2half2_rn(__uint_as_float(w[j] << 16) * down,
                                                                 __uint_as_float(w[j] & 0xffff0000u) * down);
                             w[j] = *reinterpret_cast<const uint32_t*>(&h);
                         }
-                        v = make_uint4(w[0], w[1], w[2], w[3]);
+                        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    v.x ^= qflip;
-                    v.y ^= qflip;
-                    v.z ^= qflip;
-                    v.w ^= qflip;
+                    v[i].x ^= qflip;
+                    v[i].y ^= qflip;
+                    v[i].z ^= qflip;
+                    v[i].w ^= qflip;
+                    *reinterpret_cast<uint4*>(qdst + (c / 8) * Sm::kQHalf + r32 * 128 + (((c & 7) ^ (r32 & 7)) << 4)) =
+                        v[i];
                 }
-                *reinterpret_cast<uint4*>(qdst + (c / 8) * Sm::kQHalf + (((c & 7) ^ (rr & 7)) << 4)) = v;
+            } else {
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
+                                                                  (row_valid ? qrow : 0) * D);
+                unsigned char* qdst = smem + Sm::kQOff + q * Sm::kQTile + rr * 128;
+                constexpr bool kToF16 = kF8 && DType<T>::id == PA_BF16;
+                float down = 1.f;
+                if constexpr (kToF16) {
+                    // a bf16 row becomes f16 operands: a power of two 2^-e puts its largest
+                    // |q| in [2^14, 2^15), so the 8-bit mantissas convert exactly; 2^e goes
+                    // into the row's score scale
+                    float amax = 0.f;
+                    if (row_valid && !qzero) {
+#pragma unroll 4
+                        for (int c = 0; c < D / 8; ++c) {
+                            const uint4 v = __ldg(src + c);
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)),
+                                                         fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+                        }
+                    }
+                    const int ex = (__float_as_int(amax) >> 23) & 0xff;   // biased exponent
+                    // amax in [2^(ex-127), 2^(ex-126)): scale by 2^(141 - ex); rows of zeros,
+                    // tiny rows and a NaN / infinite row keep the scale 1
+                    const int sh = (ex == 0 || ex == 255) ? 0 : max(-100, min(100, 141 - ex));
+                    down = __int_as_float((127 + sh) << 23);
+                    sl2 *= __int_as_float((127 - sh) << 23);
+                }
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (row_valid && !qzero) {
+                        v = __ldg(src + c);
+                        if constexpr (kToF16) {
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const __half2 h = __floats2half2_rn(__uint_as_float(w[j] << 16) * down,
+                                                                    __uint_as_float(w[j] & 0xffff0000u) * down);
+                                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                            v = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        v.x ^= qflip;
+                        v.y ^= qflip;
+                        v.z ^= qflip;
+                        v.w ^= qflip;
+                    }
+                    *reinterpret_cast<uint4*>(qdst + (c / 8) * Sm::kQHalf + (((c & 7) ^ (rr & 7)) << 4)) = v;
+                }
             }
         }
         fence_proxy_async_smem();
@@ -1158,26 +1223,89 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
             // cannot overflow: |O| <= l max|v|, far inside fp32)
             const bool watch = kVConv && row_valid && !poisoned && lsum > 0.f && lsum < INFINITY;
             bool unconvertible = false;
+            if constexpr (kWideIO) {
+                // Rows go out through this warp's 32 rows of the query tile (no product reads them any
+                // more), so that its lanes store whole rows; piece c of a row at c ^ (row & 7).
+                unsigned char* stage = smem + Sm::kQOff + q * Sm::kQTile + 32 * wq * 128;
+                const int64_t orow = row_valid ? qrow : -1;
+                auto piece = [&](int r32, int c) -> uint4* {
+                    return reinterpret_cast<uint4*>(stage + (c / 8) * Sm::kQHalf + r32 * 128 +
+                                                    (((c & 7) ^ (r32 & 7)) << 4));
+                };
 #pragma unroll 1
-            for (int c4 = 0; c4 < D / 32; ++c4) {
-                float o[32];
-                tmem_ld32(o_col + 32 * c4, o);
-                if (!row_valid)
-                    continue;
-                if (watch)
+                for (int c4 = 0; c4 < D / 32; ++c4) {
+                    float o[32];
+                    tmem_ld32(o_col + 32 * c4, o);
+                    if (watch)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        unconvertible |= !(fabsf(o[i]) < INFINITY);
-                if (split) {
-                    const int64_t prw = qrow * p.max_parts + part;
-                    store_row32(p.part_o, prw * D + 32 * c4, o, inv, poisoned, 0);
-                    if (c4 == 0) {
-                        p.part_ml[prw * 2 + 0] = poisoned ? __int_as_float(0x7fc00000) : m_ref;
-                        // the sum carries 2^7; the suffix rows it is merged with do not
-                        p.part_ml[prw * 2 + 1] = MODE == kPrefix ? lsum * 0x1p-7f : lsum;
+                        for (int i = 0; i < 32; ++i)
+                            unconvertible |= !(fabsf(o[i]) < INFINITY);
+                    if (which != 0) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *piece(lane, 4 * c4 + k) = pack_out8(o + 8 * k, inv, poisoned, which);
+                        continue;
                     }
-                } else {
-                    store_row32(p.out, qrow * D + 32 * c4, o, inv, poisoned, which);
+                    // fp32: 32 columns are 128 bytes of a row
+                    const float qnan = __int_as_float(0x7fc00000);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 f = poisoned ? make_float4(qnan, qnan, qnan, qnan)
+                                                  : make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv,
+                                                                o[4 * k + 3] * inv);
+                        *piece(lane, k) = *reinterpret_cast<const uint4*>(&f);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t row = __shfl_sync(kFullMask, orow, 4 * i + lane / 8);
+                        if (row >= 0) {
+                            float* dst = split ? p.part_o + (row * p.max_parts + part) * D
+                                               : static_cast<float*>(p.out) + row * D;
+                            *reinterpret_cast<uint4*>(dst + 32 * c4 + 4 * (lane % 8)) = *piece(4 * i + lane / 8, lane % 8);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (which != 0) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < CPR; ++i) {
+                        const int r32 = i * RPW + lane / CPR;
+                        const int64_t row = __shfl_sync(kFullMask, orow, r32);
+                        if (row >= 0)
+                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + 8 * (lane % CPR)) =
+                                *piece(r32, lane % CPR);
+                    }
+                }
+                if (split && row_valid) {
+                    const int64_t prw = qrow * p.max_parts + part;
+                    p.part_ml[prw * 2 + 0] = poisoned ? __int_as_float(0x7fc00000) : m_ref;
+                    // the sum carries 2^7; the suffix rows it is merged with do not
+                    p.part_ml[prw * 2 + 1] = MODE == kPrefix ? lsum * 0x1p-7f : lsum;
+                }
+            } else {
+#pragma unroll 1
+                for (int c4 = 0; c4 < D / 32; ++c4) {
+                    float o[32];
+                    tmem_ld32(o_col + 32 * c4, o);
+                    if (!row_valid)
+                        continue;
+                    if (watch)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            unconvertible |= !(fabsf(o[i]) < INFINITY);
+                    if (split) {
+                        const int64_t prw = qrow * p.max_parts + part;
+                        store_row32(p.part_o, prw * D + 32 * c4, o, inv, poisoned, 0);
+                        if (c4 == 0) {
+                            p.part_ml[prw * 2 + 0] = poisoned ? __int_as_float(0x7fc00000) : m_ref;
+                            // the sum carries 2^7; the suffix rows it is merged with do not
+                            p.part_ml[prw * 2 + 1] = MODE == kPrefix ? lsum * 0x1p-7f : lsum;
+                        }
+                    } else {
+                        store_row32(p.out, qrow * D + 32 * c4, o, inv, poisoned, which);
+                    }
                 }
             }
             if (kVConv && __any_sync(kFullMask, unconvertible) && lane == 0)

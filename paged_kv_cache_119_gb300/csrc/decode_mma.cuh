@@ -404,16 +404,11 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
             next = (lane < nblk) ? __ldg(bt_row + lane) : 0;
         // kBlock: the scales of this lane's block of the batch (entries are then fetched two
         // batches ahead, their scales one)
-        auto scale_of = [&](int e) -> float4 {
-            return e >= 0 && (int64_t)e < p.num_blocks
-                       ? block_scale(p.k_scale, p.v_scale, (int64_t)e * p.scale_stride + kvh)
-                       : make_float4(1.f, 0.f, 1.f, 0.f);
-        };
         int after = 0;
-        float4 sc{};
+        RawScale sc{};
         if constexpr (kBlk) {
             after = entry(32 + lane);
-            sc = scale_of(next);
+            sc = load_scale(p, next, kvh);
         }
         bool aborted = false;
         // block-table entries 32 at a time (BPT divides 32, so no tile straddles two
@@ -421,10 +416,10 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
         for (int base = 0; base < nblk && !aborted; base += 32) {
             const int cur = next;
             if constexpr (kBlk) {
-                scales[(base + lane) & (kScaleRing - 1)] = sc;
+                scales[(base + lane) & (kScaleRing - 1)] = block_scale(sc);
                 __syncwarp();
                 next = after;
-                sc = scale_of(next);
+                sc = load_scale(p, next, kvh);
                 after = entry(base + 64 + lane);
             } else if constexpr (kIsMod) {
                 next = entry(base + 32 + lane);

@@ -620,15 +620,11 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
             const int t = tile_token(it) + tl;
             return it < ntiles && t < t1 ? __ldg(bt_row + t / BS) : -1;
         };
-        auto scale_of = [&](int e) -> float4 {
-            return e >= 0 && (int64_t)e < p.num_blocks
-                       ? block_scale(p.k_scale, p.v_scale, (int64_t)e * p.scale_stride + kvh)
-                       : make_float4(1.f, 0.f, 1.f, 0.f);
-        };
         int next_block = -1;
-        float4 sc{}, next_sc{};
+        float4 sc{};
+        RawScale next_sc{};
         if constexpr (kBlk) {
-            next_sc = scale_of(block_of(0));
+            next_sc = load_scale(p, block_of(0), kvh);
             next_block = block_of(1);
         }
         for (int it = 0; it < ntiles; ++it) {
@@ -636,8 +632,8 @@ __global__ void __launch_bounds__(kTc8Threads, 3)
             const int st = it % NST;
             const int tb = tile_token(it);
             if constexpr (kBlk) {
-                sc = next_sc;
-                next_sc = scale_of(next_block);
+                sc = block_scale(next_sc);
+                next_sc = load_scale(p, next_block, kvh);
                 next_block = block_of(it + 2);
             }
             // the scores imply the tile's K (the K slot may already hold a later tile:
