@@ -547,10 +547,8 @@ def pa_chunk_attention_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
     return out
 
 
-def _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_size,
-                    block_scaled=False):
-    """Checks shared by the calls below; returns the device.  block_scaled: E4M3 caches whose
-    scales (and whose types) the caller checks."""
+def _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_size):
+    """Checks shared by the calls below; returns the device."""
     _cuda("q", q)
     dev = torch.cuda.current_device()
     quick = q.get_device() == dev and _dense_on(dev, (out, k_cache, v_cache, *scales, *[t for _, t in ints]))
@@ -570,8 +568,6 @@ def _attention_args(out, q, k_cache, v_cache, scales, ints, num_kv_heads, block_
         _scales(*scales, num_kv_heads)
         if q.dtype not in (torch.float16, torch.bfloat16):
             raise TypeError("q must be float16 or bfloat16 for an E4M3 cache")
-    elif block_scaled:
-        pass
     elif k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
         raise TypeError("q, k_cache and v_cache must share a dtype")
     if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or \
@@ -815,70 +811,100 @@ def pa_decode_prefix_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tens
                    workspace, stream)
 
 
-def _block_scales(k_scales, v_scales, k_cache, quick):
-    """Checks the scales of a block-scaled cache, float32 [N, stride >= Hkv] of dense rows;
-    returns the stride."""
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if not quick:
-            _cuda(name, t)
-        if t.dtype != torch.float32 or t.dim() != 2 or t.shape[0] != k_cache.shape[0] or \
-                t.shape[1] < k_cache.shape[1]:
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _plan_scales(kc, ks, kst, vs, vst):
+    """Checks the scales of a block-scaled cache; returns the floats from row to row."""
+    for name, shape, dtype in (("k_scales", ks, kst), ("v_scales", vs, vst)):
+        if dtype != torch.float32 or len(shape) != 2 or shape[0] != kc[0] or shape[1] < kc[1]:
             raise ValueError(f"{name} must be float32 [num_blocks, at least num_kv_heads]")
-    if k_scales.shape != v_scales.shape:
+    if ks != vs:
         raise ValueError("k_scales and v_scales must have one shape")
-    return k_scales.shape[1]
+    return ks[1]
 
 
-def _paged(fn, out, q, k_cache, v_cache, head_scales, block_scales, block_tables, context_lens,
-           query_start, scale, num_kv_heads, block_size, max_query_len, max_context_len,
-           partition_size, workspace, stream):
-    """Body of the cross attention and of the attention over block-scaled caches."""
-    ints = [("block_tables", block_tables), ("context_lens", context_lens)]
-    if query_start is not None:
-        ints.append(("query_start", query_start))
-    if block_scales:
-        _fp8_cache("k_cache", k_cache)
-        _fp8_cache("v_cache", v_cache)
-        if q.dtype not in (torch.float16, torch.bfloat16):
-            raise TypeError("q must be float16 or bfloat16 for an E4M3 cache")
-    dev = _attention_args(out, q, k_cache, v_cache, head_scales, ints, num_kv_heads, block_size,
-                          bool(block_scales))
-    stride = ()
-    if block_scales:
-        quick = _dense_on(q.get_device(), block_scales)
-        stride = (_block_scales(*block_scales, k_cache, quick),)
-        if not quick:
-            _one_device(q, *block_scales)
-    R, Hq, D = q.shape
-    S = context_lens.shape[0]
-    if context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != S:
-        raise ValueError("block_tables must be [S, W] and context_lens [S]")
-    if query_start is None and S != R:
-        raise ValueError("q must hold one row per sequence")
-    if query_start is not None and query_start.shape != (S + 1,):
-        raise ValueError("query_start must be [S + 1]")
-    W = block_tables.shape[1]
-    if max_context_len is None:
-        max_context_len = W * block_size
-    if partition_size < 0 or workspace is not None:
-        need = 0
-    elif query_start is None:
-        need = _decode_need(S, Hq, D, max_context_len, block_size, partition_size)
+# What a call's shapes and types alone decide is worked out once for each set of them (a step's
+# calls repeat theirs; the checks one by one took a third of a small call's host time).
+
+@functools.lru_cache(maxsize=1024)
+def _paged_plan(kind, chunk, Hkv, B, max_context_len, partition_size, fresh, o, ot, q, qt, kc, kct, vc, vct,
+                bt, btt, cl, clt, qs, qst, ks=None, kst=None, vs=None, vst=None):
+    """Checks shapes and types; returns (out code, q code, rows, query heads, head_dim, sequences,
+    table width, max_context_len, scale stride, workspace bytes)."""
+    if btt != torch.int32 or clt != torch.int32 or (chunk and qst != torch.int32):
+        raise TypeError("block_tables, context_lens and query_start must be int32")
+    if len(q) != 3 or o != q:
+        raise ValueError(f"q and out must be [rows, Hq, D] of one shape, got {tuple(q)}, {tuple(o)}")
+    R, Hq, D = q
+    if len(kc) != 4 or kc != vc or kc[1:] != (Hkv, B, D):
+        raise ValueError(f"k_cache/v_cache must be [N, {Hkv}, {B}, {D}], got {tuple(kc)}, {tuple(vc)}")
+    stride = 0
+    if kind == "half":
+        if kct != qt or vct != qt:
+            raise TypeError("q, k_cache and v_cache must share a dtype")
     else:
-        need = _chunk_need(R, Hq, D, max_context_len, partition_size)
-    workspace, ws_ptr, ws_bytes = _scratch(need, workspace, q, stream)
-    scales = block_scales or head_scales
-    args = [out.data_ptr(), _dtype(out), q.data_ptr()]
+        if kct not in _E4M3 or vct not in _E4M3:
+            raise TypeError("k_cache and v_cache must hold E4M3 codes (torch.float8_e4m3fn or uint8)")
+        if qt not in (torch.float16, torch.bfloat16):
+            raise TypeError("q must be float16 or bfloat16 for an E4M3 cache")
+        if kind == "block":
+            stride = _plan_scales(kc, ks, kst, vs, vst)
+        elif not (kst == vst == torch.float32 and ks == vs == (Hkv,)):
+            raise ValueError("k_scale and v_scale must be float32 [num_kv_heads]")
+    if len(cl) != 1 or len(bt) != 2 or bt[0] != cl[0]:
+        raise ValueError("block_tables must be [S, W] and context_lens [S]")
+    S, W = bt
+    if not chunk and S != R:
+        raise ValueError("q must hold one row per sequence")
+    if chunk and qs != (S + 1,):
+        raise ValueError("query_start must be [S + 1]")
+    for t in (ot, qt):
+        if t not in _DT:
+            raise TypeError(f"unsupported dtype {t}; expected float32, float16 or bfloat16")
+    if max_context_len is None:
+        max_context_len = W * B
+    need = 0
+    if fresh and partition_size >= 0:
+        need = (_chunk_need(R, Hq, D, max_context_len, partition_size) if chunk else
+                _decode_need(S, Hq, D, max_context_len, B, partition_size))
+    return _DT[ot], _DT[qt], R, Hq, D, S, W, int(max_context_len), stride, need
+
+
+def _paged(kind, fn, out, q, k_cache, v_cache, scales, block_tables, context_lens, query_start, scale,
+           num_kv_heads, block_size, max_query_len, max_context_len, partition_size, workspace, stream):
+    """Body of the cross attention and of the attention over block-scaled caches.  kind: "half",
+    "head" (E4M3, a scale for each head) or "block"."""
+    tensors = (out, q, k_cache, v_cache, block_tables, context_lens, *scales) if query_start is None else \
+        (out, q, k_cache, v_cache, block_tables, context_lens, query_start, *scales)
+    dev = torch.cuda.current_device()
+    if not _dense_on(dev, tensors):
+        for t in tensors:
+            _cuda("every tensor", t)
+        _one_device(q, *tensors)
+    qs = context_lens if query_start is None else query_start
+    more = ()
     if scales:
-        args.append(_dtype(q))
-    args += [k_cache.data_ptr(), v_cache.data_ptr()]
-    args += [t.data_ptr() for t in scales] if scales else [_dtype(q)]
-    args += [*stride, k_cache.shape[0], block_tables.data_ptr(), W, context_lens.data_ptr()]
+        ks, vs = scales
+        more = (ks.shape, ks.dtype, vs.shape, vs.dtype)
+    oc, qc, R, Hq, D, S, W, max_context_len, stride, need = _paged_plan(
+        kind, query_start is not None, num_kv_heads, block_size, max_context_len, partition_size,
+        workspace is None, out.shape, out.dtype, q.shape, q.dtype, k_cache.shape, k_cache.dtype,
+        v_cache.shape, v_cache.dtype, block_tables.shape, block_tables.dtype, context_lens.shape,
+        context_lens.dtype, qs.shape, qs.dtype, *more)
+    workspace, ws_ptr, ws_bytes = _scratch(need, workspace, q, stream)
+    tail = (max_context_len, S, Hq, num_kv_heads, D, block_size, float(scale), int(partition_size), ws_ptr,
+            ws_bytes, _stream(stream, dev))
     if query_start is not None:
-        args += [query_start.data_ptr(), R, int(max_query_len)]
-    args += [int(max_context_len), S, Hq, num_kv_heads, D, block_size, float(scale),
-             int(partition_size), ws_ptr, ws_bytes, _stream(stream, dev)]
-    N.check(fn, getattr(N.load(), fn)(*args))
+        tail = (query_start.data_ptr(), R, int(max_query_len), *tail)
+    tail = (k_cache.shape[0], block_tables.data_ptr(), W, context_lens.data_ptr(), *tail)
+    if kind == "half":
+        tail = (k_cache.data_ptr(), v_cache.data_ptr(), qc, *tail)
+    else:
+        if kind == "block":
+            tail = (stride, *tail)
+        tail = (qc, k_cache.data_ptr(), v_cache.data_ptr(), ks.data_ptr(), vs.data_ptr(), *tail)
+    N.check(fn, getattr(N.load(), fn)(out.data_ptr(), oc, q.data_ptr(), *tail))
     return out
 
 
@@ -892,8 +918,8 @@ def pa_cross_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor
     all context_lens[s] tokens of sequence s (an encoder's states, say), however many rows
     there are; a sequence without tokens gives rows of zeros.  max_query_len bounds the rows of
     a sequence; a workspace of pa_chunk_workspace_bytes(...) is allocated when none is given."""
-    return _paged("pa_cross_attention", out, q, k_cache, v_cache, (), (), block_tables, context_lens,
-                  query_start, scale, num_kv_heads, block_size, max_query_len, max_context_len,
+    return _paged("half", "pa_cross_attention", out, q, k_cache, v_cache, (), block_tables, context_lens, query_start,
+                  scale, num_kv_heads, block_size, max_query_len, max_context_len,
                   partition_size, workspace, stream)
 
 
@@ -905,8 +931,8 @@ def pa_cross_attention_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Te
                            partition_size: int = 0, workspace: torch.Tensor | None = None,
                            stream=None) -> torch.Tensor:
     """pa_cross_attention over E4M3 caches with a scale for each kv head (float32 [Hkv])."""
-    return _paged("pa_cross_attention_fp8", out, q, k_cache, v_cache, (k_scale, v_scale), (),
-                  block_tables, context_lens, query_start, scale, num_kv_heads, block_size,
+    return _paged("head", "pa_cross_attention_fp8", out, q, k_cache, v_cache, (k_scale, v_scale), block_tables,
+                  context_lens, query_start, scale, num_kv_heads, block_size,
                   max_query_len, max_context_len, partition_size, workspace, stream)
 
 
@@ -919,8 +945,8 @@ def pa_cross_attention_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: to
                                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """pa_cross_attention over E4M3 caches with a scale for each block and kv head (float32
     [num_blocks, stride >= Hkv])."""
-    return _paged("pa_cross_attention_fp8_block", out, q, k_cache, v_cache, (), (k_scales, v_scales),
-                  block_tables, context_lens, query_start, scale, num_kv_heads, block_size,
+    return _paged("block", "pa_cross_attention_fp8_block", out, q, k_cache, v_cache, (k_scales, v_scales), block_tables,
+                  context_lens, query_start, scale, num_kv_heads, block_size,
                   max_query_len, max_context_len, partition_size, workspace, stream)
 
 
@@ -932,8 +958,8 @@ def pa_decode_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tenso
                         stream=None) -> torch.Tensor:
     """pa_decode_fp8 over E4M3 caches with a scale for each block and kv head (float32
     [num_blocks, stride >= Hkv]), as pa_append_fp8_block writes them."""
-    return _paged("pa_decode_fp8_block", out, q, k_cache, v_cache, (), (k_scales, v_scales),
-                  block_tables, context_lens, None, scale, num_kv_heads, block_size, None,
+    return _paged("block", "pa_decode_fp8_block", out, q, k_cache, v_cache, (k_scales, v_scales), block_tables,
+                  context_lens, None, scale, num_kv_heads, block_size, None,
                   max_context_len, partition_size, workspace, stream)
 
 
@@ -945,69 +971,86 @@ def pa_chunk_attention_fp8_block(out: torch.Tensor, q: torch.Tensor, k_cache: to
                                  max_context_len: int | None = None, partition_size: int = 0,
                                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """pa_chunk_attention_fp8 over E4M3 caches with a scale for each block and kv head."""
-    return _paged("pa_chunk_attention_fp8_block", out, q, k_cache, v_cache, (), (k_scales, v_scales),
-                  block_tables, context_lens, query_start, scale, num_kv_heads, block_size,
+    return _paged("block", "pa_chunk_attention_fp8_block", out, q, k_cache, v_cache, (k_scales, v_scales), block_tables,
+                  context_lens, query_start, scale, num_kv_heads, block_size,
                   max_query_len, max_context_len, partition_size, workspace, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def _append_plan(k, k_st, dt, v, v_st, vt, kc, kct, vc, vct, ks, kst, vs, vst, bt, btt, cl, clt, qs, qst, pos, post,
+                 q=None, q_st=None, qt=None, o=None, o_st=None, ot=None):
+    """Checks shapes and types; returns (dtype code, query heads, sequences, table width, scale
+    stride, token strides of k, v, q and q_out)."""
+    strides = []
+    for name, shape, st in (("k", k, k_st), ("v", v, v_st), ("q", q, q_st), ("q_out", o, o_st)):
+        if shape is not None:
+            if len(shape) != 3:
+                raise ValueError(f"{name} must be [T, H, D]")
+            if shape[0] and ((st[2] != 1 and shape[2] > 1) or (shape[1] > 1 and st[1] != shape[2])):
+                raise ValueError(f"{name} must have dense rows [H, D]")
+            strides.append(st[0] if shape[0] > 1 else shape[1] * shape[2])
+    T, Hkv, D = k
+    if not btt == clt == qst == post == torch.int32:
+        raise TypeError("block_tables, context_lens, query_start and positions must be int32")
+    if v != (T, Hkv, D) or vt != dt:
+        raise ValueError("k and v must be [T, Hkv, D] of one shape and dtype")
+    if q is not None:
+        if o != q or (q[0], q[2]) != (T, D):
+            raise ValueError("q and q_out must be [T, Hq, D]")
+        if not qt == ot == dt:
+            raise TypeError("q, q_out, k and v must share a dtype")
+    if kct not in _E4M3 or vct not in _E4M3:
+        raise TypeError("k_cache and v_cache must hold E4M3 codes (torch.float8_e4m3fn or uint8)")
+    if len(kc) != 4 or kc != vc or (kc[1], kc[3]) != (Hkv, D):
+        raise ValueError(f"caches must be [N, {Hkv}, B, {D}]")
+    stride = _plan_scales(kc, ks, kst, vs, vst)
+    if len(cl) != 1 or len(bt) != 2 or bt[0] != cl[0] or qs != (cl[0] + 1,):
+        raise ValueError("block_tables must be [S, W], context_lens [S] and query_start [S + 1]")
+    if pos != (T,):
+        raise ValueError("positions must be [T]")
+    if dt not in _DT:
+        raise TypeError(f"unsupported dtype {dt}; expected float32, float16 or bfloat16")
+    return _DT[dt], Hkv if q is None else q[1], bt[0], bt[1], stride, strides
 
 
 def _append(fn, q_out, q, k, v, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
             query_start, positions, inv_freq, interleaved, magnitude, max_query_len, stream):
-    rows = [("k", k), ("v", v)] if q is None else [("q_out", q_out), ("q", q), ("k", k), ("v", v)]
-    strides = [_rows(name, t) for name, t in rows]
-    ints = [("block_tables", block_tables), ("context_lens", context_lens),
-            ("query_start", query_start)]
+    rows, more = (k, v), ()
+    if q is not None:
+        rows = (k, v, q, q_out)
+        more = (q.shape, q.stride(), q.dtype, q_out.shape, q_out.stride(), q_out.dtype)
+    dense = (k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, query_start)
     if positions is not None:
-        ints.append(("positions", positions))
+        dense += (positions,)
     dev = torch.cuda.current_device()
-    quick = _dense_on(dev, (k_cache, v_cache, k_scales, v_scales, *[t for _, t in ints])) and \
-        all(t.get_device() == dev for _, t in rows)
-    if not quick:
-        for name, t in ints:
-            _cuda(name, t)
-    for name, t in ints:
-        if t.dtype != torch.int32:
-            raise TypeError(f"{name} must be int32")
-    T, Hkv, D = k.shape
-    if v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError("k and v must be [T, Hkv, D] of one shape and dtype")
-    Hq = Hkv
-    if q is not None:
-        Hq = q.shape[1]
-        if q_out.shape != q.shape or (q.shape[0], q.shape[2]) != (T, D):
-            raise ValueError("q and q_out must be [T, Hq, D]")
-        if not q.dtype == q_out.dtype == k.dtype:
-            raise TypeError("q, q_out, k and v must share a dtype")
-    _fp8_cache("k_cache", k_cache)
-    _fp8_cache("v_cache", v_cache)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or \
-            (k_cache.shape[1], k_cache.shape[3]) != (Hkv, D):
-        raise ValueError(f"caches must be [N, {Hkv}, B, {D}]")
-    stride = _block_scales(k_scales, v_scales, k_cache, quick)
-    S = context_lens.shape[0]
-    if context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != S or \
-            query_start.shape != (S + 1,):
-        raise ValueError("block_tables must be [S, W], context_lens [S] and query_start [S + 1]")
-    if positions is not None and positions.shape != (T,):
-        raise ValueError("positions must be [T]")
-    if not quick:
-        _one_device(k, v, k_cache, v_cache, k_scales, v_scales, *[t for _, t in rows],
-                    *[t for _, t in ints])
-    if max_query_len is None:
-        max_query_len = T
-    args = []
-    for (_, t), st in zip(rows, strides):
-        args += [t.data_ptr(), st]
-    args += [_dtype(k), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
-             v_scales.data_ptr(), stride, k_cache.shape[0], block_tables.data_ptr(),
-             block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr()]
-    if q is not None:
-        args.append(0 if positions is None else positions.data_ptr())
-    args += [T, int(max_query_len), S] + ([Hq] if q is not None else []) + [Hkv, D, k_cache.shape[2]]
-    if q is not None:
+    if not (_dense_on(dev, dense) and all([isinstance(t, torch.Tensor) and t.get_device() == dev for t in rows])):
+        for t in dense:
+            _cuda("every cache, scale and index tensor", t)
+        for t in rows:
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise ValueError("q_out, q, k and v must be CUDA tensors")
+        _one_device(k, *rows, *dense)
+    pos_shape, pos_dtype = (k.shape[:1], torch.int32) if positions is None else (positions.shape, positions.dtype)
+    code, Hq, S, W, stride, st = _append_plan(
+        k.shape, k.stride(), k.dtype, v.shape, v.stride(), v.dtype, k_cache.shape, k_cache.dtype, v_cache.shape, v_cache.dtype,
+        k_scales.shape, k_scales.dtype, v_scales.shape, v_scales.dtype, block_tables.shape,
+        block_tables.dtype, context_lens.shape, context_lens.dtype, query_start.shape, query_start.dtype,
+        pos_shape, pos_dtype, *more)
+    T = k.shape[0]
+    blocks, Hkv, B, D = k_cache.shape
+    max_query_len = T if max_query_len is None else int(max_query_len)
+    head = () if q is None else (q_out.data_ptr(), st[3], q.data_ptr(), st[2])
+    args = (*head, k.data_ptr(), st[0], v.data_ptr(), st[1], code, k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), stride, blocks, block_tables.data_ptr(), W,
+            context_lens.data_ptr(), query_start.data_ptr())
+    if q is None:
+        args += (T, max_query_len, S, Hkv, D, B)
+    else:
         freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
         if freq.ndim != 1:
             raise ValueError("inv_freq must be a host sequence of rotary_dim / 2 numbers")
-        args += [freq.tobytes(), 2 * freq.size, int(bool(interleaved)), float(magnitude)]
+        args += (0 if positions is None else positions.data_ptr(), T, max_query_len, S, Hq, Hkv, D, B,
+                 freq.tobytes(), 2 * freq.size, int(bool(interleaved)), float(magnitude))
     N.check(fn, getattr(N.load(), fn)(*args, _stream(stream, dev)))
 
 
