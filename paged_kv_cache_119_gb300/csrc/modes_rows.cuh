@@ -13,8 +13,11 @@ namespace pa {
 template <typename T, typename TK, int D, int BS, int NH, int MODE>
 struct RowsMode {
     static constexpr int kBPT = mma_blocks_per_tile<TK, D, BS>();
-    // a row kernel's 32-token tiles: four stages (64 KB over 16-bit caches at head_dim 128)
-    static constexpr int kStages = NH <= 8 ? MmaStages<TK, D, BS * kBPT>::value : kDecodeConsumerWarps;
+    // a row kernel's 32-token tiles: 64 KB of stages at head_dim 128, so eight over E4M3 caches
+    // (with four, a warp of 16 rows had one stage, and waited a load's latency a tile: 32 sequences of
+    // 4 new tokens over 8192, 4 heads a kv head, blocks of 32, 144 against 105 us)
+    static constexpr int kStages = NH <= 8 ? MmaStages<TK, D, BS * kBPT>::value
+                                           : kDecodeConsumerWarps * (sizeof(TK) == 1 ? 2 : 1);
     static constexpr int kThreads = kDecodeThreads;
     static constexpr int smem_bytes()
     {
