@@ -514,8 +514,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
             return wanted(it) ? __ldg(bt_row + tile_token(it) / BS + lane) : -1;
         };
         int cur = -1, next = -1;
-        float4 sc{};
-        RawScale next_sc{};
+        RawScale sc{}, next_sc{};
         if constexpr (kBlk) {
             cur = entry(0);
             next = entry(1);
@@ -535,7 +534,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 nb = __popc(__ballot_sync(kFullMask, want));
                 cur = next;
                 next = entry(it + 2);
-                sc = block_scale(next_sc);       // (behind the wait for the slot: 1.22 us a tile, 1.01 here)
+                sc = next_sc;
                 next_sc = load_scale(p, cur, kvh);
             } else if constexpr (kIsMod) {        // only blocks that hold a seen token
                 want = want && any_seen(seen, (b0 + lane) * BS, min((b0 + lane) * BS + BS, t1));
@@ -564,16 +563,13 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
             if (!__shfl_sync(kFullMask, ok, 0))
                 break;
             if constexpr (kBlk) {
-                // the slot is free: its scales, then the announcement that carries them
-                if (lane < BPT)
-                    raw_scale[st * 4 + lane] = sc;
-                __syncwarp();
+                // the copies go out first; the arrival follows with the scales (below)
                 if (lane == 0) {
                     const int nvalid = __popc(vmask);
                     pok[st] = nvalid == nb ? 1 : 0;
                     if (nvalid != nb)
                         atomicOr(p.err, PA_DEVERR_BLOCK_ID);
-                    mbar_arrive_expect_tx(&pfull[st], (uint32_t)nvalid * 2u * BS * 128u);
+                    mbar_expect_tx(&pfull[st], (uint32_t)nvalid * 2u * BS * 128u);
                 }
                 __syncwarp();
             }
@@ -591,6 +587,14 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     tma_load_3d(kdst + Sm::kKBytes + h * Sm::kKVHalf, &tv, 64 * h, 0, z, &full[st],
                                 policy);
                 }
+            }
+            if constexpr (kBlk) {
+                // (scales before the copies: 1.22 us a tile, the copies waiting for them)
+                if (lane < BPT)
+                    raw_scale[st * 4 + lane] = block_scale(sc);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&pfull[st]);
             }
             issued = it + 1;
         }
@@ -811,8 +815,6 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         const int low = kIsMod && p.mods.window > 0 ? max(0, pos - p.mods.window + 1) : 0;
         const float slope = kSlope ? base2_slope(p.mods.slopes[kvh * G + g]) : 0.f;
         const int64_t qrow = (int64_t)(qs0 + j0 + tok) * p.num_q_heads + (int64_t)kvh * G + g;
-        // 16-byte pieces of a row of 16-bit elements, and the rows a warp moves at a time
-        constexpr int CPR = D / 8, RPW = 32 / CPR;
         // scores are used as s * sl2 with sl2 > 0: a negative scale flips the sign of q
         // (exact), a zero scale makes q zero (every score 0); over E4M3 caches the K scale
         // of the kv head joins the softmax scale (kBlock: the one of a block, tile by tile)
@@ -820,23 +822,28 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
         const uint32_t qflip = sl2_raw < 0.f ? 0x80008000u : 0u;
         const bool qzero = sl2_raw == 0.f;
         float sl2 = qzero ? 1.f : fabsf(sl2_raw);
+        // kWideIO: a row is CPR lanes of 16 bytes wide; rows of q and out (all heads) from the CTA's
+        // first one, -1: none
+        constexpr int CPR = D / 8, RPW = 32 / CPR;
+        const int64_t row_base = (int64_t)(qs0 + j0) * p.num_q_heads + (int64_t)kvh * G;
+        const int my_row = row_valid ? tok * p.num_q_heads + g : -1;
         {
             // Q rows into the 128-byte-swizzled operand layout; rows past the chunk are 0.  The
             // lanes of a warp read whole rows (CPR lanes of 16 bytes each), not one row a lane:
             // with the epilogue's stores, which go the same way, one row a lane cost a CTA 3 to 5 us
-            // at head_dim 128 (256 rows over 64 tokens 12 against 9.5 us, 4 x 512 tokens of 8192, 64/8
-            // heads, 525 against 510).  Capped and biased scores keep a row a lane: their loops
+            // at head_dim 128 (256 rows over 64 tokens 12.2 against 8.7 us, 4 x 512 tokens of 8192, 64/8
+            // heads, bf16, 526 against 517).  Capped and biased scores keep a row a lane: their loops
             // lose more to the registers (568 against 608 us, capped, f16).
             if constexpr (kWideIO) {
                 unsigned char* qdst = smem + Sm::kQOff + q * Sm::kQTile + 32 * wq * 128;
                 constexpr bool kToF16 = kF8 && DType<T>::id == PA_BF16;
-                uint4 v[CPR];
+                const uint4* src =
+                    reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + row_base * D) + lane % CPR;
+                uint4 qv[CPR];
 #pragma unroll
                 for (int i = 0; i < CPR; ++i) {
-                    const int64_t row = __shfl_sync(kFullMask, row_valid && !qzero ? qrow : -1, i * RPW + lane / CPR);
-                    v[i] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + row * D) +
-                                            lane % CPR)
-                                    : make_uint4(0u, 0u, 0u, 0u);
+                    const int row = __shfl_sync(kFullMask, qzero ? -1 : my_row, i * RPW + lane / CPR);
+                    qv[i] = row >= 0 ? __ldg(src + (int64_t)row * CPR) : make_uint4(0u, 0u, 0u, 0u);
                 }
 #pragma unroll
                 for (int i = 0; i < CPR; ++i) {
@@ -845,15 +852,18 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                         // a bf16 row becomes f16 operands: a power of two 2^-e puts its largest
                         // |q| in [2^14, 2^15), so the 8-bit mantissas convert exactly; 2^e goes
                         // into the row's score scale
-                        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
                         float amax = 0.f;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)),
                                                      fabsf(__uint_as_float(w[j] & 0xffff0000u))));
-#pragma unroll
-                        for (int m = CPR / 2; m >= 1; m >>= 1)
-                            amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, m));
+                        // over the lanes of either row (magnitudes order as their bits do)
+                        static_assert(!kToF16 || RPW == 2, "two rows a step");
+                        const unsigned bits = __float_as_uint(amax);
+                        const unsigned lo = __reduce_max_sync(kFullMask, lane < 16 ? bits : 0u);
+                        const unsigned hi = __reduce_max_sync(kFullMask, lane < 16 ? 0u : bits);
+                        amax = __uint_as_float(lane < 16 ? lo : hi);
                         const int ex = (__float_as_int(amax) >> 23) & 0xff;   // biased exponent
                         // amax in [2^(ex-127), 2^(ex-126)): scale by 2^(141 - ex); rows of zeros,
                         // tiny rows and a NaN / infinite row keep the scale 1
@@ -868,14 +878,14 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                                                                 __uint_as_float(w[j] & 0xffff0000u) * down);
                             w[j] = *reinterpret_cast<const uint32_t*>(&h);
                         }
-                        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        qv[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    v[i].x ^= qflip;
-                    v[i].y ^= qflip;
-                    v[i].z ^= qflip;
-                    v[i].w ^= qflip;
+                    qv[i].x ^= qflip;
+                    qv[i].y ^= qflip;
+                    qv[i].z ^= qflip;
+                    qv[i].w ^= qflip;
                     *reinterpret_cast<uint4*>(qdst + (c / 8) * Sm::kQHalf + r32 * 128 + (((c & 7) ^ (r32 & 7)) << 4)) =
-                        v[i];
+                        qv[i];
                 }
             } else {
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
@@ -1227,7 +1237,6 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 // Rows go out through this warp's 32 rows of the query tile (no product reads them any
                 // more), so that its lanes store whole rows; piece c of a row at c ^ (row & 7).
                 unsigned char* stage = smem + Sm::kQOff + q * Sm::kQTile + 32 * wq * 128;
-                const int64_t orow = row_valid ? qrow : -1;
                 auto piece = [&](int r32, int c) -> uint4* {
                     return reinterpret_cast<uint4*>(stage + (c / 8) * Sm::kQHalf + r32 * 128 +
                                                     (((c & 7) ^ (r32 & 7)) << 4));
@@ -1258,10 +1267,10 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int64_t row = __shfl_sync(kFullMask, orow, 4 * i + lane / 8);
+                        const int row = __shfl_sync(kFullMask, my_row, 4 * i + lane / 8);
                         if (row >= 0) {
-                            float* dst = split ? p.part_o + (row * p.max_parts + part) * D
-                                               : static_cast<float*>(p.out) + row * D;
+                            float* dst = split ? p.part_o + ((row_base + row) * p.max_parts + part) * D
+                                               : static_cast<float*>(p.out) + (row_base + row) * D;
                             *reinterpret_cast<uint4*>(dst + 32 * c4 + 4 * (lane % 8)) = *piece(4 * i + lane / 8, lane % 8);
                         }
                     }
@@ -1272,10 +1281,10 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
 #pragma unroll
                     for (int i = 0; i < CPR; ++i) {
                         const int r32 = i * RPW + lane / CPR;
-                        const int64_t row = __shfl_sync(kFullMask, orow, r32);
+                        const int row = __shfl_sync(kFullMask, my_row, r32);
                         if (row >= 0)
-                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + 8 * (lane % CPR)) =
-                                *piece(r32, lane % CPR);
+                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (row_base + row) * D +
+                                                      8 * (lane % CPR)) = *piece(r32, lane % CPR);
                     }
                 }
                 if (split && row_valid) {
