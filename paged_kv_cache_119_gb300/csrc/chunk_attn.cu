@@ -14,7 +14,7 @@ struct ChunkVariant {
     static constexpr int kStages = F8 ? 3 : ChunkStages<D>::value;
     static constexpr int kRaw = F8 ? 4 : 0;
     static constexpr int kThreads =
-        (F8 || std::is_same_v<T, __nv_bfloat16>) ? kChunkThreadsConv : kChunkThreads;
+        chunk_threads<T, kRaw, kPlain>();
     using Sm = ChunkSmem<D, kStages, kRaw>;
     static constexpr auto kernel() { return chunk_attn_kernel<T, D, BS, kStages, kRaw>; }
     static cudaError_t configure()

@@ -81,23 +81,26 @@
 
 namespace pa {
 
-constexpr int kChunkQTiles = 2;      // 128-row query tiles per CTA
 constexpr int kChunkRows = 128;      // M of the tensor-core tile
 constexpr int kChunkTileTok = 64;    // tokens per K/V tile (N of the score product)
-constexpr int kChunkSoftmaxWarps = 4 * kChunkQTiles;
-// warps: 0 producer, 1 tensor-memory allocator + MMA issuer of query tile 0, 2-9
-// softmax, 10 MMA issuer of query tile 1; over E4M3 and bf16 caches, 11-14 convert
-// tiles to f16
-constexpr int kChunkThreads = 64 + 32 * kChunkSoftmaxWarps + 32;
-constexpr int kChunkConvWarps = 4;
-constexpr int kChunkThreadsConv = kChunkThreads + 32 * kChunkConvWarps;
+// A CTA of QT (1 or 2) 128-row query tiles.  Warps: 0 producer, 1 tensor-memory allocator + MMA
+// issuer of query tile 0, then 4 QT softmax warps, the issuer of query tile 1 if there is one,
+// and over E4M3 and bf16 caches (or to zero V rows) the warps that convert tiles to f16.
+template <int QT>
+struct ChunkWarps {
+    static_assert(QT == 1 || QT == 2, "one or two query tiles");
+    static constexpr int kSoftmax = 4 * QT;
+    static constexpr int kIssuer1 = 2 + kSoftmax;
+    static constexpr int kConv0 = 1 + QT + kSoftmax;           // the first converter
+    static constexpr int kConv = 2 * QT;
+};
 // P.V takes P as 2^kChunkPExp p: p <= 2^8 (the lazy rescale), so 2^15 at most in f16
 constexpr float kChunkPExp = 7.f;
 static_assert(kChunkPExp == 7.f, "the partial rows of a shared prefix take 2^-7 off again");
 
 // NRAW > 0 (E4M3 caches): a ring of NRAW raw one-byte K + V tiles that the converter
 // warps turn into the 16-bit tiles of the NST-stage ring.
-template <int D, int NST, int NRAW = 0>
+template <int D, int NST, int NRAW = 0, int QT = 2>
 struct ChunkSmem {
     static constexpr int kHalves = D / 64;                       // 128-byte column groups
     static constexpr int kQHalf = kChunkRows * 128;              // 16 KB
@@ -106,7 +109,7 @@ struct ChunkSmem {
     static constexpr int kKBytes = kHalves * kKVHalf;
     static constexpr int kStageBytes = 2 * kKBytes;              // K then V
     static constexpr int kQOff = 0;
-    static constexpr int kStageOff = kQOff + kChunkQTiles * kQTile;
+    static constexpr int kStageOff = kQOff + QT * kQTile;
     static constexpr int kRawTile = kChunkTileTok * D;           // one E4M3 K (or V) tile
     static constexpr int kRawStage = 2 * kRawTile;
     static constexpr int kRawOff = kStageOff + NST * kStageBytes;
@@ -122,9 +125,9 @@ struct ChunkSmem {
     static constexpr int kScaleOff = (kBytes + 15) / 16 * 16;
     static constexpr int kAllocBlock = kScaleOff + (NST + NRAW) * 64 + 1024;
     // tensor memory: O of query tile q at column 128 q, its two S/P buffers at
-    // 256 + 128 q and 256 + 128 q + 64 (P: f16 pairs in the first 32 columns)
-    static constexpr int kTmemCols = 512;
-    static constexpr int kSCol = 256;
+    // 128 (QT + q) and 64 on (P: f16 pairs in the first 32 columns)
+    static constexpr int kTmemCols = 256 * QT;
+    static constexpr int kSCol = 128 * QT;
     static_assert(D <= 128, "O must fit in 128 columns");
     static_assert(NRAW == 0 || D == 128, "E4M3 tiles need 128-byte rows");
     static_assert(kRawTile % 1024 == 0, "swizzle atoms need 1 KB alignment");
@@ -287,8 +290,7 @@ __device__ __forceinline__ void cap_row(float (&s)[kChunkTileTok], float mul, co
     }
 }
 
-// grid = (partitions, num_kv_heads * m_tiles, num_seqs); kChunkThreads threads over
-// f16 caches, kChunkThreadsConv over E4M3 (NRAW > 0) and bf16 caches.  T: query /
+// grid = (partitions, num_kv_heads * m_tiles, num_seqs); chunk_threads() threads.  T: query /
 // native output type.  Over E4M3 caches (value = code * per-kv-head scale) the
 // tensor-core operands are f16: the codes convert exactly, a bf16 query row is scaled
 // into f16 range by a power of two (exact), and the scales fold into the scores and
@@ -298,20 +300,25 @@ __device__ __forceinline__ void cap_row(float (&s)[kChunkTileTok], float mul, co
 // row sees; kPrefix, the rows of a group of sequences (query_start = the group's first one)
 // over the tokens they share, partial rows only; kBlock, kMod over an E4M3 cache with a scale for
 // each block (four or two in a tile).
-template <typename T, int NRAW, int MODE>
+// QT: query tiles of a CTA.  Two, but one for kMod over 16-bit caches at head_dim 64, where two
+// such CTAs fit on an SM: what a CTA does once (set-up, reading q, the first tile's latency,
+// writing out: 5 us beside 0.8 a tile) then goes on under the other's tiles, and a unit is 128 rows.
+template <typename T, int NRAW, int MODE, int QT = 2>
 constexpr int chunk_threads()
 {
-    return (NRAW > 0 || (std::is_same_v<T, __nv_bfloat16> && MODE != kPrefix) || is_mod(MODE))
-               ? kChunkThreadsConv
-               : kChunkThreads;
+    const bool conv =
+        NRAW > 0 || (std::is_same_v<T, __nv_bfloat16> && MODE != kPrefix) || is_mod(MODE);
+    return 32 * (ChunkWarps<QT>::kConv0 + (conv ? ChunkWarps<QT>::kConv : 0));
 }
 
-template <typename T, int D, int BS, int NST, int NRAW = 0, int MODE = kPlain>
-__global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
+template <typename T, int D, int BS, int NST, int NRAW = 0, int MODE = kPlain, int QT = 2>
+__global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE, QT>(), 3 - QT)
     chunk_attn_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv)
 {
-    using Sm = ChunkSmem<D, NST, NRAW>;
+    using Sm = ChunkSmem<D, NST, NRAW, QT>;
+    using Warps = ChunkWarps<QT>;
+    constexpr int kConvThreads = 32 * Warps::kConv;
     constexpr bool kF8 = NRAW > 0;
     constexpr bool kIsMod = is_mod(MODE), kCap = has_cap(MODE), kSlope = has_slope(MODE);
     constexpr bool kBlk = is_block(MODE);
@@ -454,29 +461,29 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int s = 0; s < NST; ++s) {
-            mbar_init(&full[s], kF8 ? kChunkConvWarps : 1);   // converters, or the TMA
-            mbar_init(&empty[s], kChunkQTiles);          // one commit per issuer
+            mbar_init(&full[s], kF8 ? Warps::kConv : 1);   // converters, or the TMA
+            mbar_init(&empty[s], QT);          // one commit per issuer
         }
 #pragma unroll
         for (int s = 0; s < NRAW; ++s) {
             mbar_init(&raw_full[s], 1);
-            mbar_init(&raw_empty[s], kChunkConvWarps);
+            mbar_init(&raw_empty[s], Warps::kConv);
         }
 #pragma unroll
         for (int s = 0; s < NST; ++s)
-            mbar_init(&vconv[s], kChunkConvWarps);
+            mbar_init(&vconv[s], Warps::kConv);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
         }
 #pragma unroll
-        for (int q = 0; q < kChunkQTiles; ++q) {
+        for (int q = 0; q < QT; ++q) {
             mbar_init(&pv_done[q], 1);
             mbar_init(&mma_done[q], 1);
         }
-        mbar_init(q_full, kChunkSoftmaxWarps);
-        mbar_init(v_zero, kChunkSoftmaxWarps);
+        mbar_init(q_full, Warps::kSoftmax);
+        mbar_init(v_zero, Warps::kSoftmax);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -603,13 +610,13 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
             for (int it = max(0, issued - NP); it < issued; ++it)
                 mbar_wait(&pfull[it % NP], (it / NP) & 1);
         __syncwarp();
-    } else if ((kF8 || kVHand) && warp > 2 + kChunkSoftmaxWarps) {
+    } else if ((kF8 || kVHand) && warp >= Warps::kConv0) {
         // ------------------------------------------------ E4M3 -> f16 tile conversion
         // A raw tile row is 128 codes in 128-byte-swizzled order (16-byte chunk c of row
         // t at c ^ (t & 7)); the f16 tile is two 64-dim halves of 128-byte rows in the
         // same swizzle.  Each (token, 16-code chunk) item becomes two f16 chunks.
         if constexpr (kF8) {
-            const int ct = threadIdx.x - kChunkThreads;      // 0 .. 32 * kChunkConvWarps - 1
+            const int ct = threadIdx.x - 32 * Warps::kConv0;  // 0 .. kConvThreads - 1
             constexpr int kItems = NT * 8;                   // per K (or V) tile
             for (int it = 0; it < ntiles; ++it) {
                 const int r = it % NRAW;
@@ -629,7 +636,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll 4
-                    for (int item = ct; item < kItems; item += 32 * kChunkConvWarps) {
+                    for (int item = ct; item < kItems; item += kConvThreads) {
                         const int t = item >> 3;
                         const int c = item & 7;
                         uint4 w = *reinterpret_cast<const uint4*>(
@@ -648,11 +655,11 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     }
                 }
                 fence_proxy_async_smem();                    // f16 tiles -> tensor core
-                if (kBlk && warp == 3 + kChunkSoftmaxWarps && lane < BPT)
+                if (kBlk && warp == Warps::kConv0 && lane < BPT)
                     stage_scale[st * 4 + lane] = raw_scale[r * 4 + lane];
                 __syncwarp();
                 if (lane == 0) {
-                    if (warp == 3 + kChunkSoftmaxWarps)
+                    if (warp == Warps::kConv0)
                         stage_ok[st] = raw_ok[r];
                     mbar_arrive(&full[st]);
                     mbar_arrive(&raw_empty[r]);
@@ -665,10 +672,10 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
             // only after both P.V of the tile, which wait for this hand-over.  A value
             // without an f16 value becomes infinite (or stays NaN); the epilogue reports
             // the rows it reaches.
-            const int ct = threadIdx.x - kChunkThreads;      // 0 .. 32 * kChunkConvWarps - 1
+            const int ct = threadIdx.x - 32 * Warps::kConv0;  // 0 .. kConvThreads - 1
             constexpr int kItems = NT * 8 * Sm::kHalves;     // 16-byte chunks of a V tile
-            constexpr int kPer = kItems / (32 * kChunkConvWarps);
-            static_assert(kItems % (32 * kChunkConvWarps) == 0, "whole chunks per thread");
+            constexpr int kPer = kItems / kConvThreads;
+            static_assert(kItems % kConvThreads == 0, "whole chunks per thread");
             for (int it = 0; it < ntiles; ++it) {
                 const int st = it % NST;
                 if (!mbar_wait(&full[st], (it / NST) & 1)) {
@@ -682,7 +689,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 unsigned char* vt = smem + Sm::kStageOff + st * Sm::kStageBytes + Sm::kKBytes;
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
-                    const int item = ct + i * 32 * kChunkConvWarps;
+                    const int item = ct + i * kConvThreads;
                     const int w = item % (NT * 8);           // chunk within a 64-dim half
                     uint4* chunk = reinterpret_cast<uint4*>(vt + (item / (NT * 8)) * Sm::kKVHalf +
                                                             w * 16);
@@ -708,7 +715,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
             }
         } else if constexpr (kVHand) {
             // f16 V needs no conversion: only the rows of tokens no row sees become 0
-            const int ct = threadIdx.x - kChunkThreads;
+            const int ct = threadIdx.x - 32 * Warps::kConv0;
             for (int it = 0; it < ntiles; ++it) {
                 const int st = it % NST;
                 if (!mbar_wait(&full[st], (it / NST) & 1)) {
@@ -719,7 +726,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 const int tb = tile_token(it);
                 if (!tile_seen(seen, tb, NT)) {
                     unsigned char* vt = smem + Sm::kStageOff + st * Sm::kStageBytes + Sm::kKBytes;
-                    for (int item = ct; item < NT * 8 * Sm::kHalves; item += 32 * kChunkConvWarps) {
+                    for (int item = ct; item < NT * 8 * Sm::kHalves; item += kConvThreads) {
                         const int w = item % (NT * 8);
                         if (!is_seen(seen, tb + (w >> 3)))
                             *reinterpret_cast<uint4*>(vt + (item / (NT * 8)) * Sm::kKVHalf + w * 16) =
@@ -732,7 +739,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                     mbar_arrive(&vconv[st]);
             }
         }
-    } else if (warp == 1 || warp == 2 + kChunkSoftmaxWarps) {
+    } else if (warp == 1 || (QT == 2 && warp == Warps::kIssuer1)) {
         // ------------------------------------------- MMA issue, one query tile per warp
         const int q = warp == 1 ? 0 : 1;
         if (lane == 0) {
@@ -1197,7 +1204,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE>(), 1)
                 const int rows = NT - v0;
                 unsigned char* vbase = smem + Sm::kStageOff + st * Sm::kStageBytes + Sm::kKBytes;
                 for (int idx = threadIdx.x - 64; idx < Sm::kHalves * rows * 8;
-                     idx += 32 * kChunkSoftmaxWarps) {
+                     idx += 32 * Warps::kSoftmax) {
                     const int h = idx / (rows * 8);
                     const int w = idx - h * rows * 8;
                     *reinterpret_cast<uint4*>(vbase + h * Sm::kKVHalf + (v0 + w / 8) * 128 +

@@ -142,7 +142,8 @@ Plan plan_heads(const Shape& s)
 // Kernel of a pass with `tokens` x group rows per kv head: at most few_rows of them (and
 // E4M3 at head_dim 64, whose tiles no tensor map reaches) on a decode kernel's row mode,
 // more on the tcgen05 chunk kernel.
-Plan plan_rows(const Shape& s, int64_t tokens, int few_rows)
+// cta_rows: rows of a CTA of the chunk kernel.
+Plan plan_rows(const Shape& s, int64_t tokens, int few_rows, int cta_rows = kChunkCtaRows)
 {
     Plan pl{};
     const int64_t rows = tokens * s.group();
@@ -154,7 +155,7 @@ Plan plan_rows(const Shape& s, int64_t tokens, int few_rows)
         return pl;
     }
     pl.family = Family::kChunk;
-    const int tt = kChunkCtaRows / s.group();    // tokens per CTA
+    const int tt = cta_rows / s.group();         // tokens per CTA
     pl.per = tt * s.group();
     pl.chunks = (int)std::min<int64_t>((tokens + tt - 1) / tt, INT32_MAX);
     pl.tile = 64;
@@ -328,14 +329,18 @@ int mod_impl(Call call, void* out, pa_dtype out_dtype, const void* q, const Shap
     // (32 rows of a chunk on a decode kernel's row mode against the chunk kernel, 32 sequences,
     // capped: 35.1 against 49.3 us over a window of 1024, 198 against 278 over 8192 tokens; 64 rows
     // 60.2 against 51.4 and 377 against 280)
-    Plan pl = decode ? plan_heads(s) : plan_rows(s, qlen, kChunkRowsMax);
-    AttnMode mode = s.block_scales() ? kBlock : kMod;
     const bool cap = softcap > 0.f, slope = alibi_slopes != nullptr;
-    if (s.block_scales())
-        ;                                        // (no cap, no slopes)
-    else if (pl.family == Family::kChunk)
-        mode = cap ? (slope ? kModBoth : kModCap) : (slope ? kModSlope : kMod);
-    else if (pl.family == Family::kRows)
+    // what the chunk kernel would run in
+    const AttnMode chunk_mode = s.block_scales() ? kBlock
+                                : cap            ? (slope ? kModBoth : kModCap)
+                                                 : (slope ? kModSlope : kMod);
+    Plan pl = decode ? plan_heads(s)
+                     : plan_rows(s, qlen, kChunkRowsMax,
+                                 kChunkCtaRows / 2 * chunk_query_tiles(chunk_mode, s.head_dim, s.fp8()));
+    AttnMode mode = s.block_scales() ? kBlock : kMod;
+    if (pl.family == Family::kChunk)
+        mode = chunk_mode;
+    else if (pl.family == Family::kRows && !s.block_scales())
         mode = cap || slope ? kModBoth : kMod;
     const int length =
         (int)std::min<int64_t>(seen_bound(max_context_len, window, max_global_len, qlen, pl.tile), INT32_MAX);

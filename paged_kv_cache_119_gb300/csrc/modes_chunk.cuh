@@ -9,12 +9,13 @@ namespace pa {
 
 template <typename T, int D, int BS, bool F8, int MODE>
 struct ChunkMode {
-    static constexpr int kStages = F8 ? 3 : ChunkStages<D>::value;
+    static constexpr int kQT = chunk_query_tiles(MODE, D, F8);
+    static constexpr int kStages = F8 ? 3 : kQT == 1 ? 5 : ChunkStages<D>::value;
     static constexpr int kRaw = F8 ? 4 : 0;
-    using Sm = ChunkSmem<D, kStages, kRaw>;
-    static constexpr int kThreads = chunk_threads<T, kRaw, MODE>();
+    using Sm = ChunkSmem<D, kStages, kRaw, kQT>;
+    static constexpr int kThreads = chunk_threads<T, kRaw, MODE, kQT>();
     static constexpr int kSmem = is_block(MODE) ? Sm::kAllocBlock : Sm::kAlloc;
-    static constexpr auto kernel() { return chunk_attn_kernel<T, D, BS, kStages, kRaw, MODE>; }
+    static constexpr auto kernel() { return chunk_attn_kernel<T, D, BS, kStages, kRaw, MODE, kQT>; }
     static cudaError_t configure()
     {
         return configure_once(reinterpret_cast<const void*>(kernel()), kSmem);

@@ -317,6 +317,11 @@ cudaError_t kv_tensor_map(CUtensorMap* map, const void* base, int64_t num_blocks
 
 // (query token, query head) rows one chunk-attention CTA serves (two 128-row tiles).
 constexpr int kChunkCtaRows = 256;
+// 128-row query tiles of a CTA of the chunk kernel (chunk_attn.cuh).
+__host__ __device__ constexpr int chunk_query_tiles(int mode, int head_dim, bool fp8)
+{
+    return mode == kMod && head_dim == 64 && !fp8 ? 1 : 2;
+}
 
 // Causal attention of chunks of new query tokens over the paged cache (the
 // tensor-core kernel of chunk_attn.cuh).  Rows of q / out are (query token, query
