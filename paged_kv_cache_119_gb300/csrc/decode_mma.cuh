@@ -165,16 +165,28 @@ __device__ __forceinline__ void convert_e4m3_tile(const unsigned char* src, unsi
     }
 }
 
+// Where the 16-byte chunk of an E4M3 tile's token row lies: lines of 128 bytes, one token of 128
+// codes or two of 64, with 128-byte swizzle (chunk of the line ^ line % 8).
+template <int D>
+__device__ __forceinline__ uint32_t e4m3_at(int row, int chunk)
+{
+    if constexpr (D == 128)
+        return row * 128 + ((chunk ^ (row & 7)) << 4);
+    else
+        return (row >> 1) * 128 + (((((row & 1) << 2) | chunk) ^ ((row >> 1) & 7)) << 4);
+}
+
 // Shared memory of the tensor-core kernel.  16-bit caches: the ring holds the
 // swizzled K and V tiles the tensor-map TMA writes.  E4M3 caches: the ring holds
 // the raw one-byte tiles (1-D bulk copies) and each consumer warp owns a staging
 // pair of 16-bit swizzled tiles, in the same layout, that it converts them into.
-template <typename TK, int D, int BS, int NSTAGE>
+// IN_PLACE: E4M3 tiles at head_dim 64 are read directly too (kBlock).
+template <typename TK, int D, int BS, int NSTAGE, bool IN_PLACE = false>
 struct MmaSmem {
     static constexpr bool kFp8 = sizeof(TK) == 1;
     // E4M3 with head_dim 128: a tile row is 128 bytes, so the raw tile arrives by
     // tensor-map TMA with 128-byte swizzle and fragments are read from it directly
-    static constexpr bool kDirect = kFp8 && D == 128;
+    static constexpr bool kDirect = kFp8 && (D == 128 || IN_PLACE);
     static constexpr int kHalfBytes = BS * 128;                // one 64-dim box: B rows x 128 B
     static constexpr int kTileBytes = (D / 64) * kHalfBytes;   // one 16-bit K (or V) tile
     static constexpr int kScratchBytes =
@@ -203,8 +215,13 @@ struct MmaSmem {
 // Four CTAs per SM (at most 96 registers a thread) keep the 16-bit and block-size-16
 // E4M3 forms resident; the block-size-32 E4M3 form converts wider tiles and runs
 // faster at 128 registers and three CTAs.
-template <typename TK, int BS>
-constexpr int mma_min_blocks() { return (sizeof(TK) == 1 && BS == 32) ? 3 : 4; }
+template <typename TK, int BS, int D = 128, int MODE = kPlain>
+constexpr int mma_min_blocks()
+{
+    if (D == 64 && is_block(MODE))
+        return 4;                                // (three: 92 us against 71, 64 x 4096 tokens, 64/8 heads, blocks of 32)
+    return (sizeof(TK) == 1 && BS == 32) ? 3 : 4;
+}
 
 // T: query / native output type (the mma operand type).  TK: cache element type,
 // T itself (tiles by tensor-map TMA) or __nv_fp8_e4m3 (raw tiles by 1-D bulk copy,
@@ -221,12 +238,12 @@ constexpr int mma_min_blocks() { return (sizeof(TK) == 1 && BS == 32) ? 3 : 4; }
 // over an E4M3 cache with a scale for each block.
 template <typename T, typename TK, int D, int BS, int NH, int NSTAGE, bool CH = false, int BPT = 1,
           int MODE = kPlain>
-__global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>())
+__global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT, D, MODE>())
     decode_mma_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv)
 {
     constexpr int TB = BS * BPT;      // tokens per tile
-    using Sm = MmaSmem<TK, D, TB, NSTAGE>;
+    using Sm = MmaSmem<TK, D, TB, NSTAGE, is_block(MODE)>;
     constexpr bool kFp8 = Sm::kFp8;
     constexpr bool kIsMod = is_mod(MODE), kBlk = is_block(MODE);
     // tensor-core operand type: the query type for 16-bit caches; f16 for E4M3 caches
@@ -468,7 +485,7 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                             for (int b = 0; b < BPT; ++b) {
                                 if (!want(b) || pbn[b] < 0 || (int64_t)pbn[b] >= p.num_blocks)
                                     continue;
-                                unsigned char* bdst = dst + b * (BS * 128);   // rows of block b
+                                unsigned char* bdst = dst + b * (BS * (kFp8 ? D : 128));   // rows of block b
                                 if constexpr (kDirect) {
                                     const int z = pbn[b] * p.num_kv_heads + kvh;
                                     tma_load_3d(bdst, &tk, 0, 0, z, &full[stage], policy);
@@ -683,8 +700,8 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                 const int r0 = 16 * mb + g, r1 = r0 + 8;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    const uint32_t w0 = lds_u32(kbase + r0 * 128 + ((ks ^ (r0 & 7)) << 4) + 4 * c);
-                    const uint32_t w1 = lds_u32(kbase + r1 * 128 + ((ks ^ (r1 & 7)) << 4) + 4 * c);
+                    const uint32_t w0 = lds_u32(kbase + e4m3_at<D>(r0, ks) + 4 * c);
+                    const uint32_t w1 = lds_u32(kbase + e4m3_at<D>(r1, ks) + 4 * c);
                     const uint32_t a[4] = {e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w1),
                                            e4m3x2_to_f16x2(w0 >> 16), e4m3x2_to_f16x2(w1 >> 16)};
                     Mma<TM>::run(s, a, qb[ks][0], qb[ks][1]);
@@ -824,13 +841,10 @@ __global__ void __launch_bounds__(kDecodeThreads, mma_min_blocks<TK, BS * BPT>()
                         const int t0 = 16 * mb + 2 * c;
                         const int chunk = 2 * j + (g >> 2);
                         const int off = 4 * (g & 3);
-                        const uint32_t w0 = lds_u32(vbase + t0 * 128 + ((chunk ^ (t0 & 7)) << 4) + off);
-                        const uint32_t w1 = lds_u32(vbase + (t0 + 1) * 128 +
-                                                    ((chunk ^ ((t0 + 1) & 7)) << 4) + off);
-                        const uint32_t w8 = lds_u32(vbase + (t0 + 8) * 128 +
-                                                    ((chunk ^ ((t0 + 8) & 7)) << 4) + off);
-                        const uint32_t w9 = lds_u32(vbase + (t0 + 9) * 128 +
-                                                    ((chunk ^ ((t0 + 9) & 7)) << 4) + off);
+                        const uint32_t w0 = lds_u32(vbase + e4m3_at<D>(t0, chunk) + off);
+                        const uint32_t w1 = lds_u32(vbase + e4m3_at<D>(t0 + 1, chunk) + off);
+                        const uint32_t w8 = lds_u32(vbase + e4m3_at<D>(t0 + 8, chunk) + off);
+                        const uint32_t w9 = lds_u32(vbase + e4m3_at<D>(t0 + 9, chunk) + off);
                         const uint32_t e01 = __byte_perm(w0, w1, 0x5140);   // dims +0, +1
                         const uint32_t e23 = __byte_perm(w0, w1, 0x7362);   // dims +2, +3
                         const uint32_t f01 = __byte_perm(w8, w9, 0x5140);
@@ -1012,8 +1026,8 @@ struct MmaStages {
 // tile (an 8 KB stage, 32 tokens) spreads each consumer's per-tile softmax and
 // hand-over work over as many bytes as at block size 32 (one block of 16 tokens is
 // 4 KB of K + V).
-template <typename TK, int D, int BS>
-constexpr int mma_blocks_per_tile() { return (sizeof(TK) == 1 && D == 128 && BS == 16) ? 2 : 1; }
+template <typename TK, int D, int BS, bool IN_PLACE = false>
+constexpr int mma_blocks_per_tile() { return (sizeof(TK) == 1 && (D == 128 || IN_PLACE) && BS == 16) ? 2 : 1; }
 
 template <typename T, typename TK, int D, int BS, int NH>
 struct MmaVariant {

@@ -56,14 +56,18 @@ struct RowsSmem {
     // kBlock: the scales of the CTA's blocks behind all that
     static constexpr int kScaleOffset = (kBytes + 15) / 16 * 16;
     static constexpr int kAllocBlock = kScaleOffset + kScaleRingBytes + 1024;
-    static_assert(!kFp8 || D == 128, "E4M3 tiles are read in place: 128-byte rows");
     static_assert(kHalfBytes % 1024 == 0, "swizzle atoms need 1 KB alignment");
 };
+
+// CTAs per SM.  The small tiles of kBlock at head_dim 64 want warps (16 x 8192 tokens, 128/8 heads,
+// blocks of 16: 65.7 us with two, 52.0 with three, 45.7 with four; 64 rows a CTA: 130, 131, 136).
+template <int D, int MODE, int RW>
+constexpr int rows_min_blocks() { return D == 64 && is_block(MODE) ? (RW == 4 ? 3 : 4) : 2; }
 
 // T: query / native output type.  TK: T, or __nv_fp8_e4m3 (value = code * per-kv-head scale).
 // A tile is 32 tokens: one cache block, or two of 16.
 template <typename T, typename TK, int D, int BS, int NSTAGE, int MODE, int RW>
-__global__ void __launch_bounds__(kDecodeThreads, 2)
+__global__ void __launch_bounds__(kDecodeThreads, rows_min_blocks<D, MODE, RW>())
     decode_rows_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv)
 {
@@ -78,6 +82,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     constexpr int KS = D / 16;        // k-steps of the score product
     constexpr int NB = D / 8;         // 8-dim column blocks of O
     constexpr bool kIsMod = is_mod(MODE), kBlk = is_block(MODE);
+    static_assert(!kFp8 || D == 128 || kBlk, "E4M3 tiles are read in place: head_dim 128, or kBlock's maps");
     static_assert(!kBlk || (kFp8 && NSTAGE * BPT <= 32), "the ring of scales outlasts the ring of tiles");
     static_assert(kIsMod || MODE == kPrefix || MODE == kSuffix, "the plain mode has its own kernels");
     static_assert(NCW % RW == 0 && NSTAGE % NCW == 0, "each ring stage belongs to one warp of a row group");
@@ -270,10 +275,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
                         for (int b = 0; b < BPT; ++b) {
                             if (!valid[b])
                                 continue;
-                            unsigned char* bdst = dst + b * (BS * 128);     // rows of block b
+                            unsigned char* bdst = dst + b * (BS * (kFp8 ? D : 128));   // rows of block b
                             const int z = pbn[b] * p.num_kv_heads + kvh;    // < 2^31 (checked on the host)
 #pragma unroll
-                            for (int h = 0; h < D * (int)sizeof(TK) / 128; ++h) {
+                            for (int h = 0; h < (kFp8 ? 1 : D / 64); ++h) {
                                 tma_load_3d(bdst + h * Sm::kHalfBytes, &tk, 64 * h, 0, z, &full[stage], policy);
                                 tma_load_3d(bdst + Sm::kTileBytes + h * Sm::kHalfBytes, &tv, 64 * h, 0, z,
                                             &full[stage], policy);
@@ -395,12 +400,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         if constexpr (kFp8) {
             // token row 8h + g: the 4 codes at head dims 16ks + 4c .. +3 (chunk ks, swizzled by
             // the row; the row's low bits are g whatever h is)
-            const uint32_t ka = kbase + g * 128 + (g << 4) + 4 * c;
+            // (head_dim 64: two tokens a line, so eight rows on are four lines on, and column ^ 4)
+            const uint32_t ka = kbase + e4m3_at<D>(g, 0) + 4 * c;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    const uint32_t w = lds_u32((ka ^ (ks << 4)) + h * 1024);
+                    const uint32_t w = lds_u32((ka ^ (ks << 4) ^ (D == 64 ? (h & 1) << 6 : 0)) + h * 8 * D);
                     Mma<TM>::run(s[h], qa[ks], e4m3x2_to_f16x2(w), e4m3x2_to_f16x2(w >> 16));
                 }
         } else {
@@ -560,14 +566,16 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             if constexpr (kFp8) {
                 // 4-byte loads of the token rows 2c, 2c+1 (+8) at dims 32j + 4g .. +3: token
                 // pairs interleaved by byte_perm are the B fragments of four column blocks
-                const uint32_t va = vbase + mb * 2048 + 2 * c * 128 + (((g >> 2) ^ (2 * c)) << 4) + 4 * (g & 3);
-                const uint32_t vb = va ^ 0x90;         // row 2c + 1: 128 bytes on, column ^ 1
+                const uint32_t va = vbase + mb * 16 * D + e4m3_at<D>(2 * c, g >> 2) + 4 * (g & 3);
+                // row 2c + 1: a line on and column ^ 1, or the line's other half
+                const uint32_t vb = va ^ (D == 128 ? 0x90 : 0x40);
+                constexpr uint32_t kEight = D == 128 ? 0 : 0x40;       // rows + 8: column ^ 4 of D / 16 lines on
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) {
                     const uint32_t w0 = lds_u32(va ^ (j << 5));
                     const uint32_t w1 = lds_u32(vb ^ (j << 5));
-                    const uint32_t w8 = lds_u32((va ^ (j << 5)) + 1024);
-                    const uint32_t w9 = lds_u32((vb ^ (j << 5)) + 1024);
+                    const uint32_t w8 = lds_u32((va ^ (j << 5) ^ kEight) + 8 * D);
+                    const uint32_t w9 = lds_u32((vb ^ (j << 5) ^ kEight) + 8 * D);
                     const uint32_t e01 = __byte_perm(w0, w1, 0x5140), e23 = __byte_perm(w0, w1, 0x7362);
                     const uint32_t f01 = __byte_perm(w8, w9, 0x5140), f23 = __byte_perm(w8, w9, 0x7362);
                     const uint32_t b0[4] = {e4m3x2_to_f16x2(e01), e4m3x2_to_f16x2(e01 >> 16),

@@ -83,12 +83,12 @@ void choose_split(Plan& pl, const Shape& s, AttnMode mode, int64_t count, int le
 
 // Rows of a kv head that a mma.sync CTA serves when there are `rows` of them: 4 or 8
 // (decode_mma_kernel), 16, 32 or 64 (decode_rows_kernel; E4M3 at head_dim 64, whose tiles are
-// converted warp by warp, stays at 8).
+// converted warp by warp, stays at 8; with block scales they are read in place).
 int rows_per_cta(const Shape& s, int64_t rows)
 {
     if (rows <= 4)
         return 4;
-    if (rows <= 8 || (s.fp8() && s.head_dim == 64))
+    if (rows <= 8 || (s.fp8() && s.head_dim == 64 && !s.block_scales()))
         return 8;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
@@ -96,7 +96,7 @@ int rows_per_cta(const Shape& s, int64_t rows)
 // Tokens of a mma.sync kernel's tile.
 int rows_tile(const Shape& s, int per)
 {
-    return per > 8 || (s.fp8() && s.head_dim == 128) ? 32 : s.block_size;
+    return per > 8 || (s.fp8() && (s.head_dim == 128 || s.block_scales())) ? 32 : s.block_size;
 }
 
 // Kernel of a pass with one row per query head of a sequence (decode, or the suffix of the
@@ -198,7 +198,7 @@ cudaError_t launch(const Shape& s, AttnMode mode, const Plan& pl, const DecodePa
 cudaError_t maps(const Shape& s, const void* k_cache, const void* v_cache, int64_t num_blocks,
                  CUtensorMap* tk, CUtensorMap* tv)
 {
-    if (s.kv_dtype == PA_F32 || (s.fp8() && s.head_dim != 128))
+    if (s.kv_dtype == PA_F32 || (s.fp8() && s.head_dim != 128 && !s.block_scales()))
         return cudaSuccess;                      // 1-D bulk copies
     cudaError_t e = kv_tensor_map(tk, k_cache, num_blocks, s.num_kv_heads, s.block_size, s.head_dim,
                                   s.kv_dtype);

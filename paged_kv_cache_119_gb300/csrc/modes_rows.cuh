@@ -12,7 +12,7 @@ namespace pa {
 // Up to 8 rows per CTA on decode_mma_kernel, 16, 32 or 64 on decode_rows_kernel.
 template <typename T, typename TK, int D, int BS, int NH, int MODE>
 struct RowsMode {
-    static constexpr int kBPT = mma_blocks_per_tile<TK, D, BS>();
+    static constexpr int kBPT = mma_blocks_per_tile<TK, D, BS, is_block(MODE)>();
     // a row kernel's 32-token tiles: 64 KB of stages at head_dim 128, so eight over E4M3 caches
     // (with four, a warp of 16 rows had one stage, and waited a load's latency a tile: 32 sequences of
     // 4 new tokens over 8192, 4 heads a kv head, blocks of 32, 144 against 105 us)
@@ -22,7 +22,7 @@ struct RowsMode {
     static constexpr int smem_bytes()
     {
         if constexpr (NH <= 8) {
-            using Sm = MmaSmem<TK, D, BS * kBPT, kStages>;
+            using Sm = MmaSmem<TK, D, BS * kBPT, kStages, is_block(MODE)>;
             return is_block(MODE) ? Sm::kAllocBlock : Sm::kAlloc;
         } else {
             using Sm = RowsSmem<TK, D, kStages, NH / kRowsGroup>;
@@ -44,7 +44,7 @@ struct RowsMode {
 };
 
 // Calls f with the variant's type; false when it is not built (E4M3 caches at head_dim 128
-// take 4 rows on decode_tc8_kernel, at head_dim 64 no more than 8).
+// take 4 rows on decode_tc8_kernel, at head_dim 64 no more than 8, but for kBlock).
 template <typename T, typename TK, int MODE, typename F>
 bool rows_variant(int head_dim, int block_size, int nh, F&& f)
 {
@@ -58,11 +58,13 @@ bool rows_variant(int head_dim, int block_size, int nh, F&& f)
     PA_ROWS_MODE(128, 16, 16) PA_ROWS_MODE(128, 32, 16) PA_ROWS_MODE(128, 16, 32) PA_ROWS_MODE(128, 32, 32)
     if constexpr (sizeof(TK) != 1) {
         PA_ROWS_MODE(128, 16, 4) PA_ROWS_MODE(128, 32, 4)
+    }
+    if constexpr (sizeof(TK) != 1 || is_block(MODE)) {
         PA_ROWS_MODE(64, 16, 16) PA_ROWS_MODE(64, 32, 16) PA_ROWS_MODE(64, 16, 32) PA_ROWS_MODE(64, 32, 32)
     }
     if constexpr (MODE != kPrefix) {               // (a shared prefix takes the chunk kernel there)
         PA_ROWS_MODE(128, 16, 64) PA_ROWS_MODE(128, 32, 64)
-        if constexpr (sizeof(TK) != 1) {
+        if constexpr (sizeof(TK) != 1 || is_block(MODE)) {
             PA_ROWS_MODE(64, 16, 64) PA_ROWS_MODE(64, 32, 64)
         }
     }

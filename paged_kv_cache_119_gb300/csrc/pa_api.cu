@@ -84,15 +84,18 @@ cudaError_t kv_tensor_map(CUtensorMap* map, const void* base, int64_t num_blocks
         }
     EncodeTiledFn fn = encode_tiled_fn();
     const bool fp8 = dtype == PA_FP8_E4M3;
-    if (!fn || (!fp8 && elem_size(dtype) != 2) || (fp8 && head_dim != 128))
+    if (!fn || (!fp8 && elem_size(dtype) != 2) || (fp8 && head_dim != 128 && head_dim != 64))
         return cudaErrorNotSupported;
     if (num_blocks * (int64_t)num_kv_heads >= (int64_t(1) << 31))
         return cudaErrorInvalidValue;           // the TMA z coordinate is a signed 32-bit int
     const cuuint64_t esz = fp8 ? 1 : 2;
-    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)block_size,
+    // tokens of a row: two of 64 codes fill one of 128 bytes
+    const int per_row = fp8 && head_dim == 64 ? 2 : 1;
+    const cuuint32_t rows = (cuuint32_t)(block_size / per_row);
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim * per_row, rows,
                                 (cuuint64_t)num_blocks * (cuuint64_t)num_kv_heads};
-    const cuuint64_t strides[2] = {head_dim * esz, (cuuint64_t)block_size * head_dim * esz};
-    const cuuint32_t box[3] = {fp8 ? 128u : 64u, (cuuint32_t)block_size, 1};   // 128-byte rows
+    const cuuint64_t strides[2] = {head_dim * per_row * esz, (cuuint64_t)block_size * head_dim * esz};
+    const cuuint32_t box[3] = {fp8 ? 128u : 64u, rows, 1};                      // 128-byte rows
     const cuuint32_t estride[3] = {1, 1, 1};
     CUtensorMap m;
     const CUresult r = fn(&m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8

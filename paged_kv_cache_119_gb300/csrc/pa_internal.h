@@ -310,7 +310,7 @@ cudaError_t launch_swap_blocks(const SwapParams& p, cudaStream_t stream);
 // Tensor map over a [num_blocks][num_kv_heads][block_size][head_dim] cache, as
 // 3-D (head_dim, block_size, num_blocks * num_kv_heads) with 128-byte swizzle and
 // a box of 128-byte rows x block_size tokens (64 dims of a 16-bit dtype, or 128
-// E4M3 codes; E4M3 needs head_dim 128).  Encoded maps are cached per (base,
+// E4M3 codes; at head_dim 64 a row is two tokens, 3-D (128, block_size / 2, ..)).  Encoded maps are cached per (base,
 // shape, dtype).
 cudaError_t kv_tensor_map(CUtensorMap* map, const void* base, int64_t num_blocks, int num_kv_heads,
                           int block_size, int head_dim, pa_dtype dtype);
