@@ -9,8 +9,8 @@
 // the softmax attention of section "背景" over that prefix, read through the
 // block table.
 //
-// Organisation.  A CTA owns 256 (query token, query head) rows that share a kv
-// head -- TT = 256 / G consecutive chunk tokens x the G heads of the group, row
+// Organisation.  A CTA owns 256 (query token, query head) rows (128 with one query tile: see
+// chunk_threads) that share a kv head -- TT = 256 / G consecutive chunk tokens x the G heads of the group, row
 // r = token * G + head -- as two 128-row query tiles.  K and V stream through the
 // block table in tiles of 64 tokens, each tile serving both query tiles:
 //   S_q[128 x 64]  = Q_q[128 x D] . K^T      (tcgen05.mma kind::f16, fp32 in TMEM)
@@ -66,7 +66,8 @@
 // the ring above (E4M3 -> f16 is exact), then hand it to the issuers and release the raw
 // slot.  The operands are f16: a bf16 query row is scaled into f16 range by a power of
 // two (exact) that joins the row's score scale together with the kv head's K scale, and
-// the V scale multiplies the output.
+// the V scale multiplies the output.  With block scales (kBlock, block_scale.cuh) a tile's scales
+// follow it from the producer through the converters to the softmax warps.
 #pragma once
 
 #include <cuda.h>

@@ -1,6 +1,7 @@
 // decode_rows.cuh -- paged attention of 9 to 64 rows of a kv head on mma.sync (sm_103a): the
 // (token, head) rows of a short chunk, the heads of a wide group, or the (sequence, head) rows
-// of a group that shares a prefix; fp16 / bf16 caches, and E4M3 caches at head_dim 128.
+// of a group that shares a prefix; fp16 / bf16 caches, and E4M3 caches at head_dim 128, or with
+// block scales at 64 too.
 //
 // decode_mma_kernel puts 16 tokens on the M side of the matrix instruction and 8 rows on the
 // N side, which suits 8 rows: their K and V fragments feed nothing else.  With more rows that
@@ -22,7 +23,7 @@
 // 32 sequences of 5 new tokens, 4 heads a kv head, f16, a window of 1024: 33.7 us (4.1 TB/s);
 // the pass over 16 prefixes of 1024 tokens for 8 x 4 rows each, bf16: 18 us.  On decode_mma_kernel
 // (8 rows a CTA) the first took 89 us, on a transposed tcgen05 form of 16 and 32 rows 65.
-// Modes: kMod (chunk rows, or with query_start null the heads of each sequence's last token;
+// Modes: kMod and kBlock (chunk rows, or with query_start null the heads of each sequence's last token;
 // kModBoth when the scores have a cap or slopes),
 // kPrefix and kSuffix, which write partial rows only.
 #pragma once

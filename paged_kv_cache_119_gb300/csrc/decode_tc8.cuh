@@ -41,7 +41,8 @@
 //     read the P.V result of the previous tile and fold it into their accumulators.
 // S and O tensor-memory buffers and the Pt buffers alternate between tiles, so the
 // softmax of tile i+1 overlaps P.V of tile i.  Every wait is bounded; an invalid
-// block id makes the CTA's rows NaN, decided after the final CTA barrier.
+// block id makes the CTA's rows NaN, decided after the final CTA barrier.  With block scales
+// (kBlock, block_scale.cuh) a softmax thread fetches the scales of its own token's block, a tile ahead.
 #pragma once
 
 #include <cuda.h>

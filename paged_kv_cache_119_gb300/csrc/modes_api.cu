@@ -104,7 +104,7 @@ int rows_tile(const Shape& s, int per)
 // than a 16-row matrix fragment that is mostly empty (the rule of pa_decode); E4M3 codes at
 // head_dim 128 go to the tensor core as they are for up to four rows.  Other groups take
 // the next of 4, 8, 16, 32 or 64 rows, padded, so that a K/V byte is read once whatever the
-// group.  Capped decode of contexts up to 2048, this rule's kernel against mma.sync: f16, one head
+// group (block-scaled caches at head_dim 64 from one row on).  Capped decode of contexts up to 2048, this rule's kernel against mma.sync: f16, one head
 // (64 sequences, 40 kv heads) 195 against 237 us, bf16, two heads (128, 20) 205 against 238; E4M3,
 // one head 105 against 170, four heads (256, 8) 97 against 139.
 Plan plan_heads(const Shape& s)
@@ -326,8 +326,9 @@ int mod_impl(Call call, void* out, pa_dtype out_dtype, const void* q, const Shap
     if (!global_lens)
         max_global_len = 0;
     const int qlen = decode ? 1 : max_query_len;
-    // (32 rows of a chunk on a decode kernel's row mode against the chunk kernel, 32 sequences,
-    // capped: 35.1 against 49.3 us over a window of 1024, 198 against 278 over 8192 tokens; 64 rows
+    // (Block scales: 32 rows over 1500 tokens, 32 sequences, 45.7 us, and the chunk kernel, which takes
+    // as long for any number of rows, 61.  32 rows of a chunk on a decode kernel's row mode against the
+    // chunk kernel, 32 sequences, capped: 35.1 against 49.3 us over a window of 1024, 198 against 278 over 8192 tokens; 64 rows
     // 60.2 against 51.4 and 377 against 280)
     const bool cap = softcap > 0.f, slope = alibi_slopes != nullptr;
     // what the chunk kernel would run in
