@@ -649,7 +649,8 @@ int pa_cross_attention_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtyp
  * pa_chunk_attention_fp8 and pa_cross_attention_fp8 over such caches.  Other arguments, checks,
  * accuracy and workspace as there (max_context_len at most 2^30; partition_size a multiple of 128;
  * block_table entries are read, and V rows of slots past the context may hold anything, as
- * in the modified-score calls).
+ * in the modified-score calls).  An output beyond out_dtype's range is an infinity (PA_F16: scales
+ * can hold values past 65504).
  */
 int pa_append_fp8_block(const void* k, int64_t k_stride, const void* v, int64_t v_stride, pa_dtype dtype,
                         void* k_cache, void* v_cache, float* k_scales, float* v_scales,

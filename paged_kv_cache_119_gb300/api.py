@@ -868,7 +868,7 @@ def _paged_plan(kind, chunk, Hkv, B, max_context_len, partition_size, fresh, o, 
     if fresh and partition_size >= 0:
         need = (_chunk_need(R, Hq, D, max_context_len, partition_size) if chunk else
                 _decode_need(S, Hq, D, max_context_len, B, partition_size))
-    return _DT[ot], _DT[qt], R, Hq, D, S, W, int(max_context_len), stride, need
+    return _DT[ot], _DT[qt], R, Hq, D, S, W, max_context_len, stride, need
 
 
 def _paged(kind, fn, out, q, k_cache, v_cache, scales, block_tables, context_lens, query_start, scale,
@@ -877,6 +877,10 @@ def _paged(kind, fn, out, q, k_cache, v_cache, scales, block_tables, context_len
     "head" (E4M3, a scale for each head) or "block"."""
     tensors = (out, q, k_cache, v_cache, block_tables, context_lens, *scales) if query_start is None else \
         (out, q, k_cache, v_cache, block_tables, context_lens, query_start, *scales)
+    # plain numbers: the plan below is kept by value
+    num_kv_heads, block_size, partition_size = int(num_kv_heads), int(block_size), int(partition_size)
+    if max_context_len is not None:
+        max_context_len = int(max_context_len)
     dev = torch.cuda.current_device()
     if not _dense_on(dev, tensors):
         for t in tensors:
@@ -893,7 +897,7 @@ def _paged(kind, fn, out, q, k_cache, v_cache, scales, block_tables, context_len
         v_cache.shape, v_cache.dtype, block_tables.shape, block_tables.dtype, context_lens.shape,
         context_lens.dtype, qs.shape, qs.dtype, *more)
     workspace, ws_ptr, ws_bytes = _scratch(need, workspace, q, stream)
-    tail = (max_context_len, S, Hq, num_kv_heads, D, block_size, float(scale), int(partition_size), ws_ptr,
+    tail = (max_context_len, S, Hq, num_kv_heads, D, block_size, float(scale), partition_size, ws_ptr,
             ws_bytes, _stream(stream, dev))
     if query_start is not None:
         tail = (query_start.data_ptr(), R, int(max_query_len), *tail)

@@ -231,3 +231,18 @@ def test_a_long_cache_beyond_two_to_the_31_bytes():
     ref, size = R.attend(c)
     out = torch.empty_like(c.q)
     check(pa.pa_decode_fp8_block(out, c.q, k, v, ks, vs, table, lens, c.scale, H, B), ref, size)
+
+
+def test_a_bound_that_changes_between_calls():
+    """max_context_len is taken by its value at each call: the same object, holding another number
+    the second time (the first call's contexts fit in 16 tokens, the second's do not)."""
+    bound = torch.tensor(16)
+    c = R.build(40, [90, 64], [1, 1], 8, 2, 128, 16, torch.bfloat16)
+    ref, size = R.attend(c)
+    whole = c.context_lens.clone()
+    c.context_lens.fill_(16)
+    call(c, max_context_len=bound)
+    bound.fill_(90)
+    c.context_lens.copy_(whole)
+    check(call(c, max_context_len=bound), ref, size)
+    assert no_error()
