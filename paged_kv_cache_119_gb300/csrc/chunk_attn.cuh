@@ -95,6 +95,11 @@ struct ChunkWarps {
     static constexpr int kConv0 = 1 + QT + kSoftmax;           // the first converter
     static constexpr int kConv = 2 * QT;
 };
+// Least factor of the scores over E4M3 caches.  Hidden columns are -infinity before the factor
+// meets them, so it is never 0, which the product of a tiny bf16 row's power of two (2^-100 at
+// least) and a tiny K scale can be.  Scores are below 2^33 before it: from here down they change
+// no weight.
+__device__ __forceinline__ float score_factor(float f) { return f < 0x1p-126f ? 0x1p-126f : f; }
 // P.V takes P as 2^kChunkPExp p: p <= 2^8 (the lazy rescale), so 2^15 at most in f16
 constexpr float kChunkPExp = 7.f;
 static_assert(kChunkPExp == 7.f, "the partial rows of a shared prefix take 2^-7 off again");
@@ -948,6 +953,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE, QT>(), 3 - QT)
                 }
             }
         }
+        if constexpr (kF8 && !kBlk)
+            sl2 = score_factor(sl2);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0)
@@ -1083,7 +1090,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE, QT>(), 3 - QT)
                         const float top = max3f(s[k * BS + BS - 4], s[k * BS + BS - 3],
                                                 fmaxf(s[k * BS + BS - 2], s[k * BS + BS - 1]));
                         const float4 sc = stage_scale[st * 4 + k];
-                        tmax = fmaxf(tmax, fmaf(max3f(max3f(mx[0], mx[1], mx[2]), mx[3], top), sl2 * sc.x, sc.y));
+                        tmax = fmaxf(tmax, fmaf(max3f(max3f(mx[0], mx[1], mx[2]), mx[3], top), score_factor(sl2 * sc.x),
+                                                sc.y));
                     }
                 } else {
                     tmax = smax == -INFINITY ? -INFINITY : smax * mul;
@@ -1130,7 +1138,8 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE, QT>(), 3 - QT)
 #pragma unroll
                     for (int k = 0; k < BPT; ++k) {
                         const float4 sc = stage_scale[st * 4 + k];
-                        const float2 f = make_float2(sl2 * sc.x, sl2 * sc.x), add = make_float2(nm + sc.y, nm + sc.y);
+                        const float mul_k = score_factor(sl2 * sc.x);
+                        const float2 f = make_float2(mul_k, mul_k), add = make_float2(nm + sc.y, nm + sc.y);
                         float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                         for (int c = k * BS; c < (k + 1) * BS; c += 2) {
