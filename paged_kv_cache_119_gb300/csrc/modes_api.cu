@@ -346,7 +346,12 @@ int mod_impl(Call call, void* out, pa_dtype out_dtype, const void* q, const Shap
     const int length =
         (int)std::min<int64_t>(seen_bound(max_context_len, window, max_global_len, qlen, pl.tile), INT32_MAX);
     choose_split(pl, s, mode, num_seqs, length, partition_size);
-    if ((int64_t)s.num_kv_heads * pl.chunks > 65535 || pl.units > INT32_MAX / 64)
+    // kv heads x row tiles are a grid's y.  (The chunk kernel's grid is one-dimensional here; its rows
+    // are counted in tiles of 256 whatever its CTAs take, so that one length is taken in every mode.)
+    const int tile_tokens = kChunkCtaRows / s.group();
+    const int64_t row_tiles =
+        pl.family == Family::kChunk ? ((int64_t)qlen + tile_tokens - 1) / tile_tokens : pl.chunks;
+    if (s.num_kv_heads * row_tiles > 65535 || pl.units > INT32_MAX / 64)
         return PA_ERR_INVALID;
 
     Buffers b;
