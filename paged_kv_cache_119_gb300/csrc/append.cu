@@ -182,6 +182,19 @@ struct QWalk {
     }
 };
 
+// Whether the call serves a sequence with rows q0 .. q1 - 1 and L tokens.
+__device__ __forceinline__ bool append_sound(const AppendParams& p, int q0, int q1, int L, int block_size)
+{
+    return q0 >= 0 && q1 >= q0 && (int64_t)q1 <= p.num_tokens && q1 - q0 <= L && q1 - q0 <= p.max_query_len &&
+           (int64_t)L <= p.bt_stride * block_size;
+}
+
+// Whether sequence s leaves no row before it, if it is the first, and none behind it, if the last.
+__device__ __forceinline__ bool append_owned(const AppendParams& p, int s, int q0, int q1)
+{
+    return (s > 0 || q0 == 0) && (s < p.num_seqs - 1 || (int64_t)q1 == p.num_tokens);
+}
+
 // CTAs per SM: the rows of q want loads in flight more than K and V want registers (4096 tokens and
 // more of 64 + 2 x 8 heads: 121 us with four, 133 with three); a tile of 32 rows of 128 is 64
 // registers a lane.
@@ -232,15 +245,23 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas<D, B, ONE>()) appe
     const int qs0 = p.query_start[s], qs1 = p.query_start[s + 1];
     const int n = qs1 - qs0;
     const int L = p.context_lens[s];
-    const bool first_cta = b == 0 && blockIdx.y == 0 && threadIdx.x == 0;
-    if (first_cta && s == p.num_seqs - 1 && (int64_t)qs1 != p.num_tokens)
-        atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);       // rows after the last sequence belong to no one
-    if (qs0 < 0 || n < 0 || (int64_t)qs1 > p.num_tokens || n > L || n > p.max_query_len ||
-        (int64_t)L > p.bt_stride * bs) {
-        if (first_cta)
+    const bool sound = append_sound(p, qs0, qs1, L, bs);
+    // Sequences to skip and rows that no sequence owns are flagged once: by each sequence's first CTA,
+    // or, where units are searched for (a malformed query_start may leave a sequence none), by the
+    // grid's first.
+    if (p.per_seq > 0) {
+        if (b == 0 && blockIdx.y == 0 && threadIdx.x == 0 &&
+            !(sound && append_owned(p, s, qs0, qs1)))
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
-        return;
+    } else if (blockIdx.x == 0 && blockIdx.y == 0) {
+        for (int i = threadIdx.x; i < p.num_seqs; i += kAppendThreads) {
+            const int q0 = p.query_start[i], q1 = p.query_start[i + 1];
+            if (!(append_sound(p, q0, q1, p.context_lens[i], bs) && append_owned(p, i, q0, q1)))
+                atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
+        }
     }
+    if (!sound)
+        return;
     const int first = L - n;                          // position of the first new token
     const int lb = first / bs + b;                    // logical block
     if (b < 0 || lb >= (L + bs - 1) / bs || n == 0)
