@@ -317,6 +317,14 @@ constexpr int chunk_threads()
     return 32 * (ChunkWarps<QT>::kConv0 + (conv ? ChunkWarps<QT>::kConv : 0));
 }
 
+// kWideIO: live rows of a CTA up to which its warps write them out a row a lane.  The code that stores
+// whole rows is longer and, run once a CTA, gains nothing for few rows.  A row a lane / whole rows, us,
+// 152 CTAs over 256 tokens, head_dim 128, modified scores: f16, 40 rows 9.6 / 10.3 (fp32 out 10.0 /
+// 11.7), 64 rows 9.9 / 10.5, 128 rows 11.0 / 10.7, 256 rows 15.6 / 12.0; E4M3 caches, 40 rows 11.1 /
+// 11.9, 64 rows 12.5 / 11.9.  Partial rows of a shared prefix, 64 of them: 19.4 / 18.5.
+template <bool F8>
+constexpr int kNarrowRows = F8 ? 48 : 64;
+
 template <typename T, int D, int BS, int NST, int NRAW = 0, int MODE = kPlain, int QT = 2>
 __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE, QT>(), 3 - QT)
     chunk_attn_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap tk,
@@ -328,7 +336,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE, QT>(), 3 - QT)
     constexpr bool kF8 = NRAW > 0;
     constexpr bool kIsMod = is_mod(MODE), kCap = has_cap(MODE), kSlope = has_slope(MODE);
     constexpr bool kBlk = is_block(MODE);
-    constexpr bool kWideIO = !kCap && !kSlope;   // warps read q and write out by whole rows
+    constexpr bool kWideIO = !kCap && !kSlope;   // warps read q and write out by whole rows, but for few
     static_assert(!kBlk || kF8, "block scales belong to E4M3 caches");
     constexpr bool kTwoTerms = MODE == kPrefix;  // P as hi + lo of V's type, else one f16 term
     constexpr bool kVConv = !kF8 && std::is_same_v<T, __nv_bfloat16> && !kTwoTerms;   // bf16 V -> f16 in place
@@ -840,14 +848,17 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE, QT>(), 3 - QT)
         constexpr int CPR = D / 8, RPW = 32 / CPR;
         const int64_t row_base = (int64_t)(qs0 + j0) * p.num_q_heads + (int64_t)kvh * G;
         const int my_row = row_valid ? tok * p.num_q_heads + g : -1;
+        const bool wide = kWideIO && (MODE == kPrefix || ntok * G > kNarrowRows<kF8>);
         {
             // Q rows into the 128-byte-swizzled operand layout; rows past the chunk are 0.  The
             // lanes of a warp read whole rows (CPR lanes of 16 bytes each), not one row a lane:
-            // with the epilogue's stores, which go the same way, one row a lane cost a CTA 3 to 5 us
-            // at head_dim 128 (256 rows over 64 tokens 12.2 against 8.7 us, 4 x 512 tokens of 8192, 64/8
-            // heads, bf16, 526 against 517).  Capped and biased scores keep a row a lane: their loops
-            // lose more to the registers (568 against 608 us, capped, f16).
-            if constexpr (kWideIO) {
+            // with the epilogue's stores, which go the same way, one row a lane cost a CTA of 256 rows
+            // 2 to 5 us at head_dim 128 (over 64 tokens 12.2 against 10.1 us; 4 x 512 tokens of 8192,
+            // 64/8 heads, bf16, 526 against 511).  At head_dim 64 few rows are read a row a lane, as
+            // they are written (kNarrowRows; 40 rows under a window of 128, 7.5 against 7.0 us).
+            // Capped and biased scores keep a row a lane: their loops lose more to the registers
+            // (568 against 608 us, capped, f16).
+            if (kWideIO && (D == 128 || wide)) {
                 unsigned char* qdst = smem + Sm::kQOff + q * Sm::kQTile + 32 * wq * 128;
                 constexpr bool kToF16 = kF8 && DType<T>::id == PA_BF16;
                 const uint4* src =
@@ -1250,7 +1261,7 @@ __global__ void __launch_bounds__(chunk_threads<T, NRAW, MODE, QT>(), 3 - QT)
             // cannot overflow: |O| <= l max|v|, far inside fp32)
             const bool watch = kVConv && row_valid && !poisoned && lsum > 0.f && lsum < INFINITY;
             bool unconvertible = false;
-            if constexpr (kWideIO) {
+            if (wide) {
                 // Rows go out through this warp's 32 rows of the query tile (no product reads them any
                 // more), so that its lanes store whole rows; piece c of a row at c ^ (row & 7).
                 unsigned char* stage = smem + Sm::kQOff + q * Sm::kQTile + 32 * wq * 128;
