@@ -306,9 +306,10 @@ __device__ __forceinline__ void cap_row(float (&s)[kChunkTileTok], float mul, co
 // row sees; kPrefix, the rows of a group of sequences (query_start = the group's first one)
 // over the tokens they share, partial rows only; kBlock, kMod over an E4M3 cache with a scale for
 // each block (four or two in a tile).
-// QT: query tiles of a CTA.  Two, but one for kMod over 16-bit caches at head_dim 64, where two
-// such CTAs fit on an SM: what a CTA does once (set-up, reading q, the first tile's latency,
-// writing out: 5 us beside 0.8 a tile) then goes on under the other's tiles, and a unit is 128 rows.
+// QT: query tiles of a CTA.  Two; for kMod over 16-bit caches at head_dim 64 also one, where two such
+// CTAs fit on an SM: what a CTA does once (set-up, reading q, the first tile's latency, writing
+// out: 5 us beside 0.8 a tile) then goes on under the other's tiles, and a unit is 128 rows.
+// (choose_query_tiles in modes_api.cu has the rule; one tile was not tried for the other modes.)
 template <typename T, int NRAW, int MODE, int QT = 2>
 constexpr int chunk_threads()
 {

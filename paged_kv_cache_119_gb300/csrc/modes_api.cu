@@ -25,6 +25,7 @@ struct Plan {
     int chunks;
     int tile;
     int partition;
+    int query_tiles;             // kChunk: of a CTA
     int64_t units, slots;
 };
 
@@ -42,8 +43,6 @@ int occupancy(const Shape& s, AttnMode mode, Family f, int per)
     const bool bf16 = s.q_dtype == PA_BF16;
     if (mode == kBlock && f == Family::kRows)
         return (bf16 ? occupancy_rows_block_bf16 : occupancy_rows_block_f16)(s.head_dim, s.block_size, per);
-    if (mode == kBlock && f == Family::kChunk)
-        return (bf16 ? occupancy_chunk_block_bf16 : occupancy_chunk_block_f16)(s.head_dim, s.block_size);
     switch (f) {
     case Family::kCore:
         return occupancy_core_mode(mode, s.q_dtype, s.kv_dtype, s.head_dim, s.block_size, per);
@@ -54,12 +53,7 @@ int occupancy(const Shape& s, AttnMode mode, Family f, int per)
                         : occupancy_rows_f16_fp8(mode, s.head_dim, s.block_size, per);
         return bf16 ? occupancy_rows_bf16(mode, s.head_dim, s.block_size, per)
                     : occupancy_rows_f16(mode, s.head_dim, s.block_size, per);
-    case Family::kChunk:
-        if (s.fp8())
-            return bf16 ? occupancy_chunk_bf16_fp8(mode, s.head_dim, s.block_size)
-                        : occupancy_chunk_f16_fp8(mode, s.head_dim, s.block_size);
-        return bf16 ? occupancy_chunk_bf16(mode, s.head_dim, s.block_size)
-                    : occupancy_chunk_f16(mode, s.head_dim, s.block_size);
+    case Family::kChunk: break;                  // (chunk_ctas_per_sm)
     }
     return 0;
 }
@@ -70,13 +64,20 @@ void choose_split(Plan& pl, const Shape& s, AttnMode mode, int64_t count, int le
                   int partition_size)
 {
     pl.units = count * s.num_kv_heads * pl.chunks;
-    pl.slots = partition_size == 0
-                   ? (int64_t)device_sm_count() * occupancy(s, mode, pl.family, pl.per)
-                   : 0;
+    const bool chunk = pl.family == Family::kChunk;
+    pl.slots = partition_size != 0 ? 0
+                                   : (int64_t)device_sm_count() *
+                                         (chunk ? chunk_ctas_per_sm(pl.query_tiles)
+                                                : occupancy(s, mode, pl.family, pl.per));
     if (pl.family == Family::kTc8)
         pl.partition = choose_partition_tc8(partition_size, length, pl.units, pl.slots);
-    else if (pl.family == Family::kChunk)
-        pl.partition = choose_chunk_partition(partition_size, length, pl.units, pl.slots);
+    else if (chunk)
+        // A second CTA on an SM adds two thirds of a first one: a context is cut to have one only where
+        // it is long enough to pay the merge (8 x 40 tokens of 4096, 16/16 heads of 64, 50 -> 38 us;
+        // 2 x 512 of 2048 27 -> 31, under a window of 128 9 -> 20).
+        pl.partition = choose_chunk_partition(partition_size, length, pl.units,
+                                              length < 4096 ? std::min<int64_t>(pl.slots, device_sm_count())
+                                                            : pl.slots);
     else                                         // whole tiles of any family: multiples of 64
         pl.partition = choose_partition(partition_size, length, pl.units, pl.slots, 64);
 }
@@ -142,8 +143,8 @@ Plan plan_heads(const Shape& s)
 // Kernel of a pass with `tokens` x group rows per kv head: at most few_rows of them (and
 // E4M3 at head_dim 64, whose tiles no tensor map reaches) on a decode kernel's row mode,
 // more on the tcgen05 chunk kernel.
-// cta_rows: rows of a CTA of the chunk kernel.
-Plan plan_rows(const Shape& s, int64_t tokens, int few_rows, int cta_rows = kChunkCtaRows)
+// query_tiles: of a CTA of the chunk kernel.
+Plan plan_rows(const Shape& s, int64_t tokens, int few_rows, int query_tiles = 2)
 {
     Plan pl{};
     const int64_t rows = tokens * s.group();
@@ -155,11 +156,43 @@ Plan plan_rows(const Shape& s, int64_t tokens, int few_rows, int cta_rows = kChu
         return pl;
     }
     pl.family = Family::kChunk;
-    const int tt = cta_rows / s.group();         // tokens per CTA
+    pl.query_tiles = query_tiles;
+    const int tt = kChunkCtaRows / 2 * query_tiles / s.group();       // tokens per CTA
     pl.per = tt * s.group();
     pl.chunks = (int)std::min<int64_t>((tokens + tt - 1) / tt, INT32_MAX);
     pl.tile = 64;
     return pl;
+}
+
+// Query tiles of a CTA of the chunk kernel for num_seqs sequences of at most qlen new tokens, num_tokens in all,
+// whose rows read up to `length` tokens.  Per 128 full rows two tiles are 7 % faster (one stream of K and V
+// for 256 rows: 16 x 300 tokens of 4096, 32/8 heads, 246 against 267 us), but half a tile of the last
+// rows is idle on average, and one tile spreads over more SMs (24 x 336..448 of 1500, 20/20 heads,
+// 104 against 129; 32 x 128 of 1024, 16/16, 40 against 70; 2 x 512 under a window of 128, 16/16, 9
+// against 22).  So one tile,
+//  - unless CTAs of two tiles find an SM each and CTAs of one do not (16 x 64 tokens of 600, 32/8
+//    heads: 16.0 against 14.6);
+//  - unless the rows nearly fill their tiles and contexts are long: where there are more units than
+//    SMs, or where a context is cut into parts that fill them (300 tokens of 32768, 32/8 heads, 154
+//    against 147; 256 of 4096, 16/16 heads, 21 against 22).
+int choose_query_tiles(const Shape& s, AttnMode mode, int num_seqs, int64_t num_tokens, int qlen, int length)
+{
+    if (!chunk_one_tile(mode, s.head_dim, s.fp8()))
+        return 2;
+    const int64_t sms = device_sm_count(), heads = (int64_t)num_seqs * s.num_kv_heads;
+    auto tiles = [&](int rows) -> int64_t { return ((int64_t)qlen + rows / s.group() - 1) / (rows / s.group()); };
+    const int64_t one = heads * tiles(kChunkCtaRows / 2), two = heads * tiles(kChunkCtaRows);
+    if (two <= sms && one > sms)
+        return 2;
+    if (length < (two <= sms ? 16384 : 2048))
+        return 1;
+    // rows of a sequence's tiles, full or not: as many where every sequence brings qlen tokens, else
+    // half a tile past the average
+    const bool even = num_tokens == (int64_t)num_seqs * qlen;
+    const double rows = (double)num_tokens / num_seqs * s.group();
+    const double in_one = even ? (double)tiles(kChunkCtaRows / 2) * (kChunkCtaRows / 2) : rows + kChunkCtaRows / 4;
+    const double in_two = even ? (double)tiles(kChunkCtaRows) * kChunkCtaRows : rows + kChunkCtaRows / 2;
+    return 1.07 * in_one < in_two ? 1 : 2;
 }
 
 cudaError_t launch(const Shape& s, AttnMode mode, const Plan& pl, const DecodeParams& d,
@@ -335,16 +368,18 @@ int mod_impl(Call call, void* out, pa_dtype out_dtype, const void* q, const Shap
     const AttnMode chunk_mode = s.block_scales() ? kBlock
                                 : cap            ? (slope ? kModBoth : kModCap)
                                                  : (slope ? kModSlope : kMod);
+    auto bound = [&](int tile) -> int {
+        return (int)std::min<int64_t>(seen_bound(max_context_len, window, max_global_len, qlen, tile), INT32_MAX);
+    };
     Plan pl = decode ? plan_heads(s)
                      : plan_rows(s, qlen, kChunkRowsMax,
-                                 kChunkCtaRows / 2 * chunk_query_tiles(chunk_mode, s.head_dim, s.fp8()));
+                                 choose_query_tiles(s, chunk_mode, num_seqs, num_query_tokens, qlen, bound(64)));
     AttnMode mode = s.block_scales() ? kBlock : kMod;
     if (pl.family == Family::kChunk)
         mode = chunk_mode;
     else if (pl.family == Family::kRows && !s.block_scales())
         mode = cap || slope ? kModBoth : kMod;
-    const int length =
-        (int)std::min<int64_t>(seen_bound(max_context_len, window, max_global_len, qlen, pl.tile), INT32_MAX);
+    const int length = bound(pl.tile);
     choose_split(pl, s, mode, num_seqs, length, partition_size);
     // kv heads x row tiles are a grid's y.  (The chunk kernel's grid is one-dimensional here; its rows
     // are counted in tiles of 256 whatever its CTAs take, so that one length is taken in every mode.)
@@ -409,12 +444,15 @@ int mod_impl(Call call, void* out, pa_dtype out_dtype, const void* q, const Shap
         d.mods.cap = (float)((double)softcap * 1.4426950408889634);
         d.mods.inv_cap = 1.f / d.mods.cap;
     }
-    // A one-pass grid of the chunk kernel (one CTA per SM) whose last wave is at most half full
+    // A one-pass grid of the chunk kernel with one CTA per SM whose last wave is at most half full
     // leaves the rest of the SMs idle for as long as a CTA runs: its units are then cut into as
     // many parts as fill that wave.  4 x 512 tokens of 8192, 64/8 heads, capped: 512 units on 152
-    // SMs, the last 56 in two parts, 673 -> 574 us.  Without a workspace the call runs unsplit.
+    // SMs, the last 56 in two parts, 673 -> 574 us.  Without a workspace the call runs unsplit.  (With
+    // CTAs of one query tile, two on an SM, the last ones run faster alone and a cut loses: 12 x
+    // 150..250 tokens of 1500, 16/16 heads of 64, 30 uncut, 36 cut.)
     int64_t whole_units = 0;
-    if (pl.family == Family::kChunk && pl.partition == 0 && partition_size == 0 && pl.slots > 0) {
+    if (pl.family == Family::kChunk && pl.query_tiles == 2 && pl.partition == 0 && partition_size == 0 &&
+        pl.slots > 0) {
         const int64_t rest = pl.units % pl.slots;
         const int64_t cut = rest > 0 && pl.units > pl.slots ? std::min(pl.slots / rest, (int64_t)length / 512) : 0;
         const int64_t P = cut > 1 ? ((length + cut - 1) / cut + 63) / 64 * 64 : 0;
@@ -482,6 +520,7 @@ int mod_impl(Call call, void* out, pa_dtype out_dtype, const void* q, const Shap
     c.out_f32 = d.out_f32;
     c.scale_log2 = d.scale_log2;
     c.mods = d.mods;
+    c.query_tiles = pl.query_tiles;
     c.whole_units = d.whole_units;
     c.scale_stride = s.scale_stride;
 
@@ -658,6 +697,7 @@ int prefix_impl(void* out, pa_dtype out_dtype, const void* q, const Shape& s, co
         c.max_context_len = max_prefix_len;
         c.partition_tokens = pl.prefix.partition;
         c.max_parts = max_parts;
+        c.query_tiles = pl.prefix.query_tiles;
         c.scale_log2 = d.scale_log2;
         e = launch(s, kPrefix, pl.prefix, dp, c, tk, tv,
                    dim3(pl.prefix_parts, s.num_kv_heads * pl.prefix.chunks, num_groups), st);

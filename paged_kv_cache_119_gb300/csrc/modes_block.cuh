@@ -34,13 +34,6 @@ namespace pa {
             err = launch_mode_variant<decltype(v)>(grid, stream, p, tk, tv);                         \
         });                                                                                          \
         return err;                                                                                  \
-    }                                                                                                \
-    int occupancy_chunk_block_##name(int head_dim, int block_size)                                   \
-    {                                                                                                \
-        int n = 0;                                                                                   \
-        chunk_variant<T, true, kBlock>(                                                              \
-            head_dim, block_size, [&](auto v) { n = occupancy_mode_variant<decltype(v)>(); });       \
-        return n;                                                                                    \
     }
 
 }  // namespace pa

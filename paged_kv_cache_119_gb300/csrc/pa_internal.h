@@ -317,11 +317,16 @@ cudaError_t kv_tensor_map(CUtensorMap* map, const void* base, int64_t num_blocks
 
 // (query token, query head) rows one chunk-attention CTA serves (two 128-row tiles).
 constexpr int kChunkCtaRows = 256;
-// 128-row query tiles of a CTA of the chunk kernel (chunk_attn.cuh).
-__host__ __device__ constexpr int chunk_query_tiles(int mode, int head_dim, bool fp8)
+// Whether the chunk kernel is built for CTAs of one 128-row query tile beside those of two
+// (chunk_attn.cuh); modes_api.cu chooses.
+__host__ __device__ constexpr bool chunk_one_tile(int mode, int head_dim, bool fp8)
 {
-    return mode == kMod && head_dim == 64 && !fp8 ? 1 : 2;
+    return mode == kMod && head_dim == 64 && !fp8;
 }
+// CTAs of the chunk kernel on an SM: what its registers, shared memory and tensor memory are laid out
+// for.  (The runtime's occupancy query answers 1 for either form; 152 CTAs of one query tile over
+// 4096 tokens take 51.9 us, 304 of them 62.)
+__host__ __device__ constexpr int chunk_ctas_per_sm(int query_tiles) { return query_tiles == 1 ? 2 : 1; }
 
 // Causal attention of chunks of new query tokens over the paged cache (the
 // tensor-core kernel of chunk_attn.cuh).  Rows of q / out are (query token, query
@@ -353,6 +358,7 @@ struct ChunkParams {
     int out_f32;
     float scale_log2;
     ScoreMods mods;              // kMod
+    int query_tiles;             // of a CTA
     int whole_units;             // kMod: (sequence, kv head, row tile) units that are not split
     const int32_t* prefix_lens;  // kPrefix: shared tokens of each sequence
     int64_t scale_stride;        // kBlock: k_scale, v_scale are [num_blocks][scale_stride]
@@ -420,13 +426,11 @@ cudaError_t launch_rows_block_f16(const DecodeParams& p, int head_dim, int block
 int occupancy_rows_block_f16(int head_dim, int block_size, int nh);
 cudaError_t launch_chunk_block_f16(const ChunkParams& p, int head_dim, int block_size,
                        const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid, cudaStream_t stream);
-int occupancy_chunk_block_f16(int head_dim, int block_size);
 cudaError_t launch_rows_block_bf16(const DecodeParams& p, int head_dim, int block_size, int nh,
                        const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid, cudaStream_t stream);
 int occupancy_rows_block_bf16(int head_dim, int block_size, int nh);
 cudaError_t launch_chunk_block_bf16(const ChunkParams& p, int head_dim, int block_size,
                        const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid, cudaStream_t stream);
-int occupancy_chunk_block_bf16(int head_dim, int block_size);
 // decode_tc8_kernel (E4M3, head_dim 128), 1, 2 or 4 rows per CTA:
 cudaError_t launch_tc8_mode(const DecodeParams& p, AttnMode mode, pa_dtype q_dtype, int block_size,
                             int rows, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
@@ -436,19 +440,15 @@ int occupancy_tc8_mode(AttnMode mode, pa_dtype q_dtype, int block_size, int rows
 cudaError_t launch_chunk_f16(const ChunkParams& p, AttnMode mode, int head_dim, int block_size,
                        const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                        cudaStream_t stream);
-int occupancy_chunk_f16(AttnMode mode, int head_dim, int block_size);
 cudaError_t launch_chunk_bf16(const ChunkParams& p, AttnMode mode, int head_dim, int block_size,
                        const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                        cudaStream_t stream);
-int occupancy_chunk_bf16(AttnMode mode, int head_dim, int block_size);
 cudaError_t launch_chunk_f16_fp8(const ChunkParams& p, AttnMode mode, int head_dim, int block_size,
                        const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                        cudaStream_t stream);
-int occupancy_chunk_f16_fp8(AttnMode mode, int head_dim, int block_size);
 cudaError_t launch_chunk_bf16_fp8(const ChunkParams& p, AttnMode mode, int head_dim, int block_size,
                        const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                        cudaStream_t stream);
-int occupancy_chunk_bf16_fp8(AttnMode mode, int head_dim, int block_size);
 // Merges of their partial rows (attn_merge.cuh).
 cudaError_t launch_mod_merge(const DecodeParams& p, pa_dtype q_dtype, int head_dim, int tile_tokens,
                              cudaStream_t stream);

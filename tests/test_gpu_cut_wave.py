@@ -1,7 +1,7 @@
 """The chunk kernel's last wave, cut into parts and merged, in the forms of block-scaled caches and of
-cross attention, and with one query tile a CTA: units of one CTA each, a few more than the GPU
-holds at a time, against the definition in 64 bits (tolerances in test_gpu_block_scale.py).  Empty contexts, contexts
-shorter than their rows and sequences without rows lie among the whole units and the cut ones.
+cross attention: units of one CTA each, a few more than there are SMs, against the definition in 64
+bits (tolerances in test_gpu_block_scale.py).  Empty contexts, contexts shorter than their rows and
+sequences without rows lie among the whole units and the cut ones.
 """
 import pytest
 import torch
@@ -20,13 +20,16 @@ FORMS = [("chunk", "block", 128, 16, torch.bfloat16), ("chunk", "block", 128, 32
 
 def build(call, kind, D, B, dtype):
     """One row tile a sequence and head.  The last three sequences' 24 units are the cut ones."""
-    at_once = torch.cuda.get_device_properties(0).multi_processor_count * (2 if kind == "half" and D == 64 else 1)
-    S = at_once // HEADS + 3
-    new = [40 - i % 5 for i in range(S)]
-    lens = [1040 + 7 * i % 260 for i in range(S)]
-    new[4] = 0
+    S = torch.cuda.get_device_properties(0).multi_processor_count // HEADS + 3
+    # (16-bit caches at head_dim 64 have CTAs of one row tile, which are not cut, but for long contexts
+    # and full tiles)
+    full = kind == "half" and D == 64
+    new = [256 if full else 40 - i % 5 for i in range(S)]
+    lens = [(2100 if full else 1040) + 7 * i % 260 for i in range(S)]
+    if not full:
+        new[4] = 0
     for s, L in ((1, 0), (2, 11), (S - 3, 0), (S - 1, 9)):
-        lens[s] = L if call == "cross" else 40 + L            # (a chunk's context holds its rows)
+        lens[s] = L if call == "cross" else max(new) + L      # (a chunk's context holds its rows)
     return R.build(81, lens, new, HEADS, HEADS, D, B, dtype, causal=call == "chunk", kind=kind)
 
 
