@@ -635,9 +635,11 @@ int pa_cross_attention_fp8(void* out, pa_dtype out_dtype, const void* q, pa_dtyp
  *   head_dim 64 or 128, block_size 16 or 32
  * Two sequences of a call must not append to the same block (copy it first), and sequences must
  * not share the block a call appends to.  On the device: n_s > L_s, n_s > max_query_len, L_s beyond the
- * table row and rows that no sequence owns set PA_DEVERR_CONTEXT_LEN (such a sequence is
- * skipped, such rows are left alone); a block id outside the pool sets PA_DEVERR_BLOCK_ID and its
- * tokens are skipped.
+ * table row and rows that no sequence owns (before query_start[0] or behind query_start[num_seqs])
+ * set PA_DEVERR_CONTEXT_LEN (such a sequence is skipped, such rows are left alone); a query_start that
+ * is not ascending sets it too, and may skip more of its sequences; a block id outside the pool
+ * sets PA_DEVERR_BLOCK_ID and its tokens are skipped.  With num_tokens, num_seqs or max_query_len 0
+ * nothing is launched.
  *
  * pa_rotary_and_append_fp8_block: the same with K turned by its positions first (in fp32, not rounded
  * to `dtype` on the way) and q_out[i] = rot(q[i]) as in pa_rotary_and_cache: q, q_out, inv_freq,
