@@ -223,6 +223,14 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas<D, B, ONE>()) appe
         s = (int)blockIdx.x / p.per_seq;
         b = (int)blockIdx.x - s * p.per_seq;
     } else {
+        // a malformed query_start may leave a sequence no unit that flags it: the first CTAs' threads look
+        // at a sequence each (there are 2 num_seqs units and more; a loop in one CTA cost every form 2 %)
+        const int look = (int)blockIdx.x * kAppendThreads + threadIdx.x;
+        if (blockIdx.y == 0 && look < p.num_seqs) {
+            const int q0 = p.query_start[look], q1 = p.query_start[look + 1];
+            if (!append_owned(p, look, q0, q1) || !append_sound(p, q0, q1, p.context_lens[look], bs))
+                atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
+        }
         // sequence i's units start at query_start[i] / B + 2 i: it touches at most n / B + 2 blocks
         int lo = 0, hi = p.num_seqs;                   // 33-way search, all lanes of each warp
         while (hi - lo > 1) {
@@ -245,23 +253,14 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas<D, B, ONE>()) appe
     const int qs0 = p.query_start[s], qs1 = p.query_start[s + 1];
     const int n = qs1 - qs0;
     const int L = p.context_lens[s];
-    const bool sound = append_sound(p, qs0, qs1, L, bs);
-    // Sequences to skip and rows that no sequence owns are flagged once: by each sequence's first CTA,
-    // or, where units are searched for (a malformed query_start may leave a sequence none), by the
-    // grid's first.
-    if (p.per_seq > 0) {
-        if (b == 0 && blockIdx.y == 0 && threadIdx.x == 0 &&
-            !(sound && append_owned(p, s, qs0, qs1)))
+    const bool first_cta = p.per_seq > 0 && b == 0 && blockIdx.y == 0 && threadIdx.x == 0;
+    if (first_cta && !append_owned(p, s, qs0, qs1))
+        atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);       // rows before the first sequence or behind the last
+    if (!append_sound(p, qs0, qs1, L, bs)) {
+        if (first_cta)
             atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
-    } else if (blockIdx.x == 0 && blockIdx.y == 0) {
-        for (int i = threadIdx.x; i < p.num_seqs; i += kAppendThreads) {
-            const int q0 = p.query_start[i], q1 = p.query_start[i + 1];
-            if (!(append_sound(p, q0, q1, p.context_lens[i], bs) && append_owned(p, i, q0, q1)))
-                atomicOr(p.err, PA_DEVERR_CONTEXT_LEN);
-        }
-    }
-    if (!sound)
         return;
+    }
     const int first = L - n;                          // position of the first new token
     const int lb = first / bs + b;                    // logical block
     if (b < 0 || lb >= (L + bs - 1) / bs || n == 0)
