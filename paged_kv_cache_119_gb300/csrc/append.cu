@@ -22,9 +22,10 @@
 // per unit into shared memory and serve the rows of q and k.
 // Bound: HBM (q in and out, k and v in, codes out) for prefills, near which the work per element
 // still shows: 32 prompts of 440 to 543 tokens, 64 + 2 x 8 heads of 128, bf16, 64 dims in pairs, 598
-// MB: 107 us (5.6 TB/s); 24 x 1150 to 1500 tokens of 2 x 16 heads of 64, f16, nothing turned, 195 MB:
-// 35 us (5.6 TB/s).  A step is three dependent loads and a launch: 4 sequences 6.2 us, 256 of 40 + 2 x 40
-// heads 10.3.
+// MB: 106 us (5.6 TB/s; blocks of 32 136, whole heads in halves 109 and 150, the scalar layout 717
+// and 1163); 24 x 1150 to 1500 tokens of 2 x 16 heads of 64, f16, nothing turned, 195 MB: 34 us (5.7
+// TB/s).  A step is three dependent loads and a launch: 4 sequences 4.3 us, 256 of 40 + 2 x 40 heads 8.7
+// (nothing turned 5.8).
 #include <algorithm>
 #include <type_traits>
 
